@@ -269,6 +269,118 @@ dsa_status_t dsa_lstsq_factor(int32_t m, int32_t p, const float* M, float lambda
 dsa_status_t dsa_lstsq_solve(int32_t m, int32_t p, int32_t batch, const float* M, const double* L, const float* S,
                              float* X, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The operators around the sliding attention in a video transformer block: cross attention to
+ * an encoder's states, rotary positions over (time, height, width), and the root-mean-square
+ * norm.  Ownership, streams, capture and errors as above; every one is deterministic (the same
+ * bits from run to run). */
+
+/* A view of a [B, heads, rows, d] tensor: the channels of a row are contiguous, the other
+ * dimensions have strides in elements, so both head-major tensors and the token-major rows of
+ * a (fused) projection are views.  A dimension of extent 1 may have any stride. */
+typedef struct {
+  void* data;
+  int64_t stride[3]; /* batch, head, row */
+} dsa_view_t;
+
+/* Cross attention: Lq query rows of each of `heads` heads attend to Lk states of another
+ * sequence (a text or image encoder's) through kv_heads heads of keys and values (kv_heads
+ * divides heads; head h reads kv head h / (heads / kv_heads)).  With len_b = kv_len[b] limited
+ * to [0, Lk] (kv_len: device int32 [B]; NULL: Lk for every entry):
+ *   O_n = sum_{m < len_b} softmax_m(scale <q_n, k_m>) v_m,  LSE_n = ln sum_{m < len_b} exp(scale <q_n, k_m>).
+ * Rows len_b and on of k and v are padding: whatever they hold (NaN and infinities included)
+ * reaches no result.  len_b = 0 gives O = 0 and LSE = -inf.  Lq = 0 and Lk = 0 are valid. */
+typedef struct {
+  int32_t B, heads, kv_heads, d; /* d = 128 */
+  int32_t Lq, Lk;
+  float scale;   /* softmax scale, > 0 */
+  int32_t dtype; /* DSA_BF16 */
+} dsa_cross_t;
+
+/* Bytes of device workspace dsa_fwd_cross (kind = DSA_WS_FWD; 0 unless few query rows meet many
+ * keys) or dsa_bwd_cross (DSA_WS_BWD) needs; 0 also if the problem is invalid. */
+size_t dsa_cross_workspace_size(const dsa_cross_t* p, int32_t kind);
+
+/* Forward: writes out (a view like q's, strides of its own) and lse (fp32 [B, heads, Lq]).
+ * Views: 16-byte aligned data, strides multiples of 8 elements and at least 128; the batch and
+ * head strides of an input may be 0 (broadcast).  workspace: 256-byte aligned.  P is rounded to
+ * bf16 before the value product (relative error 2^-9); scores, softmax statistics and sums are
+ * fp32.  With few query rows the keys are cut into parts whose fp32 partial results are joined
+ * by a second launch. */
+dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_view_t* k, const dsa_view_t* v,
+                           const int32_t* kv_len, const dsa_view_t* out, float* lse, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* Backward of L = sum(out * dout), given the forward's out and lse for the same inputs.  Writes
+ * dq [B, heads, Lq, 128], dk and dv [B, kv_heads, Lk, 128] through their views (a shared kv
+ * head's gradient is the sum over its heads; rows len_b and on of dk and dv are zero; an input
+ * broadcast by a stride of 0 gets the gradient of each of its entries, not their sum).  P and
+ * dS are rounded to bf16 before their products; everything is summed in fp32 in a fixed order. */
+dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_view_t* k, const dsa_view_t* v,
+                           const dsa_view_t* out, const float* lse, const dsa_view_t* dout, const int32_t* kv_len,
+                           const dsa_view_t* dq, const dsa_view_t* dk, const dsa_view_t* dv, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Rotary positions over the token grid's three axes.  axes[a] channels (even, their sum R at
+ * most d) belong to axis a (time, height, width): R / 2 pairs, the time axis' first.  A pair is
+ * channels (2j, 2j + 1) (interleaved = 1) or (j, j + R / 2) (interleaved = 0); channels R and on
+ * pass through.  A token at (t, h, w) turns pair j of axis a by its coordinate's angle:
+ *   (x, y) -> (x cos - y sin, x sin + y cos);   inverse = 1: by minus the angle, which is also the
+ * backward (the gradient of a rotation is its inverse's).
+ * table (device fp32, 8-byte aligned): for each axis in turn [n_a, axes[a] / 2] entries (cos, sin),
+ * n_a = T, H, W.  dsa_rope_table fills it with angle = (start[a] + i * step[a]) *
+ * theta^(-2j / axes[a]) (angles in fp64; step scales positions, start shifts them, for a clip
+ * taken in pieces); a table of any other angles serves as well.  grid, axes, start, step are host
+ * arrays of 3. */
+dsa_status_t dsa_rope_table(const int32_t* grid, const int32_t* axes, const double* start, const double* step,
+                            double theta, float* table, void* stream);
+
+typedef struct {
+  int32_t B, heads, d; /* any d */
+  int32_t T, H, W;
+  int32_t axes[3];
+  int32_t interleaved, inverse; /* 0 or 1 */
+  int32_t dtype;                /* dsa_dtype_t */
+} dsa_rope_t;
+
+/* Turns q and (unless k and k_out are NULL) k in one launch; views [B, heads, T*H*W, d] with any
+ * strides >= 0 for inputs and >= d for outputs.  An output may be its own input (the same view);
+ * other overlaps are not allowed.  fp32 arithmetic, one rounding. */
+dsa_status_t dsa_rope(const dsa_rope_t* p, const float* table, const dsa_view_t* q, const dsa_view_t* q_out,
+                      const dsa_view_t* k, const dsa_view_t* k_out, void* stream);
+
+/* Root-mean-square norm of `rows` rows of C <= 16384 channels, after the residual's addition:
+ *   h = x + residual (h = x without one),   y_c = weight_c * h_c / sqrt(mean_c h_c^2 + eps).
+ * x and residual have row strides x_ld, r_ld (elements, >= C), weight is [C] (NULL: ones), y and
+ * sum (= h, given exactly when a residual is) are [rows, C] contiguous, all of type dtype.  fp32
+ * arithmetic; y is taken from the unrounded h; sum may be the residual's or x's own buffer (with
+ * its row stride C). */
+typedef struct {
+  int64_t rows;
+  int32_t C;
+  float eps;     /* >= 0 */
+  int32_t dtype; /* dsa_dtype_t */
+} dsa_norm_t;
+dsa_status_t dsa_rmsnorm(const dsa_norm_t* p, const void* x, int64_t x_ld, const void* residual, int64_t r_ld,
+                         const void* weight, void* y, void* sum, void* stream);
+
+/* The same with y in 8 bits: y8 [rows, C] e4m3 and scales fp32 [rows, ceil(C / 128)], one for
+ * every 128 channels of a row: s = max |y_c| / 448 (1 if every y_c is 0; at least 2^-126) and
+ * y8_c = rn(y_c / s), so that s * y8_c stands for y_c. */
+dsa_status_t dsa_rmsnorm_fp8(const dsa_norm_t* p, const void* x, int64_t x_ld, const void* residual, int64_t r_ld,
+                             const void* weight, void* y8, float* scales, void* sum, void* stream);
+
+/* Backward of L = sum(y * dy) + sum(h * dh) with respect to h, which is the gradient of x and of
+ * the residual, and to the weight: with rho = 1 / sqrt(mean h^2 + eps) and g = weight * dy,
+ *   dx = rho g - rho^3 h mean_c(g_c h_c) + dh,   dweight_c = sum over rows of rho dy_c h_c.
+ * h is the forward's sum (or x); dh (NULL: none) is the gradient that reaches h beside the norm.
+ * dx is [rows, C] contiguous, dweight [C] (NULL: not wanted), of type dtype.  workspace (only for
+ * dweight): at least dsa_rmsnorm_bwd_workspace_size(p) bytes, 256-byte aligned. */
+size_t dsa_rmsnorm_bwd_workspace_size(const dsa_norm_t* p);
+dsa_status_t dsa_rmsnorm_bwd(const dsa_norm_t* p, const void* h, int64_t h_ld, const void* weight, const void* dy,
+                             int64_t dy_ld, const void* dh, int64_t dh_ld, void* dx, void* dweight, void* workspace,
+                             size_t ws_bytes, void* stream);
+
 /* Waits for `stream`, then reads and clears the device status word of the current device.
  * Returns DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_DEVICE (or DSA_ERR_CUDA if the read failed);
  * site / block (either may be NULL) receive where the first failure was raised. */

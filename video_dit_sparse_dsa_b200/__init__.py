@@ -14,6 +14,13 @@ each query token attends with softmax(scale q K^T) V to exactly the tokens of th
 Tensors: q, k, v, out, dout, dq, dk, dv are ``[B, heads, T, H, W, d]`` contiguous CUDA
 tensors (bf16 with d = 128, or fp32 with d in {64, 128} for the forward); lse is
 ``[B, heads, T, H, W]`` fp32; tile offsets are int32 ``[nTiles, 3]`` in tile units.
+
+Around it in a transformer block: ``forward_cross`` / ``backward_cross`` (cross attention to an
+encoder's states), ``rope_table`` / ``rope`` (rotary positions over the token grid) and
+``rms_norm`` / ``rms_norm_fp8`` / ``rms_norm_backward`` (root-mean-square norm with the
+residual's addition).  These take strided tensors (views of a projection), run on the device
+of their first argument whichever device is current, and on ``stream`` (default: that device's
+current stream).
 """
 from __future__ import annotations
 
@@ -42,7 +49,9 @@ EXPORTS = ("dsa_version", "dsa_status_string", "dsa_plan_shape", "dsa_workspace_
            "dsa_fwd_host_bytes", "dsa_fwd_host", "dsa_bwd", "dsa_device_status", "dsa_fwd_noalloc",
            "dsa_list_workspace_size", "dsa_fwd_list", "dsa_bwd_list", "dsa_plan_heads", "dsa_block_map",
            "dsa_lstsq_workspace_size", "dsa_lstsq_factor", "dsa_lstsq_solve", "dsa_prefix_workspace_size",
-           "dsa_fwd_prefix", "dsa_bwd_prefix_workspace_size", "dsa_bwd_prefix", "dsa_selftest_wait")
+           "dsa_fwd_prefix", "dsa_bwd_prefix_workspace_size", "dsa_bwd_prefix", "dsa_selftest_wait",
+           "dsa_cross_workspace_size", "dsa_fwd_cross", "dsa_bwd_cross", "dsa_rope_table", "dsa_rope", "dsa_rmsnorm",
+           "dsa_rmsnorm_fp8", "dsa_rmsnorm_bwd_workspace_size", "dsa_rmsnorm_bwd")
 
 
 class DsaError(RuntimeError):
@@ -55,6 +64,26 @@ class Problem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("T", ctypes.c_int32),
                 ("H", ctypes.c_int32), ("W", ctypes.c_int32), ("tile", ctypes.c_int32 * 3),
                 ("window", ctypes.c_int32 * 3), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class View(ctypes.Structure):
+    """dsa_view_t: a [B, heads, rows, d] tensor through its strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
+
+
+class Cross(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("Lq", ctypes.c_int32), ("Lk", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("heads", ctypes.c_int32), ("d", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("W", ctypes.c_int32), ("axes", ctypes.c_int32 * 3),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -104,10 +133,24 @@ def load_library(path: Optional[str] = None):
     lib.dsa_bwd_prefix_workspace_size.argtypes = [pp, i32]
     lib.dsa_bwd_prefix.argtypes = [pp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                    vp, vp, sz, vp]
+    cp, wp, rp, np_, i64 = ctypes.POINTER(Cross), ctypes.POINTER(View), ctypes.POINTER(Rope), ctypes.POINTER(Norm), ctypes.c_int64
+    i32x3, f64x3 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double)
+    lib.dsa_cross_workspace_size.restype = sz
+    lib.dsa_cross_workspace_size.argtypes = [cp, i32]
+    lib.dsa_fwd_cross.argtypes = [cp, wp, wp, wp, vp, wp, vp, vp, sz, vp]
+    lib.dsa_bwd_cross.argtypes = [cp, wp, wp, wp, wp, vp, wp, vp, wp, wp, wp, vp, sz, vp]
+    lib.dsa_rope_table.argtypes = [i32x3, i32x3, f64x3, f64x3, ctypes.c_double, vp, vp]
+    lib.dsa_rope.argtypes = [rp, vp, wp, wp, wp, wp, vp]
+    lib.dsa_rmsnorm.argtypes = [np_, vp, i64, vp, i64, vp, vp, vp, vp]
+    lib.dsa_rmsnorm_fp8.argtypes = [np_, vp, i64, vp, i64, vp, vp, vp, vp, vp]
+    lib.dsa_rmsnorm_bwd_workspace_size.restype = sz
+    lib.dsa_rmsnorm_bwd_workspace_size.argtypes = [np_]
+    lib.dsa_rmsnorm_bwd.argtypes = [np_, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp]
     for name in ("dsa_plan_shape", "dsa_plan", "dsa_fwd", "dsa_fwd_host", "dsa_bwd", "dsa_device_status",
                  "dsa_fwd_noalloc", "dsa_fwd_list", "dsa_bwd_list", "dsa_plan_heads", "dsa_block_map",
                  "dsa_lstsq_factor", "dsa_lstsq_solve", "dsa_fwd_prefix", "dsa_bwd_prefix",
-                 "dsa_selftest_wait"):
+                 "dsa_selftest_wait", "dsa_fwd_cross", "dsa_bwd_cross", "dsa_rope_table", "dsa_rope", "dsa_rmsnorm",
+                 "dsa_rmsnorm_fp8", "dsa_rmsnorm_bwd"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -498,6 +541,353 @@ def plan_heads(problem: Problem, offsets: torch.Tensor, stream=None):
     _check(lib.dsa_plan_heads(ctypes.byref(problem), _ptr(offsets), _ptr(row_ptr), _ptr(kv_list),
                               ctypes.c_void_p(_stream(stream))), "dsa_plan_heads")
     return row_ptr, kv_list
+
+
+# ---------------------------------------------------------------- around the sliding attention
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return DSA_BF16
+    if t.dtype == torch.float32:
+        return DSA_F32
+    raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+
+
+class _On:
+    """Runs a call on a tensor's device and on ``stream`` (default: that device's current
+    stream).  Scratch taken here is tied to that stream, so its memory is not reused while the
+    call's kernels run."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.device = t.device
+        self.guard = torch.cuda.device(t.device)
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard.__enter__()
+        self.handle = _stream(self.stream)
+        self.ptr = ctypes.c_void_p(self.handle)
+        return self
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+    def scratch(self, n_bytes: int):
+        if n_bytes == 0:
+            return None
+        t = torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
+        self.keep(t)
+        return t
+
+    def keep(self, *tensors):
+        """Tensors allocated by the call on the current stream, used on ``stream``."""
+        if self.handle != torch.cuda.current_stream(self.device).cuda_stream:
+            s = torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else \
+                torch.cuda.default_stream(self.device)
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
+
+
+def _like(t: torch.Tensor, name: str, ref: torch.Tensor, shape=None, dtype=None):
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+
+
+def _ws(ws: Optional[torch.Tensor], n_bytes: int, on: _On, ref: torch.Tensor):
+    if ws is None:
+        ws = on.scratch(n_bytes)
+    elif ws.device != ref.device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {ref.device}")
+    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def _rows_view(t: torch.Tensor, name: str) -> View:
+    """A [B, heads, rows, d] tensor as dsa_view_t."""
+    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    v = View()
+    v.data = t.data_ptr()
+    for a in range(3):
+        v.stride[a] = t.stride(a)
+    return v
+
+
+def _cross(q, k, v, kv_len, scale) -> Cross:
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, heads, Lq, d], k and v [B, kv_heads, Lk, d]")
+    B, heads, Lq, d = q.shape
+    kv_heads, Lk = k.shape[1], k.shape[2]
+    _like(k, "k", q, (B, kv_heads, Lk, d), q.dtype)
+    _like(v, "v", q, k.shape, q.dtype)
+    if kv_len is not None:
+        _like(kv_len, "kv_len", q, (B,), torch.int32)
+        if not kv_len.is_contiguous():
+            raise ValueError("kv_len must be contiguous")
+    p = Cross()
+    p.B, p.heads, p.kv_heads, p.d, p.Lq, p.Lk = B, heads, kv_heads, d, Lq, Lk
+    p.scale = float(1.0 / math.sqrt(d)) if scale is None else float(scale)
+    p.dtype = _dtype_of(q, "q")
+    return p
+
+
+def _out_like(t: torch.Tensor, name: str, ref: torch.Tensor) -> torch.Tensor:
+    """`t`, or a new tensor of ref's shape and dimension order."""
+    if t is None:
+        return torch.empty_like(ref)
+    _like(t, name, ref, ref.shape, ref.dtype)
+    return t
+
+
+def cross_workspace_size(problem: Cross, backward: bool = False) -> int:
+    return int(load_library().dsa_cross_workspace_size(ctypes.byref(problem), DSA_WS_BWD if backward else DSA_WS_FWD))
+
+
+def forward_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Optional[torch.Tensor] = None,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Cross attention to an encoder's states.  q: [B, heads, Lq, 128] bf16; k, v: [B, kv_heads,
+    Lk, 128] (kv_heads divides heads), strided views with contiguous channels; kv_len: int32
+    [B] on the device, the valid states of each batch entry (the rest is padding that reaches no
+    result; 0 gives out = 0 and lse = -inf).  Returns (out, lse), out in q's dimension order."""
+    lib = load_library()
+    p = _cross(q, k, v, kv_len, scale)
+    with _On(q, stream) as on:
+        new_out, new_lse = out is None, lse is None
+        out = _out_like(out, "out", q)
+        if new_lse:
+            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        _like(lse, "lse", q, q.shape[:3], torch.float32)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+        ws, n_ws = _ws(ws, cross_workspace_size(p), on, q)
+        on.keep(out if new_out else None, lse if new_lse else None)
+        views = [_rows_view(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
+        r = [ctypes.byref(x) for x in views]
+        _check(lib.dsa_fwd_cross(ctypes.byref(p), r[0], r[1], r[2], _ptr(kv_len), r[3], _ptr(lse), _ptr(ws), n_ws,
+                                 on.ptr), "dsa_fwd_cross")
+    return out, lse
+
+
+def backward_cross(q, k, v, out, lse, dout, kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                   dq=None, dk=None, dv=None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Backward of forward_cross (gradients of sum(out * dout)).  Returns (dq, dk, dv), in the
+    dimension orders of q, k and v; a shared kv head's gradient is summed over its heads, rows
+    past kv_len are zero."""
+    lib = load_library()
+    p = _cross(q, k, v, kv_len, scale)
+    for t, name in ((out, "out"), (dout, "dout")):
+        _like(t, name, q, q.shape, q.dtype)
+    _like(lse, "lse", q, q.shape[:3], torch.float32)
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    with _On(q, stream) as on:
+        fresh = [g is None for g in (dq, dk, dv)]
+        dq, dk, dv = _out_like(dq, "dq", q), _out_like(dk, "dk", k), _out_like(dv, "dv", v)
+        ws, n_ws = _ws(ws, cross_workspace_size(p, backward=True), on, q)
+        on.keep(*(g for g, f in zip((dq, dk, dv), fresh) if f))
+        names = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
+        views = [_rows_view(t, n) for t, n in zip((q, k, v, out, dout, dq, dk, dv), names)]
+        r = [ctypes.byref(x) for x in views]
+        _check(lib.dsa_bwd_cross(ctypes.byref(p), r[0], r[1], r[2], r[3], _ptr(lse), r[4], _ptr(kv_len), r[5], r[6],
+                                 r[7], _ptr(ws), n_ws, on.ptr), "dsa_bwd_cross")
+    return dq, dk, dv
+
+
+def _axes(axes: Sequence[int]):
+    if len(axes) != 3:
+        raise ValueError("axes must be the channels of (time, height, width)")
+    return [int(a) for a in axes]
+
+
+def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0, start=(0, 0, 0), step=(1, 1, 1),
+               device="cuda", stream=None) -> torch.Tensor:
+    """(cos, sin) of every coordinate and channel pair of each axis of a (T, H, W) token grid,
+    fp32 [T axes[0]/2 + H axes[1]/2 + W axes[2]/2, 2]: the angle of coordinate i and pair j of
+    axis a is (start[a] + i step[a]) theta^(-2j / axes[a]).  Kept by the caller for rope()."""
+    lib = load_library()
+    axes = _axes(axes)
+    if len(grid) != 3 or len(start) != 3 or len(step) != 3:
+        raise ValueError("grid, start and step must have three entries")
+    n = sum(int(g) * (a // 2) for g, a in zip(grid, axes))
+    table = torch.empty((max(n, 0), 2), dtype=torch.float32, device=device)
+    with _On(table, stream) as on:
+        on.keep(table)
+        i3, d3 = ctypes.c_int32 * 3, ctypes.c_double * 3
+        _check(lib.dsa_rope_table(i3(*(int(g) for g in grid)), i3(*axes), d3(*(float(x) for x in start)),
+                                  d3(*(float(x) for x in step)), float(theta), _ptr(table), on.ptr), "dsa_rope_table")
+    return table
+
+
+def _grid_view(t: torch.Tensor, name: str) -> View:
+    """A [B, heads, T, H, W, d] tensor whose (T, H, W) are one token dimension."""
+    B, h, T, H, W, d = t.shape
+    if t.numel() > 0 and d > 1 and t.stride(5) != 1:
+        raise ValueError(f"{name}: the channels must be contiguous")
+    token = next((t.stride(a) // n for a, n in ((4, 1), (3, W), (2, H * W)) if t.shape[a] > 1), 0)
+    for a, n in ((4, 1), (3, W), (2, H * W)):
+        if t.shape[a] > 1 and t.stride(a) != n * token:
+            raise ValueError(f"{name}: (T, H, W) must be one dimension of tokens in raster order")
+    v = View()
+    v.data = t.data_ptr()
+    v.stride[0], v.stride[1], v.stride[2] = t.stride(0), t.stride(1), token
+    return v
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: Sequence[int],
+         interleaved: bool = True, inverse: bool = False, q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions over the token grid, q and k in one launch (k may be None).  q, k:
+    [B, heads, T, H, W, d] bf16 or fp32, contiguous channels, tokens in raster order, any other
+    strides (a projection's token-major rows as a view).  axes: channels of (time, height, width);
+    interleaved: pairs (2j, 2j + 1), else (j, j + R / 2).  inverse=True turns back, which is also
+    the backward.  Returns (q_out, k_out): contiguous unless given (an output may be its input)."""
+    lib = load_library()
+    if q.dim() != 6:
+        raise ValueError("q must be [B, heads, T, H, W, d]")
+    axes = _axes(axes)
+    p = Rope()
+    p.B, p.heads, p.T, p.H, p.W, p.d = q.shape
+    for a in range(3):
+        p.axes[a] = axes[a]
+    p.interleaved, p.inverse = int(bool(interleaved)), int(bool(inverse))
+    p.dtype = _dtype_of(q, "q")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    n = p.T * (axes[0] // 2) + p.H * (axes[1] // 2) + p.W * (axes[2] // 2)
+    _like(table, "table", q, (n, 2), torch.float32)
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    with _On(q, stream) as on:
+        refs, outs = [], []
+        for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+            if x is None:
+                refs += [None, None]
+                outs.append(None)
+                continue
+            _like(x, name, q, q.shape, q.dtype)
+            if y is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+                on.keep(y)
+            _like(y, name + "_out", q, q.shape, q.dtype)
+            refs += [ctypes.byref(_grid_view(x, name)), ctypes.byref(_grid_view(y, name + "_out"))]
+            outs.append(y)
+        _check(lib.dsa_rope(ctypes.byref(p), _ptr(table), *refs, on.ptr), "dsa_rope")
+    return outs[0], outs[1]
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, C, row stride) of a [..., C] tensor whose leading dimensions are one of rows."""
+    if t.dim() == 0 or (t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1):
+        raise ValueError(f"{name}: the channels must be contiguous")
+    C, rows, ld = t.shape[-1], 1, 0
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n != 1 and t.numel() > 0:
+            if rows > 1 and s != rows * ld:
+                raise ValueError(f"{name}: the leading dimensions must be one dimension of rows")
+            if rows == 1:
+                ld = s
+        rows *= n
+    return rows, C, ld if rows > 1 else C
+
+
+def _norm(x: torch.Tensor, weight, eps: float):
+    rows, C, ld = _rows(x, "x")
+    p = Norm()
+    p.rows, p.C, p.eps, p.dtype = rows, C, float(eps), _dtype_of(x, "x")
+    if weight is not None:
+        _like(weight, "weight", x, (C,), x.dtype)
+        if not weight.is_contiguous():
+            raise ValueError("weight must be contiguous")
+    return p, ld
+
+
+def _contiguous_out(t, name: str, ref: torch.Tensor, on: _On, dtype=None):
+    if t is None:
+        t = torch.empty(ref.shape, dtype=dtype or ref.dtype, device=ref.device)
+        on.keep(t)
+    _like(t, name, ref, ref.shape, dtype or ref.dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+             residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             sum_out: Optional[torch.Tensor] = None, stream=None):
+    """Root-mean-square norm over the last dimension (C <= 16384), after the residual's addition:
+    h = x + residual, y = weight * h / sqrt(mean h^2 + eps).  x, residual: [..., C] bf16 or fp32
+    rows of any row stride; weight: [C] of the same type, or None.  Returns (y, h); h is x itself
+    without a residual.  sum_out may be the residual (updated in place)."""
+    y, h, _ = _rms_norm(x, weight, eps, residual, out, None, sum_out, None, stream)
+    return y, h
+
+
+def rms_norm_fp8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, sum_out: Optional[torch.Tensor] = None, stream=None):
+    """rms_norm with y as e4m3 and an fp32 scale for every 128 channels of a row.  Returns (y8,
+    scales, h): y8 [..., C] float8_e4m3fn, scales [..., ceil(C / 128)], y = y8 * scale."""
+    y, h, s = _rms_norm(x, weight, eps, residual, out, scales, sum_out, torch.float8_e4m3fn, stream)
+    return y, s, h
+
+
+def _rms_norm(x, weight, eps, residual, out, scales, sum_out, dtype8, stream):
+    lib = load_library()
+    p, x_ld = _norm(x, weight, eps)
+    r_ld = 0
+    if residual is not None:
+        _like(residual, "residual", x, x.shape, x.dtype)
+        r_ld = _rows(residual, "residual")[2]
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual")
+    with _On(x, stream) as on:
+        y = _contiguous_out(out, "out", x, on, dtype8)
+        h = _contiguous_out(sum_out, "sum_out", x, on) if residual is not None else None
+        args = [ctypes.byref(p), _ptr(x), x_ld, _ptr(residual), r_ld, _ptr(weight), _ptr(y)]
+        if dtype8 is None:
+            _check(lib.dsa_rmsnorm(*args, _ptr(h), on.ptr), "dsa_rmsnorm")
+        else:
+            shape = x.shape[:-1] + ((p.C + 127) // 128,)
+            if scales is None:
+                scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+                on.keep(scales)
+            _like(scales, "scales", x, shape, torch.float32)
+            if not scales.is_contiguous():
+                raise ValueError("scales must be contiguous")
+            _check(lib.dsa_rmsnorm_fp8(*args, _ptr(scales), _ptr(h), on.ptr), "dsa_rmsnorm_fp8")
+    return y, x if h is None else h, scales
+
+
+def rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], dy: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None, eps: float = 1e-6, dx: Optional[torch.Tensor] = None,
+                      dweight: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """Backward of rms_norm, given its h (= x without a residual), the gradient dy of y and,
+    optionally, the gradient dh that reaches h beside the norm.  Returns (dx, dweight): dx is
+    the gradient of x and of the residual; dweight is None without a weight."""
+    lib = load_library()
+    p, h_ld = _norm(h, weight, eps)
+    _like(dy, "dy", h, h.shape, h.dtype)
+    dy_ld, dh_ld = _rows(dy, "dy")[2], 0
+    if dh is not None:
+        _like(dh, "dh", h, h.shape, h.dtype)
+        dh_ld = _rows(dh, "dh")[2]
+    if weight is None and dweight is not None:
+        raise ValueError("dweight without a weight")
+    with _On(h, stream) as on:
+        dx = _contiguous_out(dx, "dx", h, on)
+        if weight is not None:
+            dweight = _contiguous_out(dweight, "dweight", weight, on)
+        size = int(lib.dsa_rmsnorm_bwd_workspace_size(ctypes.byref(p))) if weight is not None else 0
+        ws, n_ws = _ws(ws, size, on, h)
+        _check(lib.dsa_rmsnorm_bwd(ctypes.byref(p), _ptr(h), h_ld, _ptr(weight), _ptr(dy), dy_ld, _ptr(dh), dh_ld,
+                                   _ptr(dx), _ptr(dweight), _ptr(ws), n_ws, on.ptr), "dsa_rmsnorm_bwd")
+    return dx, dweight
 
 
 def device_status(stream=None):

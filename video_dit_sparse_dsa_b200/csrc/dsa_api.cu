@@ -12,13 +12,17 @@
 #include "../../include/dsa.h"
 #include "dsa_bwd_bf16.cuh"
 #include "dsa_bwd_dq.cuh"
+#include "dsa_cross_bwd.cuh"
+#include "dsa_cross_fwd.cuh"
 #include "dsa_device_status.cuh"
 #include "dsa_fwd_bf16.cuh"
 #include "dsa_fwd_f32.cuh"
 #include "dsa_fwd_pair.cuh"
 #include "dsa_lists.cuh"
 #include "dsa_lstsq.cuh"
+#include "dsa_norm.cuh"
 #include "dsa_plan.cuh"
+#include "dsa_rope.cuh"
 
 namespace {
 
@@ -1416,3 +1420,6 @@ extern "C" dsa_status_t dsa_fwd_noalloc(const dsa_problem_t* p, const void* q, c
   if (st != DSA_OK) return st;
   return launch_fwd(p, g, q, k, v, plan + starts_ints, out, lse, s);
 }
+
+// The operators around the sliding attention in a transformer block.
+#include "dsa_api_block.cuh"

@@ -1,0 +1,736 @@
+// C entry points of the operators around the sliding attention in a transformer block (declared
+// in include/dsa.h): cross attention to an encoder's states, rotary positions, and the
+// root-mean-square norm.  Included by dsa_api.cu (the library is one translation unit), whose
+// status, alignment and tensor-map helpers these use.
+#pragma once
+
+namespace {
+
+// SMs that the splits below are planned for (a B200); other counts only change the balance.
+constexpr int kPlanSms = 148;
+
+// ---------------------------------------------------------------- views
+// A [B, heads, rows, 128] view: strides in elements, each a whole number of 16-byte vectors; a
+// broadcast (stride 0) batch or head dimension is fine for an input.
+bool view_ok(const dsa_view_t* v, int64_t B, int64_t heads, int64_t rows, bool output) {
+  if (v == nullptr || v->data == nullptr || !aligned(v->data, 16)) return false;
+  const int64_t n[3] = {B, heads, rows};
+  for (int a = 0; a < 3; ++a) {
+    if (n[a] <= 1) continue;
+    const int64_t s = v->stride[a];
+    if (s < 0 || s % 8 != 0 || s >= (int64_t(1) << 39)) return false;
+    if (s == 0 ? (output || a == 2) : s < 128) return false;
+  }
+  return true;
+}
+
+// Rank-4 or rank-5 map of a view: (channel, row[, head in the group], head, batch), boxes of 64
+// channels x box_rows rows (x box_heads heads of the group), 128-byte swizzled; rows and heads
+// past the end load as zeros.  A broadcast dimension gets extent 1; m[0..2] (group, head, batch)
+// is 0 for it, the factor of its coordinate, and 1 otherwise.
+bool make_view_map(CUtensorMap* map, const dsa_view_t* v, int64_t B, int64_t heads, int64_t group, int64_t rows,
+                   int box_rows, int box_heads, int m[3]) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int rank = group > 0 ? 5 : 4;
+  const int64_t g = group > 0 ? group : 1;
+  // extents and strides in elements of row, head in the group, head (of heads / g), batch
+  int64_t n[4] = {rows, g, heads / g, B}, s[4] = {v->stride[2], v->stride[1], v->stride[1] * g, v->stride[0]};
+  for (int a = 0; a < 4; ++a) {
+    if (n[a] <= 1 || s[a] == 0) {  // one entry: its stride is never taken
+      if (a > 0) m[a - 1] = n[a] <= 1 ? 1 : 0;
+      n[a] = 1;
+      s[a] = 128;
+    } else if (a > 0) {
+      m[a - 1] = 1;
+    }
+  }
+  cuuint64_t dims[5] = {128}, strides[4];
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), 1, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  int r = 1;
+  for (int a = 0; a < 4; ++a) {
+    if (a == 1) {
+      if (rank == 4) continue;
+      box[r] = static_cast<cuuint32_t>(box_heads);
+    }
+    dims[r] = static_cast<cuuint64_t>(n[a]);
+    strides[r - 1] = static_cast<cuuint64_t>(s[a]) * 2;
+    ++r;
+  }
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, v->data, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------- cross attention
+struct CrossPlan {
+  int group, pk, tiles;   // heads per kv head; heads packed into a 128-row unit; units per kv head
+  int64_t units;          // B * kv_heads * tiles
+  int chunks;             // 128-key chunks of Lk
+  int64_t rows;           // B * heads * Lq
+  int split_q;            // parts of the keys (forward, and dQ)
+  int split_kv;           // parts of the query chunks (dK, dV)
+  int Lp;                 // Lq rounded up to 64
+};
+
+dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
+  if (p == nullptr) return DSA_ERR_INVALID_ARG;
+  if (p->B <= 0 || p->heads <= 0 || p->kv_heads <= 0 || p->heads % p->kv_heads != 0 || p->Lq < 0 || p->Lk < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return DSA_ERR_INVALID_ARG;
+  if (p->dtype != DSA_F32 && p->dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+  if (p->dtype != DSA_BF16 || p->d != 128) return DSA_ERR_UNSUPPORTED;
+  c->group = p->heads / p->kv_heads;
+  c->pk = c->group > 1 && p->Lq > 0 && p->Lq <= 64 ? (c->group < 128 / p->Lq ? c->group : 128 / p->Lq) : 1;
+  const int64_t tiles = c->pk > 1 ? (c->group + c->pk - 1) / c->pk
+                                  : static_cast<int64_t>(c->group) * ((static_cast<int64_t>(p->Lq) + 127) / 128);
+  const int64_t slices = static_cast<int64_t>(p->B) * p->kv_heads;
+  c->rows = static_cast<int64_t>(p->B) * p->heads * p->Lq;
+  // unit and row indices are 32 bits in the kernels
+  if (p->Lq > INT32_MAX - 128 || p->Lk > INT32_MAX - 128 || tiles > INT32_MAX || slices > INT32_MAX ||
+      slices * tiles > INT32_MAX || c->rows > INT32_MAX - 64 * slices * c->group)
+    return DSA_ERR_UNSUPPORTED;
+  c->tiles = static_cast<int>(tiles);
+  c->units = slices * tiles;
+  c->chunks = (p->Lk + 127) / 128;
+  c->Lp = (p->Lq + 63) / 64 * 64;
+  // Too few units to fill the GPU: the keys are cut into parts of at least four chunks (two
+  // steps), for about four units per SM.
+  c->split_q = 1;
+  if (c->units > 0 && c->units < kPlanSms && c->chunks >= 8) {
+    int64_t s = 4 * kPlanSms / c->units;
+    if (s > c->chunks / 4) s = c->chunks / 4;
+    int64_t per = (c->chunks + s - 1) / s;
+    per = (per + 1) / 2 * 2;
+    c->split_q = static_cast<int>((c->chunks + per - 1) / per);
+  }
+  // dK, dV: a unit is 128 keys of one kv head over every query chunk of its group; the query
+  // chunks are cut so that the units fill whole waves of SMs (the smallest estimate of waves x
+  // (chunks of a part + 4 for the part's own start and end), parts of at least 8 chunks).
+  const int64_t kv_units = slices * (c->chunks > 0 ? c->chunks : 1);
+  const int64_t q_chunks = static_cast<int64_t>(c->group) * (c->Lp / 64);
+  if (kv_units > INT32_MAX / 64 || q_chunks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  c->split_kv = 1;
+  int64_t best = -1;
+  for (int64_t s = 1; s <= 64 && (s == 1 || s * 8 <= q_chunks); ++s) {
+    const int64_t per = (q_chunks + s - 1) / s, waves = (kv_units * s + kPlanSms - 1) / kPlanSms;
+    const int64_t cost = waves * (per + 4);
+    if (best < 0 || cost < best) {
+      best = cost;
+      c->split_kv = static_cast<int>((q_chunks + per - 1) / (per > 0 ? per : 1));
+      if (c->split_kv < 1) c->split_kv = 1;
+    }
+  }
+  return DSA_OK;
+}
+
+struct CrossWorkspace {
+  float *part_o, *part_lse;                       // forward, split_q > 1
+  float *delta, *lse_pad, *dq_part, *dk_part, *dv_part;  // backward
+  size_t bytes;
+};
+
+CrossWorkspace cross_workspace(const dsa_cross_t* p, const CrossPlan& c, int kind, void* base) {
+  CrossWorkspace w;
+  std::memset(&w, 0, sizeof(w));
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t floats) {
+    float* at = reinterpret_cast<float*>(b + off);
+    off += round_up(sizeof(float) * floats, kAlign);
+    return at;
+  };
+  const size_t kv_rows = static_cast<size_t>(p->B) * p->kv_heads * p->Lk;
+  if (kind == DSA_WS_FWD) {
+    if (c.split_q > 1) {
+      w.part_o = take(static_cast<size_t>(c.split_q) * c.rows * 128);
+      w.part_lse = take(static_cast<size_t>(c.split_q) * c.rows);
+    }
+  } else {
+    w.delta = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
+    w.lse_pad = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
+    if (c.split_q > 1) w.dq_part = take(static_cast<size_t>(c.split_q) * c.rows * 128);
+    if (c.split_kv > 1) {
+      w.dk_part = take(c.split_kv * kv_rows * 128);
+      w.dv_part = take(c.split_kv * kv_rows * 128);
+    }
+  }
+  w.bytes = off;
+  return w;
+}
+
+// Grid of a persistent kernel, one CTA per SM; checks the registers its setmaxnreg split needs.
+template <typename K>
+dsa_status_t persistent_grid(K kernel, uint32_t smem, int regs, int64_t units, unsigned* grid) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return DSA_ERR_CUDA;
+    if (fa.numRegs < regs) return DSA_ERR_UNSUPPORTED;
+  }
+  int sms = 0;
+  if (sm_count(&sms) != DSA_OK) return DSA_ERR_CUDA;
+  *grid = static_cast<unsigned>(units < sms ? units : sms);
+  return DSA_OK;
+}
+
+dsa_status_t launch_combine(const dsa::CrossCombineParams& cp, cudaStream_t s) {
+  const int64_t threads = static_cast<int64_t>(cp.B) * cp.heads * cp.L * 32;
+  if (threads == 0) return DSA_OK;
+  const dim3 grid(static_cast<unsigned>((threads + 255) / 256), static_cast<unsigned>(cp.n_out));
+  dsa::cross_combine<<<grid, 256, 0, s>>>(cp);
+  return launch_status();
+}
+
+void copy_strides(int64_t (&d)[3], const dsa_view_t* v) {
+  for (int a = 0; a < 3; ++a) d[a] = v->stride[a];
+}
+
+// ---------------------------------------------------------------- rotary positions
+bool rope_axes_ok(const int32_t* axes) {
+  for (int a = 0; a < 3; ++a)
+    if (axes[a] < 0 || axes[a] % 2 != 0) return false;
+  return static_cast<int64_t>(axes[0]) + axes[1] + axes[2] > 0;
+}
+
+// ---------------------------------------------------------------- norm
+dsa_status_t check_norm(const dsa_norm_t* p) {
+  if (p == nullptr || p->rows < 0 || p->C <= 0) return DSA_ERR_INVALID_ARG;
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return DSA_ERR_INVALID_ARG;
+  if (p->dtype != DSA_F32 && p->dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+  if (p->C > dsa::norm::kMaxC || p->rows > (int64_t(1) << 30)) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+// Row stride of a [rows, C] operand: at least C unless there is one row.
+bool ld_ok(int64_t ld, const dsa_norm_t* p) { return p->rows <= 1 || ld >= p->C; }
+
+// Whole 16-byte vectors of 8 channels: address and row stride (C is checked apart).
+bool vec_ok(const void* ptr, int64_t ld, const dsa_norm_t* p) {
+  return ptr == nullptr || (aligned(ptr, 16) && (p->rows <= 1 || ld % (p->dtype == DSA_BF16 ? 8 : 4) == 0));
+}
+
+struct NormShape {
+  int NV, W, R;  // vectors per thread, warps per row, rows per block
+};
+
+// Fewest idle lanes; among equals the widest NV up to nv_pref (fewer warps meet at the row's
+// barrier).
+NormShape norm_shape(int C, int nv_pref, int threads) {
+  const int nvec = (C + dsa::norm::kVec - 1) / dsa::norm::kVec;
+  NormShape best = {0, 0, 0};
+  int waste = INT32_MAX;
+  for (int pass = 0; pass < 2 && best.NV == 0; ++pass) {
+    for (int nv = pass == 0 ? nv_pref : dsa::norm::kMaxNV; nv >= 1; --nv) {
+      const int W = (nvec + 32 * nv - 1) / (32 * nv);
+      if (W > dsa::norm::kMaxWarps) continue;
+      const int idle = 32 * nv * W - nvec;
+      if (idle < waste) {
+        waste = idle;
+        best.NV = nv;
+        best.W = W;
+      }
+    }
+  }
+  best.R = threads / (32 * best.W) > 1 ? threads / (32 * best.W) : 1;
+  return best;
+}
+
+template <typename T, bool kFp8>
+dsa_status_t launch_norm(const dsa::NormParams& np, const NormShape& sh, bool vec, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((np.rows + sh.R - 1) / sh.R), threads = 32 * sh.W * sh.R;
+#define DSA_NORM_CASE(NV)                                                              \
+  case NV:                                                                             \
+    if (vec)                                                                           \
+      dsa::rmsnorm_kernel<T, NV, true, kFp8><<<grid, threads, 0, s>>>(np);             \
+    else                                                                               \
+      dsa::rmsnorm_kernel<T, NV, false, kFp8><<<grid, threads, 0, s>>>(np);            \
+    break;
+  switch (sh.NV) {
+    DSA_NORM_CASE(1)
+    DSA_NORM_CASE(2)
+    DSA_NORM_CASE(3)
+    DSA_NORM_CASE(4)
+  }
+#undef DSA_NORM_CASE
+  return launch_status();
+}
+
+dsa_status_t norm_fwd(const dsa_norm_t* p, const void* x, int64_t x_ld, const void* r, int64_t r_ld, const void* w,
+                      void* y, float* scales, void* h, bool fp8, void* stream) {
+  dsa_status_t st = check_norm(p);
+  if (st != DSA_OK) return st;
+  if (!ld_ok(x_ld, p) || (r != nullptr && !ld_ok(r_ld, p))) return DSA_ERR_INVALID_ARG;
+  if ((r != nullptr) != (h != nullptr)) return DSA_ERR_INVALID_ARG;
+  const size_t elem = p->dtype == DSA_BF16 ? 2 : 4;
+  if (!aligned(x, elem) || !aligned(r, elem) || !aligned(w, elem) || !aligned(h, elem) ||
+      !aligned(y, fp8 ? 1 : elem) || !aligned(scales, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (p->rows == 0) return DSA_OK;
+  if (!x || !y || (fp8 && !scales)) return DSA_ERR_INVALID_ARG;
+  dsa::NormParams np;
+  np.x = x;
+  np.r = r;
+  np.w = w;
+  np.y = y;
+  np.h = h;
+  np.scales = scales;
+  np.rows = p->rows;
+  np.x_ld = x_ld;
+  np.r_ld = r_ld;
+  np.C = p->C;
+  np.eps = p->eps;
+  const NormShape sh = norm_shape(p->C, 4, 256);
+  np.W = sh.W;
+  const bool vec = p->C % 8 == 0 && vec_ok(x, x_ld, p) && vec_ok(r, r_ld, p) && vec_ok(w, 0, p) && vec_ok(h, 0, p) &&
+                   (fp8 ? aligned(y, 8) : aligned(y, 16));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p->dtype == DSA_BF16)
+    return fp8 ? launch_norm<__nv_bfloat16, true>(np, sh, vec, s) : launch_norm<__nv_bfloat16, false>(np, sh, vec, s);
+  return fp8 ? launch_norm<float, true>(np, sh, vec, s) : launch_norm<float, false>(np, sh, vec, s);
+}
+
+// Blocks of the persistent backward: at most this many per-block partial dw.
+unsigned norm_bwd_blocks(const dsa_norm_t* p, const NormShape& sh) {
+  const int64_t groups = (p->rows + sh.R - 1) / sh.R;
+  const int threads = 32 * sh.W * sh.R, per_sm = threads > 256 ? (threads > 384 ? 1 : 2) : 3;
+  return static_cast<unsigned>(groups < per_sm * kPlanSms ? groups : per_sm * kPlanSms);
+}
+
+template <typename T, bool kDw>
+dsa_status_t launch_norm_bwd(const dsa::NormBwdParams& np, const NormShape& sh, unsigned grid, bool vec,
+                             cudaStream_t s) {
+  const unsigned threads = 32 * sh.W * sh.R;
+  const size_t smem = kDw && sh.R > 1 ? sizeof(float) * np.C : 0;
+#define DSA_NORM_CASE(NV)                                                              \
+  case NV:                                                                             \
+    if (vec)                                                                           \
+      dsa::rmsnorm_bwd_kernel<T, NV, true, kDw><<<grid, threads, smem, s>>>(np);       \
+    else                                                                               \
+      dsa::rmsnorm_bwd_kernel<T, NV, false, kDw><<<grid, threads, smem, s>>>(np);      \
+    break;
+  switch (sh.NV) {
+    DSA_NORM_CASE(1)
+    DSA_NORM_CASE(2)
+    DSA_NORM_CASE(3)
+    DSA_NORM_CASE(4)
+  }
+#undef DSA_NORM_CASE
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_cross_workspace_size(const dsa_cross_t* p, int32_t kind) {
+  CrossPlan c;
+  if (cross_plan(p, &c) != DSA_OK || (kind != DSA_WS_FWD && kind != DSA_WS_BWD)) return 0;
+  return cross_workspace(p, c, kind, nullptr).bytes;
+}
+
+dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_view_t* k, const dsa_view_t* v,
+                           const int32_t* kv_len, const dsa_view_t* out, float* lse, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  CrossPlan c;
+  dsa_status_t st = cross_plan(p, &c);
+  if (st != DSA_OK) return st;
+  if (p->Lq == 0) return DSA_OK;
+  if (!view_ok(q, p->B, p->heads, p->Lq, false) || !view_ok(out, p->B, p->heads, p->Lq, true) || lse == nullptr ||
+      !aligned(lse, 4) || !aligned(kv_len, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (p->Lk > 0 && (!view_ok(k, p->B, p->kv_heads, p->Lk, false) || !view_ok(v, p->B, p->kv_heads, p->Lk, false)))
+    return DSA_ERR_INVALID_ARG;
+  const CrossWorkspace ws = cross_workspace(p, c, DSA_WS_FWD, workspace);
+  if (ws.bytes > 0 && (workspace == nullptr || ws_bytes < ws.bytes || !aligned(workspace, kAlign)))
+    return DSA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  dsa::CrossFwdParams fp;
+  std::memset(&fp, 0, sizeof(fp));
+  fp.kv_len = kv_len;
+  fp.out = static_cast<__nv_bfloat16*>(out->data);
+  fp.ob = out->stride[0];
+  fp.oh = out->stride[1];
+  fp.ol = out->stride[2];
+  fp.lse = lse;
+  fp.part_o = ws.part_o;
+  fp.part_lse = ws.part_lse;
+  fp.B = p->B;
+  fp.heads = p->heads;
+  fp.kv_heads = p->kv_heads;
+  fp.group = c.group;
+  fp.Lq = p->Lq;
+  fp.Lk = p->Lk;
+  fp.pk = c.pk;
+  fp.tiles = c.tiles;
+  fp.n_split = p->Lk > 0 ? c.split_q : 0;
+  fp.n_units = static_cast<int>(c.units * c.split_q);
+  fp.scale_log2 = p->scale * 1.4426950408889634f;
+  if (p->Lk > 0) {
+    CUtensorMap tq, tk, tv;
+    int mq[3], mk[3], mv[3];
+    const int box_rows = c.pk > 1 ? p->Lq : 128;
+    if (!make_view_map(&tq, q, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mq) ||
+        !make_view_map(&tk, k, p->B, p->kv_heads, 0, p->Lk, 128, 1, mk) ||
+        !make_view_map(&tv, v, p->B, p->kv_heads, 0, p->Lk, 128, 1, mv))
+      return DSA_ERR_CUDA;
+    fp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;
+    fp.qg = mq[0];
+    fp.qk = mq[1];
+    fp.qb = mq[2];
+    fp.kh = mk[1];
+    fp.kb = mk[2];
+    fp.vh = mv[1];
+    fp.vb = mv[2];
+    unsigned grid = 0;
+    st = persistent_grid(dsa::cross_fwd_kernel, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, fp.n_units, &grid);
+    if (st != DSA_OK) return st;
+    dsa::cross_fwd_kernel<<<grid, dsa::crossf::kThreads, dsa::crossf::kSmemBytes, s>>>(tq, tk, tv, fp);
+    st = launch_status();
+    if (st != DSA_OK || c.split_q == 1) return st;
+  }
+  dsa::cross_merge_kernel<<<static_cast<unsigned>(c.rows), 256, 0, s>>>(fp);  // without keys: O = 0, LSE = -inf
+  return launch_status();
+}
+
+dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_view_t* k, const dsa_view_t* v,
+                           const dsa_view_t* out, const float* lse, const dsa_view_t* dout, const int32_t* kv_len,
+                           const dsa_view_t* dq, const dsa_view_t* dk, const dsa_view_t* dv, void* workspace,
+                           size_t ws_bytes, void* stream) {
+  CrossPlan c;
+  dsa_status_t st = cross_plan(p, &c);
+  if (st != DSA_OK) return st;
+  if (p->Lq > 0 && (!view_ok(q, p->B, p->heads, p->Lq, false) || !view_ok(out, p->B, p->heads, p->Lq, false) ||
+                    !view_ok(dout, p->B, p->heads, p->Lq, false) || !view_ok(dq, p->B, p->heads, p->Lq, true) ||
+                    lse == nullptr))
+    return DSA_ERR_INVALID_ARG;
+  if (p->Lk > 0 && (!view_ok(k, p->B, p->kv_heads, p->Lk, false) || !view_ok(v, p->B, p->kv_heads, p->Lk, false) ||
+                    !view_ok(dk, p->B, p->kv_heads, p->Lk, true) || !view_ok(dv, p->B, p->kv_heads, p->Lk, true)))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(kv_len, 4)) return DSA_ERR_INVALID_ARG;
+  const CrossWorkspace ws = cross_workspace(p, c, DSA_WS_BWD, workspace);
+  if (ws.bytes > 0 && (workspace == nullptr || ws_bytes < ws.bytes || !aligned(workspace, kAlign)))
+    return DSA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the sums of the parts; with no queries or no keys they write the zero gradients
+  dsa::CrossCombineParams ckv, cq;
+  std::memset(&ckv, 0, sizeof(ckv));
+  std::memset(&cq, 0, sizeof(cq));
+  ckv.B = cq.B = p->B;
+  ckv.heads = p->kv_heads;
+  ckv.L = p->Lk;
+  ckv.len = kv_len;
+  ckv.part_stride = static_cast<int64_t>(p->B) * p->kv_heads * p->Lk * 128;
+  ckv.n_out = 2;
+  ckv.part[0] = ws.dk_part;
+  ckv.part[1] = ws.dv_part;
+  ckv.scale[0] = p->scale;
+  ckv.scale[1] = 1.f;
+  cq.heads = p->heads;
+  cq.L = p->Lq;
+  cq.part_stride = c.rows * 128;
+  cq.n_out = 1;
+  cq.part[0] = ws.dq_part;
+  cq.scale[0] = 1.f;
+  if (p->Lk > 0) {
+    ckv.out[0] = static_cast<__nv_bfloat16*>(dk->data);
+    ckv.out[1] = static_cast<__nv_bfloat16*>(dv->data);
+    copy_strides(ckv.s[0], dk);
+    copy_strides(ckv.s[1], dv);
+  }
+  if (p->Lq > 0) {
+    cq.out[0] = static_cast<__nv_bfloat16*>(dq->data);
+    copy_strides(cq.s[0], dq);
+  }
+  if (p->Lq == 0) return launch_combine(ckv, s);
+  if (p->Lk == 0) return launch_combine(cq, s);
+
+  dsa::CrossPrepParams pp;
+  pp.o = static_cast<const __nv_bfloat16*>(out->data);
+  pp.dout = static_cast<const __nv_bfloat16*>(dout->data);
+  copy_strides(pp.o_s, out);
+  copy_strides(pp.do_s, dout);
+  pp.lse = lse;
+  pp.delta_pad = ws.delta;
+  pp.lse_pad = ws.lse_pad;
+  pp.B = p->B;
+  pp.heads = p->heads;
+  pp.Lq = p->Lq;
+  pp.Lp = c.Lp;
+  const int64_t BH = static_cast<int64_t>(p->B) * p->heads;
+  dsa::cross_preprocess<<<static_cast<unsigned>((BH * c.Lp * 16 + 255) / 256), 256, 0, s>>>(pp);
+  st = launch_status();
+  if (st != DSA_OK) return st;
+
+  CUtensorMap tq, tdo, tk, tv, tlse, tdel;
+  int mq[3], mdo[3], mk[3], mv[3];
+  if (!make_view_map(&tq, q, p->B, p->heads, c.group, p->Lq, 64, 1, mq) ||
+      !make_view_map(&tdo, dout, p->B, p->heads, c.group, p->Lq, 64, 1, mdo) ||
+      !make_view_map(&tk, k, p->B, p->kv_heads, 0, p->Lk, 128, 1, mk) ||
+      !make_view_map(&tv, v, p->B, p->kv_heads, 0, p->Lk, 128, 1, mv) || !make_vec_map(&tlse, ws.lse_pad, BH, c.Lp) ||
+      !make_vec_map(&tdel, ws.delta, BH, c.Lp))
+    return DSA_ERR_CUDA;
+  {
+    dsa::BwdBf16Params bp;
+    std::memset(&bp, 0, sizeof(bp));
+    bp.dk = static_cast<__nv_bfloat16*>(dk->data);
+    bp.dv = static_cast<__nv_bfloat16*>(dv->data);
+    copy_strides(bp.dk_s, dk);
+    copy_strides(bp.dv_s, dv);
+    bp.scale = p->scale;
+    bp.scale_log2 = p->scale * 1.4426950408889634f;
+    bp.Lk = p->Lk;
+    bp.Nq = p->Lq;
+    bp.n_split = c.split_kv;
+    bp.dk_part = ws.dk_part;
+    bp.dv_part = ws.dv_part;
+    bp.part_stride = ckv.part_stride;
+    bp.kv_len = kv_len;
+    bp.kv_heads = p->kv_heads;
+    bp.group = c.group;
+    bp.qg = mq[0];
+    bp.qk = mq[1];
+    bp.qb = mq[2];
+    bp.dg = mdo[0];
+    bp.dkv = mdo[1];
+    bp.db = mdo[2];
+    bp.kh = mk[1];
+    bp.kb = mk[2];
+    bp.vh = mv[1];
+    bp.vb = mv[2];
+    bp.n_units = static_cast<int>(static_cast<int64_t>(p->B) * p->kv_heads * c.chunks * c.split_kv);
+    bp.G1 = bp.G2 = bp.tt = bp.th = bp.tw = bp.T = bp.H = bp.W = bp.KU = bp.QS = bp.n_tiles = 1;
+    auto kernel = dsa::bwd_bf16_kernel<true, false, true>;
+    unsigned grid = 0;
+    st = persistent_grid(kernel, dsa::bwd::kSmemBytes, 0, bp.n_units, &grid);
+    if (st != DSA_OK) return st;
+    kernel<<<grid, dsa::bwd::kThreads, dsa::bwd::kSmemBytes, s>>>(tq, tk, tv, tdo, tlse, tdel, tq, tdo, tlse, tdel, bp);
+    st = launch_status();
+    if (st != DSA_OK) return st;
+    if (c.split_kv > 1) {
+      ckv.n_part = c.split_kv;
+      st = launch_combine(ckv, s);
+      if (st != DSA_OK) return st;
+    }
+  }
+  dsa::BwdDqParams dp;
+  std::memset(&dp, 0, sizeof(dp));
+  dp.q = static_cast<const __nv_bfloat16*>(q->data);
+  dp.dout = static_cast<const __nv_bfloat16*>(dout->data);
+  dp.dq = static_cast<__nv_bfloat16*>(dq->data);
+  copy_strides(dp.q_s, q);
+  copy_strides(dp.do_s, dout);
+  copy_strides(dp.dq_s, dq);
+  dp.lse = ws.lse_pad;
+  dp.delta = ws.delta;
+  dp.ld_rows = c.Lp;
+  dp.Lq = p->Lq;
+  dp.Lk = p->Lk;
+  dp.n_split = c.split_q;
+  dp.dq_part = ws.dq_part;
+  dp.part_stride = c.rows * 128;
+  dp.n_units = static_cast<int>(c.units * c.split_q);
+  dp.scale = p->scale;
+  dp.scale_log2 = p->scale * 1.4426950408889634f;
+  dp.kv_len = kv_len;
+  dp.kv_heads = p->kv_heads;
+  dp.group = c.group;
+  dp.tiles = c.tiles;
+  dp.pk = c.pk;
+  dp.kh = mk[1];
+  dp.kb = mk[2];
+  dp.vh = mv[1];
+  dp.vb = mv[2];
+  dp.tt = dp.th = dp.tw = dp.T = dp.H = dp.W = dp.S = dp.KS = 1;
+  auto kernel = dsa::bwd_dq_kernel<true, false, true>;
+  unsigned grid = 0;
+  st = persistent_grid(kernel, dsa::bdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
+  if (st != DSA_OK) return st;
+  kernel<<<grid, dsa::bdq::kThreads, dsa::bdq::kSmemBytes, s>>>(tk, tv, tk, tv, dp);
+  st = launch_status();
+  if (st != DSA_OK || c.split_q == 1) return st;
+  cq.n_part = c.split_q;
+  return launch_combine(cq, s);
+}
+
+dsa_status_t dsa_rope_table(const int32_t* grid, const int32_t* axes, const double* start, const double* step,
+                            double theta, float* table, void* stream) {
+  if (!grid || !axes || !start || !step || !table || !aligned(table, 8)) return DSA_ERR_INVALID_ARG;
+  if (!rope_axes_ok(axes) || !(theta > 0.0) || !std::isfinite(theta)) return DSA_ERR_INVALID_ARG;
+  dsa::RopeTableParams rp;
+  int64_t n = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (grid[a] <= 0 || !std::isfinite(start[a]) || !std::isfinite(step[a])) return DSA_ERR_INVALID_ARG;
+    rp.n[a] = grid[a];
+    rp.pairs[a] = axes[a] / 2;
+    rp.start[a] = start[a];
+    rp.step[a] = step[a];
+    n += static_cast<int64_t>(rp.n[a]) * rp.pairs[a];
+  }
+  if (n > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  rp.log_theta = std::log(theta);
+  rp.table = reinterpret_cast<float2*>(table);
+  dsa::rope_table_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(rp);
+  return launch_status();
+}
+
+dsa_status_t dsa_rope(const dsa_rope_t* p, const float* table, const dsa_view_t* q, const dsa_view_t* q_out,
+                      const dsa_view_t* k, const dsa_view_t* k_out, void* stream) {
+  if (p == nullptr || p->B <= 0 || p->heads <= 0 || p->d <= 0 || p->T <= 0 || p->H <= 0 || p->W <= 0)
+    return DSA_ERR_INVALID_ARG;
+  if (p->dtype != DSA_F32 && p->dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+  if ((p->interleaved & ~1) != 0 || (p->inverse & ~1) != 0) return DSA_ERR_INVALID_ARG;
+  if (!rope_axes_ok(p->axes)) return DSA_ERR_INVALID_ARG;
+  const int64_t R = static_cast<int64_t>(p->axes[0]) + p->axes[1] + p->axes[2];
+  if (R > p->d) return DSA_ERR_INVALID_ARG;
+  if (!table || !aligned(table, 8) || !q || !q_out || (k == nullptr) != (k_out == nullptr)) return DSA_ERR_INVALID_ARG;
+  const int64_t N = static_cast<int64_t>(p->T) * p->H * p->W;
+  const int64_t entries = static_cast<int64_t>(p->T) * (p->axes[0] / 2) + static_cast<int64_t>(p->H) * (p->axes[1] / 2) +
+                          static_cast<int64_t>(p->W) * (p->axes[2] / 2);
+  if (N > INT32_MAX || entries > INT32_MAX || p->B > 65535 || p->d > 65536 || N * p->d > (int64_t(1) << 38))
+    return DSA_ERR_UNSUPPORTED;
+  const size_t elem = p->dtype == DSA_BF16 ? 2 : 4;
+  const int64_t vec = 16 / elem;  // elements of 16 bytes
+  const bool halves = p->interleaved == 0;
+  bool vector = p->d % 8 == 0 && (halves ? R / 2 : R) % 8 == 0;
+  dsa::RopeParams rp;
+  std::memset(&rp, 0, sizeof(rp));
+  const dsa_view_t* in[2] = {q, k};
+  const dsa_view_t* out[2] = {q_out, k_out};
+  const int n_tens = k != nullptr ? 2 : 1;
+  for (int t = 0; t < n_tens; ++t) {
+    for (int io = 0; io < 2; ++io) {
+      const dsa_view_t* v = io ? out[t] : in[t];
+      if (v->data == nullptr || !aligned(v->data, elem)) return DSA_ERR_INVALID_ARG;
+      const int64_t n[3] = {p->B, p->heads, N};
+      dsa::RopeView& rv = io ? rp.so[t] : rp.si[t];
+      int64_t s[3];
+      for (int a = 0; a < 3; ++a) {
+        s[a] = n[a] <= 1 ? 0 : v->stride[a];
+        if (s[a] < 0 || (n[a] > 1 && io && s[a] < p->d)) return DSA_ERR_INVALID_ARG;
+        if (s[a] % vec != 0) vector = false;
+      }
+      rv.b = s[0];
+      rv.h = s[1];
+      rv.n = s[2];
+      if (!aligned(v->data, 16)) vector = false;
+    }
+    rp.in[t] = in[t]->data;
+    rp.out[t] = out[t]->data;
+  }
+  rp.table = reinterpret_cast<const float2*>(table);
+  rp.H = p->H;
+  rp.W = p->W;
+  rp.N = static_cast<int>(N);
+  rp.heads = p->heads;
+  rp.d = p->d;
+  rp.inverse = p->inverse;
+  for (int a = 0; a < 3; ++a) rp.pairs[a] = p->axes[a] / 2;
+  rp.off[1] = p->T * rp.pairs[0];
+  rp.off[2] = rp.off[1] + p->H * rp.pairs[1];
+  const int half = static_cast<int>(R / 2);
+  const int items = vector ? (halves ? half / 8 + (p->d - 2 * half) / 8 : p->d / 8) : half + (p->d - 2 * half);
+  // heads per thread: all of them when the tokens alone fill the GPU, fewer for small grids
+  const int64_t blocks = (N * items + 255) / 256;
+  int64_t groups = (8 * kPlanSms + blocks * p->B - 1) / (blocks * p->B);
+  const int64_t most = (p->heads + 3) / 4;  // at least the four heads a thread loads together
+  if (groups > most) groups = most;
+  rp.hpt = static_cast<int>((p->heads + groups - 1) / groups);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((p->heads + rp.hpt - 1) / rp.hpt),
+                  static_cast<unsigned>(p->B));
+  if (blocks > INT32_MAX || grid.y > 65535) return DSA_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+#define DSA_ROPE_LAUNCH(K, T)                                    \
+  if (halves)                                                    \
+    dsa::K<T, true><<<grid, 256, 0, s>>>(rp, items, n_tens);     \
+  else                                                           \
+    dsa::K<T, false><<<grid, 256, 0, s>>>(rp, items, n_tens);
+  if (vector) {
+    if (p->dtype == DSA_BF16) {
+      DSA_ROPE_LAUNCH(rope_kernel, __nv_bfloat16)
+    } else {
+      DSA_ROPE_LAUNCH(rope_kernel, float)
+    }
+  } else {
+    if (p->dtype == DSA_BF16) {
+      DSA_ROPE_LAUNCH(rope_any_kernel, __nv_bfloat16)
+    } else {
+      DSA_ROPE_LAUNCH(rope_any_kernel, float)
+    }
+  }
+#undef DSA_ROPE_LAUNCH
+  return launch_status();
+}
+
+dsa_status_t dsa_rmsnorm(const dsa_norm_t* p, const void* x, int64_t x_ld, const void* residual, int64_t r_ld,
+                         const void* weight, void* y, void* sum, void* stream) {
+  return norm_fwd(p, x, x_ld, residual, r_ld, weight, y, nullptr, sum, false, stream);
+}
+
+dsa_status_t dsa_rmsnorm_fp8(const dsa_norm_t* p, const void* x, int64_t x_ld, const void* residual, int64_t r_ld,
+                             const void* weight, void* y8, float* scales, void* sum, void* stream) {
+  return norm_fwd(p, x, x_ld, residual, r_ld, weight, y8, scales, sum, true, stream);
+}
+
+size_t dsa_rmsnorm_bwd_workspace_size(const dsa_norm_t* p) {
+  if (check_norm(p) != DSA_OK) return 0;
+  return round_up(sizeof(float) * norm_bwd_blocks(p, norm_shape(p->C, 2, 256)) * static_cast<size_t>(p->C), kAlign);
+}
+
+dsa_status_t dsa_rmsnorm_bwd(const dsa_norm_t* p, const void* h, int64_t h_ld, const void* weight, const void* dy,
+                             int64_t dy_ld, const void* dh, int64_t dh_ld, void* dx, void* dweight, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  dsa_status_t st = check_norm(p);
+  if (st != DSA_OK) return st;
+  if (!ld_ok(h_ld, p) || !ld_ok(dy_ld, p) || (dh != nullptr && !ld_ok(dh_ld, p))) return DSA_ERR_INVALID_ARG;
+  if (dweight != nullptr && weight == nullptr) return DSA_ERR_INVALID_ARG;
+  const size_t elem = p->dtype == DSA_BF16 ? 2 : 4;
+  if (!aligned(h, elem) || !aligned(dy, elem) || !aligned(dh, elem) || !aligned(weight, elem) || !aligned(dx, elem) ||
+      !aligned(dweight, elem))
+    return DSA_ERR_INVALID_ARG;
+  if (p->rows > 0 && (!h || !dy || !dx)) return DSA_ERR_INVALID_ARG;
+  const NormShape sh = norm_shape(p->C, 2, 256);
+  const unsigned grid = norm_bwd_blocks(p, sh);
+  if (dweight != nullptr && p->rows > 0 &&
+      (workspace == nullptr || ws_bytes < dsa_rmsnorm_bwd_workspace_size(p) || !aligned(workspace, kAlign)))
+    return DSA_ERR_WORKSPACE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(workspace);
+  if (p->rows > 0) {
+    dsa::NormBwdParams np;
+    np.h = h;
+    np.w = weight;
+    np.dy = dy;
+    np.dh = dh;
+    np.dx = dx;
+    np.dw_part = part;
+    np.rows = p->rows;
+    np.h_ld = h_ld;
+    np.dy_ld = dy_ld;
+    np.dh_ld = dh_ld;
+    np.C = p->C;
+    np.W = sh.W;
+    np.eps = p->eps;
+    const bool vec = p->C % 8 == 0 && vec_ok(h, h_ld, p) && vec_ok(dy, dy_ld, p) && vec_ok(dh, dh_ld, p) &&
+                     vec_ok(weight, 0, p) && vec_ok(dx, 0, p);
+    if (p->dtype == DSA_BF16)
+      st = dweight ? launch_norm_bwd<__nv_bfloat16, true>(np, sh, grid, vec, s)
+                   : launch_norm_bwd<__nv_bfloat16, false>(np, sh, grid, vec, s);
+    else
+      st = dweight ? launch_norm_bwd<float, true>(np, sh, grid, vec, s)
+                   : launch_norm_bwd<float, false>(np, sh, grid, vec, s);
+    if (st != DSA_OK) return st;
+  }
+  if (dweight == nullptr) return DSA_OK;
+  const unsigned blocks = static_cast<unsigned>((p->C + 31) / 32);
+  if (p->dtype == DSA_BF16)
+    dsa::rmsnorm_dw_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(part, static_cast<int>(grid), p->C,
+                                                                 static_cast<__nv_bfloat16*>(dweight));
+  else
+    dsa::rmsnorm_dw_kernel<float><<<blocks, 256, 0, s>>>(part, static_cast<int>(grid), p->C,
+                                                         static_cast<float*>(dweight));
+  return launch_status();
+}
+
+}  // extern "C"

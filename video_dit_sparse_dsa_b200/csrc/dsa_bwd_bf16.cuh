@@ -50,6 +50,14 @@ struct BwdBf16Params {
   float* dk_part;
   float* dv_part;
   int64_t part_stride;
+  // cross mode: the keys are an encoder's states, Lk rows of kv head kvh of batch entry b of
+  // which the first kv_len[b] (null: Lk) count; the queries are the Nq rows of each of the
+  // `group` heads that share the kv head; LSE and D are padded to [B * heads, Lp].  With
+  // n_split = 1 dk and dv are written as bf16 through their strides (batch, head, row).
+  const int32_t* kv_len;
+  int kv_heads, group;
+  int qb, qk, qg, db, dkv, dg, kb, kh, vb, vh;  // 1, or 0 for a broadcast (stride 0) dimension of q, dO, k, v
+  int64_t dk_s[3], dv_s[3];
 };
 
 namespace bwd {
@@ -114,11 +122,22 @@ struct BwdChunks {
   int row0, c0, nm, nx;
 };
 
-template <bool kFlatK, bool kExtra>
+// Cross mode: keys of batch entry b.
+__device__ __forceinline__ int bwd_kv_length(const BwdBf16Params& p, int bh) {
+  return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + bh / p.kv_heads), 0), p.Lk);
+}
+
+template <bool kFlatK, bool kExtra, bool kCross = false>
 __device__ __forceinline__ BwdChunks bwd_chunks(const BwdBf16Params& p, const BwdUnit& x) {
   BwdChunks q;
   const int nx = kExtra ? (p.Lxq + 63) / 64 : 0;
-  if constexpr (kFlatK) {
+  if constexpr (kCross) {  // the group's heads in turn, each head's rows in 64-row chunks
+    const int nqm = p.group * ((p.Nq + 63) / 64), per = (nqm + p.n_split - 1) / p.n_split;
+    q.row0 = 0;
+    q.c0 = x.part * per;
+    q.nm = 128 * x.kt < bwd_kv_length(p, x.bh) ? max(min(per, nqm - q.c0), 0) : 0;
+    q.nx = 0;
+  } else if constexpr (kFlatK) {
     const int nqm = (p.Nq + 63) / 64, per = (nqm + p.n_split - 1) / p.n_split;
     q.row0 = 0;
     q.c0 = x.part * per;
@@ -135,9 +154,10 @@ __device__ __forceinline__ BwdChunks bwd_chunks(const BwdBf16Params& p, const Bw
 }
 
 // Query rows present in the unit's chunk c (a flat sequence's last chunk can be partial).
-template <bool kFlatK, bool kExtra>
+template <bool kFlatK, bool kExtra, bool kCross = false>
 __device__ __forceinline__ int bwd_qvalid(const BwdBf16Params& p, const BwdChunks& q, int c) {
   if (!kFlatK && !kExtra) return 64;
+  if constexpr (kCross) return min(p.Nq - 64 * ((q.c0 + c) % ((p.Nq + 63) / 64)), 64);
   if (c < q.nm) return kFlatK ? min(p.Nq - 64 * (q.c0 + c), 64) : 64;
   return min(p.Lxq - 64 * (c - q.nm), 64);
 }
@@ -247,7 +267,12 @@ __global__ void __launch_bounds__(256) bwd_kv_combine(const float* __restrict__ 
 // the end of either load as zeros and get P = dS = 0, and their gradients are not written.
 // kExtra: extra queries (p.Lxq of them, flat maps tmQx, tmDOx, tmLsex, tmDx) follow every
 // unit's own.
-template <bool kFlatK, bool kExtra>
+// kCross (with kFlatK): the keys are an encoder's states that the heads of a group share; a
+// unit walks the query chunks of every head of the group, so the shared head's gradient is
+// summed in one accumulator.  Rank-5 maps (channel, row, head in the group, kv head, batch) of
+// q and dO, rank-4 maps of k and v.  Keys past the batch entry's length may hold anything:
+// their P and dS are set to zero rather than computed.
+template <bool kFlatK, bool kExtra, bool kCross = false>
 __global__ void __launch_bounds__(bwd::kThreads, 1)
     bwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -326,14 +351,20 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
         const BwdUnit x = bwd_unit<kFlatK>(p, u);
-        const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, x);
+        const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, x);
         const int bh = x.bh, n = qc.nm + qc.nx;
+        const int b = kCross ? bh / p.kv_heads : 0, kvh = kCross ? bh % p.kv_heads : 0;
         if (n == 0) continue;
         ok = mbar_wait(kv_free, (uc & 1) ^ 1, abort, 50);
         if (!ok) break;
         ++uc;
         mbar_arrive_expect_tx(kv_full, 2 * kKBytes);
-        if constexpr (kFlatK) {  // rows past Lk load as zeros
+        if constexpr (kCross) {
+          tma_load_4d(smem + kOffK, &tmK, kv_full, 0, 128 * x.kt, kvh * p.kh, b * p.kb);
+          tma_load_4d(smem + kOffK + kKHalf, &tmK, kv_full, 64, 128 * x.kt, kvh * p.kh, b * p.kb);
+          tma_load_4d(smem + kOffV, &tmV, kv_full, 0, 128 * x.kt, kvh * p.vh, b * p.vb);
+          tma_load_4d(smem + kOffV + kKHalf, &tmV, kv_full, 64, 128 * x.kt, kvh * p.vh, b * p.vb);
+        } else if constexpr (kFlatK) {  // rows past Lk load as zeros
           tma_load_3d(smem + kOffK, &tmK, kv_full, 0, 128 * x.kt, bh);
           tma_load_3d(smem + kOffK + kKHalf, &tmK, kv_full, 64, 128 * x.kt, bh);
           tma_load_3d(smem + kOffV, &tmV, kv_full, 0, 128 * x.kt, bh);
@@ -352,7 +383,15 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
           if (!ok) break;
           uint8_t* dst = smem + kOffStage + st * kStageBytes;
           mbar_arrive_expect_tx(ld_full + st, 2 * kQBytes + 512);
-          if ((kExtra && c >= qc.nm) || kFlatK) {  // flat rows (past the end: zeros)
+          if constexpr (kCross) {
+            const int nqc = (p.Nq + 63) / 64, hg = (qc.c0 + c) / nqc, row = 64 * ((qc.c0 + c) % nqc);
+            tma_load_5d(dst, &tmQ, ld_full + st, 0, row, hg * p.qg, kvh * p.qk, b * p.qb);
+            tma_load_5d(dst + kQHalf, &tmQ, ld_full + st, 64, row, hg * p.qg, kvh * p.qk, b * p.qb);
+            tma_load_5d(dst + kQBytes, &tmDO, ld_full + st, 0, row, hg * p.dg, kvh * p.dkv, b * p.db);
+            tma_load_5d(dst + kQBytes + kQHalf, &tmDO, ld_full + st, 64, row, hg * p.dg, kvh * p.dkv, b * p.db);
+            tma_load_2d(dst + 2 * kQBytes, &tmLse, ld_full + st, row, bh * p.group + hg);
+            tma_load_2d(dst + 2 * kQBytes + 512, &tmD, ld_full + st, row, bh * p.group + hg);
+          } else if ((kExtra && c >= qc.nm) || kFlatK) {  // flat rows (past the end: zeros)
             const bool extra = c >= qc.nm;
             const int row = extra ? 64 * (c - qc.nm) : 64 * (qc.c0 + c);
             const CUtensorMap* mq = extra ? &tmQx : &tmQ;
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       int ld = 0, uc = 0, sc = 0, pc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, bwd_unit<kFlatK>(p, u));
+        const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, bwd_unit<kFlatK>(p, u));
         const int n = qc.nm + qc.nx;
         if (n == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(kv_full, uc & 1, abort, 60));
@@ -455,12 +494,12 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
     bool ok = true;
     for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
       const BwdUnit x = bwd_unit<kFlatK>(p, u);
-      const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, x);
+      const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, x);
       const int n = qc.nm + qc.nx;
       // flat keys: this thread's key row may lie past the end (zeros, no gradient)
-      const bool k_ok = !kFlatK || 128 * x.kt + m < p.Lk;
+      const bool k_ok = !kFlatK || 128 * x.kt + m < (kCross ? bwd_kv_length(p, x.bh) : p.Lk);
       for (int c = 0; c < n; ++c, ++cc, ++ld) {
-        const int nvq = bwd_qvalid<kFlatK, kExtra>(p, qc, c) - 32 * h;  // valid queries of this half
+        const int nvq = bwd_qvalid<kFlatK, kExtra, kCross>(p, qc, c) - 32 * h;  // valid queries of this half
         const bool masked = !k_ok || nvq < 32;  // P = dS = 0 for missing keys and queries
         const int b = cc & 1;
         ok = mbar_wait(s_full + b, (cc >> 1) & 1, abort, 70);
@@ -488,6 +527,10 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
             if (masked) {
               if (!k_ok || n0 >= nvq) p0 = 0.f;
               if (!k_ok || n0 + 1 >= nvq) p1 = 0.f;
+              if constexpr (kCross) {  // a padding key's dP may be anything: 0 * (D - D)
+                if (!k_ok || n0 >= nvq) dr[n0] = __float_as_uint(dq4[2 * e]);
+                if (!k_ok || n0 + 1 >= nvq) dr[n0 + 1] = __float_as_uint(dq4[2 * e + 1]);
+              }
             }
             pk[2 * g + e] = pack_bf16x2(p0, p1);
             dk2[2 * g + e] = pack_bf16x2(p0 * (__uint_as_float(dr[n0]) - dq4[2 * e]),
@@ -520,6 +563,10 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       __nv_bfloat16* outp = h ? p.dk : p.dv;
       const float sc_out = h ? p.scale : 1.f;
       uint4* dst = reinterpret_cast<uint4*>(outp + (slice + ktok) * 128);
+      if constexpr (kCross) {
+        const int64_t* s = h ? p.dk_s : p.dv_s;
+        dst = reinterpret_cast<uint4*>(outp + (x.bh / p.kv_heads) * s[0] + (x.bh % p.kv_heads) * s[1] + ktok * s[2]);
+      }
       float4* dstp = nullptr;
       if constexpr (kFlatK) {
         const int64_t o = static_cast<int64_t>(x.part) * p.part_stride + (static_cast<int64_t>(x.bh) * p.Lk + ktok) * 128;
@@ -540,14 +587,20 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) a[j] = 0u;
         }
-        if constexpr (kFlatK) {
-          if (k_row_ok) {
+        if constexpr (kCross) {
+          if (!k_ok) {  // padding: no gradient
+#pragma unroll
+            for (int j = 0; j < 32; ++j) a[j] = 0u;
+          }
+        }
+        if (kFlatK && (!kCross || p.n_split > 1)) {
+          if (k_row_ok && (!kCross || k_ok)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               dstp[g * 8 + j] = make_float4(__uint_as_float(a[4 * j]), __uint_as_float(a[4 * j + 1]),
                                             __uint_as_float(a[4 * j + 2]), __uint_as_float(a[4 * j + 3]));
           }
-        } else {
+        } else if (k_row_ok) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint4 y;
