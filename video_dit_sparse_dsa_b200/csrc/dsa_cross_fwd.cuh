@@ -15,9 +15,9 @@
 //
 // Persistent, warp-specialised, one CTA per SM.  A unit is 128 query rows of one kv head over a
 // range of its key chunks (128 keys); it runs in steps of up to two chunks.  Roles:
-//   warp 8   TMA producer of K (3-entry ring of 32 KB chunks)
+//   warp 8   TMA producer of K (4-entry ring of 32 KB chunks)
 //   warp 10  TMA producer of V (2 entries)
-//   warp 11  TMA producer of Q (2 entries: the next unit's Q is loaded during this one)
+//   warp 11  TMA producer of Q (the next unit's, once the last scores of this one are done)
 //   warp 9   MMA issuer: the scores of step G + 1, which may be the next unit's first, as soon
 //            as the softmax warps hold those of step G in registers, then O += P(G) V(G)
 //   warps 0-7  softmax: warpgroup i takes the step's chunk i (a single chunk: its half i), a
@@ -27,8 +27,8 @@
 // written during the next unit's first step, after that step's P is stored and before it is
 // handed over (the products of that step overwrite O), when the last product of the unit has
 // long finished.
-// K and V of up to 256 keys stay in shared memory for every consecutive unit of their kv head
-// (the CTA's units are a contiguous range of the unit sequence): no reloads from L2.
+// K of up to 512 keys and V of up to 256 stay in shared memory for every consecutive unit of
+// their kv head (the CTA's units are a contiguous range of the unit sequence): no reloads.
 // Units are cut into ranges of equal cost over the CTAs (batch entries have their own lengths).
 // Few query rows over many keys (a single token over every state): up to 128 / Lq heads of a kv
 // head are packed into a unit, so K and V are read once for them, and the keys are cut into
@@ -68,9 +68,9 @@ constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kQWarp = 11;
 constexpr int kRegsSoftmax = 216, kRegsAux = 72;
 constexpr int kRegsAtLaunch = (2 * 128 * kRegsSoftmax + 128 * kRegsAux) / kThreads;  // 168
 static_assert(kRegsAtLaunch * kThreads == 2 * 128 * kRegsSoftmax + 128 * kRegsAux, "split must use the launch registers");
-constexpr int kQStages = 2, kKStages = 3, kVStages = 2;
+constexpr int kKStages = 4, kVStages = 2;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;  // 128 rows x 128 channels; 64 channels
-constexpr uint32_t kOffQ = 0, kOffK = kQStages * kTile, kOffV = kOffK + kKStages * kTile;
+constexpr uint32_t kOffQ = 0, kOffK = kTile, kOffV = kOffK + kKStages * kTile;
 constexpr uint32_t kOffBar = kOffV + kVStages * kTile;
 constexpr uint32_t kOffX = kOffBar + 256;
 constexpr uint32_t kSmemUsed = kOffX + 2 * 2 * 128 * 4;
@@ -81,20 +81,6 @@ constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, 0, 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 256, as in the window forward
 // column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
 constexpr uint32_t kPolyMask = 0x22u;
-
-struct Unit {
-  int b, kvh, part, tile;
-};
-
-__device__ __forceinline__ Unit decode(const CrossFwdParams& p, int u) {
-  Unit x;
-  x.tile = u % p.tiles;
-  const int slice = u / p.tiles;
-  x.part = slice % p.n_split;
-  x.kvh = slice / p.n_split % p.kv_heads;
-  x.b = slice / p.n_split / p.kv_heads;
-  return x;
-}
 
 __device__ __forceinline__ int kv_length(const CrossFwdParams& p, int b) {
   return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + b), 0), p.Lk);
@@ -134,51 +120,93 @@ __device__ __forceinline__ void unit_range(const CrossFwdParams& p, int cta, int
   }
 }
 
-// Walks the steps of the CTA's units that have keys.
+// A unit: 128 rows from `row` of head g of a kv head's group (pk > 1: pk heads' rows from head
+// g), over part `part` of the keys.
+struct Unit {
+  int b, kvh, part, g, row;
+};
+
+// Walks the CTA's units [begin, end) and their steps.  Consecutive units are neighbours in the
+// sequence (row, head in the group, part, kv head, batch), so moving on needs no division.
 struct Cursor {
-  int u, end;      // the unit, and the end of the CTA's range
+  int u, end;
   Unit x;
-  int len;         // keys of the unit's batch entry
-  int c0, n;       // the unit's first chunk and number of chunks
-  int t;           // step
-  bool reuse;      // K and V are those of the previous unit, still in shared memory
-  bool keep;       // the next unit uses them too
+  int len;      // keys of the unit's batch entry
+  int c0, n;    // the unit's first chunk and number of chunks
+  int t;        // step
+  bool same;    // the previous unit of this CTA has the same keys
 
   __device__ __forceinline__ bool valid() const { return u < end; }
   __device__ __forceinline__ int in_step() const { return min(n - 2 * t, 2); }  // chunks of the step
   __device__ __forceinline__ bool last() const { return 2 * t + 2 >= n; }
   // Keys present in the unit's chunk j.
   __device__ __forceinline__ int keys(int j) const { return min(len - 128 * (c0 + j), 128); }
+  // The unit's K (or V) chunks are still in the `stages` ring entries that the previous unit
+  // used; the next unit will find them there too.
+  __device__ __forceinline__ bool reuse(int stages) const { return same && n <= stages; }
+  __device__ __forceinline__ bool keep(const CrossFwdParams& p, int stages) const {
+    return n <= stages && u + 1 < end && (x.row + 128 < p.Lq || x.g + p.pk < p.group);
+  }
 
-  __device__ __forceinline__ void load(const CrossFwdParams& p, int begin) {
-    x = decode(p, u);
-    len = kv_length(p, x.b);
-    const int chunks = (len + 127) / 128, per = chunks_per_part(p, chunks);
-    c0 = x.part * per;
-    n = max(min(per, chunks - c0), 0);
-    t = 0;
-    reuse = n <= 2 && u > begin && x.tile != 0;
-    keep = n <= 2 && u + 1 < end && x.tile + 1 != p.tiles;
-  }
-  // The first unit with keys from u on.
-  __device__ __forceinline__ void settle(const CrossFwdParams& p, int begin) {
-    for (; u < end; ++u) {
-      load(p, begin);
-      if (n > 0) break;
-    }
-  }
   __device__ __forceinline__ void start(const CrossFwdParams& p, int begin, int end_) {
     u = begin;
     end = end_;
-    settle(p, begin);
-  }
-  __device__ __forceinline__ void next(const CrossFwdParams& p, int begin) {
-    if (!last()) {
-      ++t;
-      return;
+    const int tile = u % p.tiles, slice = u / p.tiles;
+    if (p.pk > 1) {
+      x.g = tile * p.pk;
+      x.row = 0;
+    } else {
+      const int per_head = (p.Lq + 127) / 128;
+      x.g = tile / per_head;
+      x.row = 128 * (tile % per_head);
     }
+    x.part = slice % p.n_split;
+    x.kvh = slice / p.n_split % p.kv_heads;
+    x.b = slice / p.n_split / p.kv_heads;
+    same = false;
+    t = 0;
+    if (valid()) chunks(p);
+  }
+  __device__ __forceinline__ void chunks(const CrossFwdParams& p) {
+    len = kv_length(p, x.b);
+    const int all = (len + 127) / 128, per = chunks_per_part(p, all);
+    c0 = x.part * per;
+    n = max(min(per, all - c0), 0);
+  }
+  // The next unit, with or without keys.
+  __device__ __forceinline__ void advance(const CrossFwdParams& p) {
     ++u;
-    settle(p, begin);
+    t = 0;
+    same = true;
+    x.row += 128;
+    if (x.row < p.Lq) return;
+    x.row = 0;
+    x.g += p.pk;
+    if (x.g < p.group) return;
+    x.g = 0;
+    same = false;
+    if (++x.part == p.n_split) {
+      x.part = 0;
+      if (++x.kvh == p.kv_heads) {
+        x.kvh = 0;
+        ++x.b;
+      }
+    }
+    if (valid()) chunks(p);
+  }
+  // This unit, or the next one that has keys.
+  __device__ __forceinline__ void settle(const CrossFwdParams& p) {
+    while (valid() && n == 0) advance(p);
+  }
+  __device__ __forceinline__ void next_unit(const CrossFwdParams& p) {
+    advance(p);
+    settle(p);
+  }
+  __device__ __forceinline__ void next_step(const CrossFwdParams& p) {
+    if (last())
+      next_unit(p);
+    else
+      ++t;
   }
 };
 
@@ -293,7 +321,48 @@ __device__ __forceinline__ void store_o_f32(uint32_t tO, float inv, float4* dst,
   }
 }
 
-// Query row of this thread in a unit: its head and position, or no row.
+// Writes a warp's 32 rows x 64 channels of O, from TMEM times inv (of the lane's own row), as
+// bf16 to rows dst + r * ld, r < n_rows.  A lane holds one row as eight 16-byte vectors; three
+// exchanges within groups of 8 lanes transpose them, so that 8 lanes write one row's 128 bytes
+// together: stores of a lane's own vectors, 32 rows to an instruction, took 22 of 90 us of the
+// 77-key and 86 of 343 us of the 203 + 512-key workload.
+__device__ __forceinline__ void store_o_rows(uint32_t tO, float inv, __nv_bfloat16* dst, int64_t ld, int n_rows) {
+  const int lane = threadIdx.x & 31;
+  uint32_t w[8][4];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint32_t o[32];
+    tmem_ld32_wait(tO + 32 * g, o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      w[4 * g + e / 4][e % 4] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+  }
+#pragma unroll
+  for (int k = 1; k < 8; k <<= 1) {
+    const bool hi = lane & k;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & k) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? w[c][e] : w[c | k][e], k);
+        if (hi)
+          w[c][e] = got;
+        else
+          w[c | k][e] = got;
+      }
+    }
+  }
+  // w[i]: vector (lane & 7) of row (lane & ~7) + i
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = (lane & ~7) + i;
+    if (r < n_rows)
+      *(reinterpret_cast<uint4*>(dst + r * ld) + (lane & 7)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+  }
+}
+
+// Query row of thread r in a unit: its head and position, or no row.
 struct Row {
   bool ok;
   int head, q;
@@ -301,15 +370,13 @@ struct Row {
 
 __device__ __forceinline__ Row unit_row(const CrossFwdParams& p, const Unit& x, int r) {
   Row y;
-  int g;
+  int g = x.g;
   if (p.pk > 1) {  // row r = (head in the pack) * Lq + position
-    g = x.tile * p.pk + r / p.Lq;
+    g += r / p.Lq;
     y.q = r % p.Lq;
     y.ok = r < p.pk * p.Lq && g < p.group;
   } else {
-    const int per_head = (p.Lq + 127) / 128;
-    g = x.tile / per_head;
-    y.q = 128 * (x.tile % per_head) + r;
+    y.q = x.row + r;
     y.ok = y.q < p.Lq;
   }
   y.head = x.kvh * p.group + g;
@@ -333,9 +400,9 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw + pad;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* q_full = bars;                  // [kQStages]
-  uint64_t* q_empty = q_full + kQStages;
-  uint64_t* k_full = q_empty + kQStages;    // [kKStages]
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;              // [kKStages]
   uint64_t* k_empty = k_full + kKStages;
   uint64_t* v_full = k_empty + kKStages;    // [kVStages]
   uint64_t* v_empty = v_full + kVStages;
@@ -348,7 +415,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
   volatile int* abort = reinterpret_cast<volatile int*>(s_full + 10);
   int* range = reinterpret_cast<int*>(s_full + 11);  // [2]
-  static_assert(2 * (kQStages + kKStages + kVStages) + 12 <= 256 / 8, "barriers must fit their 256 bytes");
+  static_assert(2 * (1 + kKStages + kVStages) + 12 <= 256 / 8, "barriers must fit their 256 bytes");
   float* xbuf = reinterpret_cast<float*>(smem + kOffX);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -356,10 +423,8 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
     tma_prefetch_map(&tmQ);
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
-    for (int s = 0; s < kQStages; ++s) {
-      mbar_init(q_full + s, 1);
-      mbar_init(q_empty + s, 1);
-    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
@@ -399,23 +464,13 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       // ------------------------------------------------------------------ TMA producer of Q
       if (lane == 0) {
         Cursor c;
+        c.start(p, begin, end);
         int n = 0;
-        for (c.start(p, begin, end); c.valid(); ++c.u, c.settle(p, begin), ++n) {
-          const int st = n % kQStages;
-          if (!mbar_wait(q_empty + st, ((n / kQStages) & 1) ^ 1, abort, 140)) break;
-          mbar_arrive_expect_tx(q_full + st, p.q_bytes);
-          int g, row;
-          if (p.pk > 1) {
-            g = c.x.tile * p.pk;
-            row = 0;
-          } else {
-            const int per_head = (p.Lq + 127) / 128;
-            g = c.x.tile / per_head;
-            row = 128 * (c.x.tile % per_head);
-          }
-          uint8_t* dst = smem + kOffQ + st * kTile;
-          tma_load_5d(dst, &tmQ, q_full + st, 0, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
-          tma_load_5d(dst + kHalf, &tmQ, q_full + st, 64, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+        for (c.settle(p); c.valid(); c.next_unit(p), ++n) {
+          if (!mbar_wait(q_empty, (n & 1) ^ 1, abort, 140)) break;
+          mbar_arrive_expect_tx(q_full, p.q_bytes);
+          tma_load_5d(smem + kOffQ, &tmQ, q_full, 0, c.x.row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          tma_load_5d(smem + kOffQ + kHalf, &tmQ, q_full, 64, c.x.row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
         }
       }
     } else if (warp == kKWarp || warp == kVWarp) {
@@ -430,8 +485,9 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         Cursor c;
         int ld = 0;
         bool ok = true;
-        for (c.start(p, begin, end); ok && c.valid(); ++c.u, c.settle(p, begin)) {
-          if (c.reuse) continue;  // still in shared memory
+        c.start(p, begin, end);
+        for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
+          if (c.reuse(stages)) continue;  // still in shared memory
           const int head = c.x.kvh * (is_k ? p.kh : p.vh), b = c.x.b * (is_k ? p.kb : p.vb);
           for (int j = 0; j < c.n; ++j, ++ld) {
             const int st = ld % stages;
@@ -453,34 +509,36 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       int qn = 0;          // units whose Q was taken
       int un = 0;          // units whose products into O were issued
       sc.start(p, begin, end);
+      sc.settle(p);
       pc = sc;
       // S of sc's step, the G-th, into the region pair of its parity
       auto issue_s = [&](int G) -> bool {
-        const int e = G & 1, qs = qn % kQStages;
-        if (sc.t == 0 && !warp_wait(q_full + qs, (qn / kQStages) & 1, abort, 150)) return false;
+        const int e = G & 1;
+        if (sc.t == 0 && !warp_wait(q_full, qn & 1, abort, 150)) return false;
         const int nb = sc.in_step();
+        const bool reuse = sc.reuse(kKStages), keep = sc.keep(p, kKStages);
         for (int b = 0; b < nb; ++b) {
           const int pos = ks + 2 * sc.t + b, st = pos % kKStages;
-          if (!sc.reuse && !warp_wait(k_full + st, (pos / kKStages) & 1, abort, 151)) return false;
+          if (!reuse && !warp_wait(k_full + st, (pos / kKStages) & 1, abort, 151)) return false;
           tc_fence_after();
           // only the columns that hold keys, in sixteens: the others are masked
           const uint32_t idesc = idesc_bf16_f32(128, (sc.keys(2 * sc.t + b) + 15) & ~15, 0, 0);
-          uint64_t q = desc_add(dQ, qs * kTile), k = desc_add(dK, st * kTile);
+          uint64_t q = dQ, k = desc_add(dK, st * kTile);
           fwd::opaque(q);
           fwd::opaque(k);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ss_warp(tmem + fwd::col_s(e) + 128 * b, desc_add(q, (kk >> 2) * kHalf + (kk & 3) * 32),
                         desc_add(k, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0);
-          if (!sc.keep) mma_commit_warp(k_empty + st);
+          if (!keep) mma_commit_warp(k_empty + st);
         }
         mma_commit_warp(s_full + e);
         if (sc.last()) {
-          mma_commit_warp(q_empty + qs);
+          mma_commit_warp(q_empty);
           ++qn;
-          if (!sc.keep) ks += sc.n;
+          if (!keep) ks += sc.n;
         }
-        sc.next(p, begin);
+        sc.next_step(p);
         return true;
       };
       bool ok = true;
@@ -493,10 +551,11 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         if (ok && pc.t == 0) ok = warp_wait(o_free, (un & 1) ^ 1, abort, 154);
         if (!ok) break;
         const int nb = pc.in_step();
+        const bool reuse = pc.reuse(kVStages), keep = pc.keep(p, kVStages);
         for (int b = 0; b < nb && ok; ++b) {
           const int pos = vs + 2 * pc.t + b, st = pos % kVStages;
           const int keys = pc.keys(2 * pc.t + b);
-          if (!pc.reuse) {
+          if (!reuse) {
             ok = warp_wait(v_full + st, (pos / kVStages) & 1, abort, 155);
             if (!ok) break;
             if (keys & 15) {
@@ -519,16 +578,16 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
             if (kk < kk_n)
               mma_ts_warp(tmem + kColO, tmem + fwd::col_p(e) + 64 * b + 8 * kk, desc_add(v, kk * 2048), kIdescPV,
                           !first || kk > 0);
-          if (!pc.keep) mma_commit_warp(v_empty + st);
+          if (!keep) mma_commit_warp(v_empty + st);
         }
         if (!ok) break;
         mma_commit_warp(o_done);
         if (pc.last()) {
           mma_commit_warp(o_final);
           ++un;
-          if (!pc.keep) vs += pc.n;
+          if (!keep) vs += pc.n;
         }
-        pc.next(p, begin);
+        pc.next_step(p);
       }
     }
   } else {
@@ -559,8 +618,13 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         store_o_f32(tO, p_inv, reinterpret_cast<float4*>(p.part_o + at * 128) + 16 * i, y.ok);
         if (i == 0 && y.ok) p.part_lse[at] = p_lse;
       } else {
-        const int64_t at = px.b * p.ob + (y.ok ? y.head * p.oh + y.q * p.ol : 0);
-        fwd::store_o(tO, 2, p_inv, reinterpret_cast<uint4*>(p.out + at) + 8 * i, y.ok);
+        if (p.pk > 1) {
+          const int64_t at = px.b * p.ob + (y.ok ? y.head * p.oh + y.q * p.ol : 0);
+          fwd::store_o(tO, 2, p_inv, reinterpret_cast<uint4*>(p.out + at) + 8 * i, y.ok);
+        } else {
+          const int r0 = px.row + (r & ~31);  // the warp's first row
+          store_o_rows(tO, p_inv, p.out + px.b * p.ob + y.head * p.oh + r0 * p.ol + 64 * i, p.ol, p.Lq - r0);
+        }
         if (i == 0 && y.ok) p.lse[row] = p_lse;
       }
       tc_fence_before();
@@ -569,9 +633,8 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       ++un;
     };
     Cursor c;
-    c.end = end;
-    for (c.u = begin; c.u < end; ++c.u) {
-      c.load(p, begin);
+    c.start(p, begin, end);
+    for (; c.valid(); c.advance(p)) {
       if (c.n == 0) {  // no keys: O = 0, LSE = ln 0
         const Row y = unit_row(p, c.x, r);
         if (y.ok) {
