@@ -65,6 +65,7 @@ bool make_view_map(CUtensorMap* map, const dsa_view_t* v, int64_t B, int64_t hea
 // ---------------------------------------------------------------- cross attention
 struct CrossPlan {
   int group, pk, tiles;   // heads per kv head; heads packed into a 128-row unit; units per kv head
+  bool pair;              // the forward runs on CTA pairs
   int64_t units;          // B * kv_heads * tiles
   int chunks;             // 128-key chunks of Lk
   int64_t rows;           // B * heads * Lq
@@ -104,6 +105,8 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
     per = (per + 1) / 2 * 2;
     c->split_q = static_cast<int>((c->chunks + per - 1) / per);
   }
+  // more than one 128-row tile per head, and not in parts: a cluster of two CTAs per 256 rows
+  c->pair = c->split_q == 1 && p->Lq > 128;
   // dK, dV: a unit is 128 keys of one kv head over every query chunk of its group; the query
   // chunks are cut so that the units fill whole waves of SMs (the smallest estimate of waves x
   // (chunks of a part + 4 for the part's own start and end), parts of at least 8 chunks).
@@ -173,6 +176,45 @@ dsa_status_t persistent_grid(K kernel, uint32_t smem, int regs, int64_t units, u
   if (sm_count(&sms) != DSA_OK) return DSA_ERR_CUDA;
   *grid = static_cast<unsigned>(units < sms ? units : sms);
   return DSA_OK;
+}
+
+// The pair form: as many clusters of two as stay resident, looked up once per device.
+dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const dsa::CrossFwdParams& fp, cudaStream_t s) {
+  static std::atomic<int> cache[kPairMaxDevices] = {};
+  auto kernel = dsa::cross_fwd_kernel<true>;
+  unsigned grid = 0;
+  dsa_status_t st = persistent_grid(kernel, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, INT32_MAX, &grid);
+  if (st != DSA_OK) return st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid / 2 * 2, 1, 1);
+  cfg.blockDim = dim3(dsa::crossf::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = dsa::crossf::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  const bool cached = dev >= 0 && dev < kPairMaxDevices;
+  if (cached) n = cache[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      return DSA_ERR_CUDA;
+    }
+    if (cached) cache[dev].store(n, std::memory_order_relaxed);
+  }
+  cfg.gridDim.x = 2u * static_cast<unsigned>(fp.n_units < n ? fp.n_units : n);
+  if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, fp) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
+  return launch_status();
 }
 
 dsa_status_t launch_combine(const dsa::CrossCombineParams& cp, cudaStream_t s) {
@@ -372,10 +414,10 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     int mq[3], mk[3], mv[3];
     const int box_rows = c.pk > 1 ? p->Lq : 128;
     if (!make_view_map(&tq, q, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mq) ||
-        !make_view_map(&tk, k, p->B, p->kv_heads, 0, p->Lk, 128, 1, mk) ||
+        !make_view_map(&tk, k, p->B, p->kv_heads, 0, p->Lk, c.pair ? 64 : 128, 1, mk) ||
         !make_view_map(&tv, v, p->B, p->kv_heads, 0, p->Lk, 128, 1, mv))
       return DSA_ERR_CUDA;
-    fp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;
+    fp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;  // per CTA
     fp.qg = mq[0];
     fp.qk = mq[1];
     fp.qb = mq[2];
@@ -383,10 +425,16 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     fp.kb = mk[2];
     fp.vh = mv[1];
     fp.vb = mv[2];
+    if (c.pair) {
+      fp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
+      fp.n_units = p->B * p->kv_heads * fp.tiles;
+      return launch_cross_pair(tq, tk, tv, fp, s);
+    }
     unsigned grid = 0;
-    st = persistent_grid(dsa::cross_fwd_kernel, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, fp.n_units, &grid);
+    st = persistent_grid(dsa::cross_fwd_kernel<false>, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, fp.n_units,
+                         &grid);
     if (st != DSA_OK) return st;
-    dsa::cross_fwd_kernel<<<grid, dsa::crossf::kThreads, dsa::crossf::kSmemBytes, s>>>(tq, tk, tv, fp);
+    dsa::cross_fwd_kernel<false><<<grid, dsa::crossf::kThreads, dsa::crossf::kSmemBytes, s>>>(tq, tk, tv, fp);
     st = launch_status();
     if (st != DSA_OK || c.split_q == 1) return st;
   }

@@ -13,26 +13,36 @@
 // stand within a factor of two of each other at 256 to 512 keys, and what decides is how well the
 // three overlap from one query tile to the next: a tile has one or two 256-key steps only.
 //
-// Persistent, warp-specialised, one CTA per SM.  A unit is 128 query rows of one kv head over a
-// range of its key chunks (128 keys); it runs in steps of up to two chunks.  Roles:
-//   warp 8   TMA producer of K (4-entry ring of 32 KB chunks)
-//   warp 10  TMA producer of V (2 entries)
-//   warp 11  TMA producer of Q (the next unit's, once the last scores of this one are done)
-//   warp 9   MMA issuer: the scores of step G + 1, which may be the next unit's first, as soon
-//            as the softmax warps hold those of step G in registers, then O += P(G) V(G)
-//   warps 0-7  softmax: warpgroup i takes the step's chunk i (a single chunk: its half i), a
-//            thread per query row; the two threads of a row agree on the row max through shared
-//            memory.
+// Two forms of one persistent, warp-specialised kernel.  Many rows (more than 128 per head) run on
+// CTA pairs (kPair): a cluster of two CTAs holds 256 rows of one head, 128 each, and every product
+// is one M = 256 tcgen05.mma.cta_group::2 issued by the even CTA; the scores take a step's 256
+// keys as N, half from each CTA's shared memory, and P V the 128 channels as N, half from each.
+// So a CTA holds half of K and V: up to 512 keys of both fit beside three Q tiles, and stay for
+// all consecutive units of their kv head, where a single CTA re-reads V for every unit and has no
+// room to load Q ahead (720p over 512 keys: 953 us as single CTAs).  Few rows over many keys (a
+// single token over every state) run on single CTAs, with up to 128 / Lq heads of a kv head packed
+// into a unit, so that K and V are read once for them, and with the keys cut into parts, one unit
+// each, whose fp32 partial outputs cross_merge_kernel joins by their LSEs.
+//
+// A unit is 128 (pair: 256) query rows of one kv head over a range of its key chunks (128 keys),
+// in steps of up to two chunks.  Roles (12 warps per CTA):
+//   warp 8   TMA producer of K and Q
+//   warp 10  TMA producer of V
+//   warp 11  takes each V chunk as it lands, zeroes the rows past the last key that the product
+//            will read (against P = 0, but 0 * NaN is NaN) and hands it to the MMA warp
+//   warp 9   MMA issuer (pair: the even CTA's): the scores of step G + 1, which may be the next
+//            unit's first, as soon as the softmax warps hold those of step G in registers, then
+//            O += P(G) V(G)
+//   warps 0-7  softmax of the CTA's own 128 rows: warpgroup i takes the step's chunk i (a single
+//            chunk: its columns [64 i, 64 i + 64)), a thread per query row; the two threads of a
+//            row agree on the row max through shared memory.
 // The pipeline does not drain between units: a unit's output is read out of TMEM, divided and
 // written during the next unit's first step, after that step's P is stored and before it is
 // handed over (the products of that step overwrite O), when the last product of the unit has
-// long finished.
-// K of up to 512 keys and V of up to 256 stay in shared memory for every consecutive unit of
-// their kv head (the CTA's units are a contiguous range of the unit sequence): no reloads.
-// Units are cut into ranges of equal cost over the CTAs (batch entries have their own lengths).
-// Few query rows over many keys (a single token over every state): up to 128 / Lq heads of a kv
-// head are packed into a unit, so K and V are read once for them, and the keys are cut into
-// parts, one unit each, whose fp32 partial outputs cross_merge_kernel joins by their LSEs.
+// long finished.  The CTA's (pair's) units are a contiguous range of the unit sequence; ranges
+// are cut at equal cost, as batch entries have their own lengths.
+// Pair barriers: loads of K and Q count on the even CTA's barriers, products commit to both
+// CTAs', and the softmax warps and V hand-overs of both arrive on the even CTA's.
 //
 // TMEM (512 columns): as the window forward: regions R0 R1 R2 of 128 columns that scores and P
 // rotate through (even steps: S in R0 R1, P in R0; odd: S in R1 R2, P in R2), O in the fourth.
@@ -41,6 +51,7 @@
 #include <stdint.h>
 
 #include "dsa_fwd_bf16.cuh"
+#include "dsa_fwd_pair.cuh"
 #include "sm100.cuh"
 
 namespace dsa {
@@ -64,20 +75,29 @@ struct CrossFwdParams {
 
 namespace crossf {
 constexpr int kThreads = 384;
-constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kQWarp = 11;
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kHandWarp = 11;
 constexpr int kRegsSoftmax = 216, kRegsAux = 72;
 constexpr int kRegsAtLaunch = (2 * 128 * kRegsSoftmax + 128 * kRegsAux) / kThreads;  // 168
 static_assert(kRegsAtLaunch * kThreads == 2 * 128 * kRegsSoftmax + 128 * kRegsAux, "split must use the launch registers");
-constexpr int kKStages = 4, kVStages = 2;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;  // 128 rows x 128 channels; 64 channels
-constexpr uint32_t kOffQ = 0, kOffK = kTile, kOffV = kOffK + kKStages * kTile;
-constexpr uint32_t kOffBar = kOffV + kVStages * kTile;
-constexpr uint32_t kOffX = kOffBar + 256;
+// Shared memory: 224 KB of Q tiles, K stages and V entries, the barriers, the exchange buffer.
+// Single: Q 1, K 3 and V 3 chunks.  Pair (per CTA): Q 3; K 2 steps, this CTA's half of the keys of
+// each; V 4 chunks of this CTA's 64 channels: both hold four chunks, 512 keys.
+template <bool kPair>
+struct Mem {
+  static constexpr int kQ = kPair ? 3 : 1, kK = kPair ? 2 : 3, kV = kPair ? 4 : 3;
+  static constexpr uint32_t kVBytes = kPair ? kHalf : kTile;
+  static constexpr uint32_t kOffK = kQ * kTile, kOffV = kOffK + kK * kTile;
+  // chunks of a unit whose K, and whose V, fit
+  static constexpr int kKChunks = kPair ? 2 * kK : kK, kVChunks = kV;
+  static_assert(kOffV + kV * kVBytes == 7 * kTile, "both forms use 224 KB");
+};
+constexpr uint32_t kOffBar = 7 * kTile;
+constexpr uint32_t kOffX = kOffBar + 512;
 constexpr uint32_t kSmemUsed = kOffX + 2 * 2 * 128 * 4;
 constexpr uint32_t kSmemBytes = 227 * 1024;
 static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
 constexpr uint32_t kTmemCols = 512, kColO = 384;
-constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, 0, 1);
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 256, as in the window forward
 // column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
 constexpr uint32_t kPolyMask = 0x22u;
@@ -120,14 +140,15 @@ __device__ __forceinline__ void unit_range(const CrossFwdParams& p, int cta, int
   }
 }
 
-// A unit: 128 rows from `row` of head g of a kv head's group (pk > 1: pk heads' rows from head
-// g), over part `part` of the keys.
+// A unit: kRows (128, pair 256) rows from `row` of head g of a kv head's group (pk > 1: pk heads'
+// rows from head g), over part `part` of the keys.
 struct Unit {
   int b, kvh, part, g, row;
 };
 
 // Walks the CTA's units [begin, end) and their steps.  Consecutive units are neighbours in the
 // sequence (row, head in the group, part, kv head, batch), so moving on needs no division.
+template <int kRows>
 struct Cursor {
   int u, end;
   Unit x;
@@ -139,13 +160,15 @@ struct Cursor {
   __device__ __forceinline__ bool valid() const { return u < end; }
   __device__ __forceinline__ int in_step() const { return min(n - 2 * t, 2); }  // chunks of the step
   __device__ __forceinline__ bool last() const { return 2 * t + 2 >= n; }
+  // A pair's step of one chunk: columns of the scores from each CTA (N in multiples of 32).
+  __device__ __forceinline__ int half_columns() const { return ((keys(2 * t) + 31) & ~31) / 2; }
   // Keys present in the unit's chunk j.
   __device__ __forceinline__ int keys(int j) const { return min(len - 128 * (c0 + j), 128); }
-  // The unit's K (or V) chunks are still in the `stages` ring entries that the previous unit
-  // used; the next unit will find them there too.
-  __device__ __forceinline__ bool reuse(int stages) const { return same && n <= stages; }
-  __device__ __forceinline__ bool keep(const CrossFwdParams& p, int stages) const {
-    return n <= stages && u + 1 < end && (x.row + 128 < p.Lq || x.g + p.pk < p.group);
+  // The unit's K (or V) is still in the ring, which holds `chunks`, from the previous unit; the
+  // next unit will find it there too.
+  __device__ __forceinline__ bool reuse(int chunks) const { return same && n <= chunks; }
+  __device__ __forceinline__ bool keep(const CrossFwdParams& p, int chunks) const {
+    return n <= chunks && u + 1 < end && (x.row + kRows < p.Lq || x.g + p.pk < p.group);
   }
 
   __device__ __forceinline__ void start(const CrossFwdParams& p, int begin, int end_) {
@@ -156,9 +179,9 @@ struct Cursor {
       x.g = tile * p.pk;
       x.row = 0;
     } else {
-      const int per_head = (p.Lq + 127) / 128;
+      const int per_head = (p.Lq + kRows - 1) / kRows;
       x.g = tile / per_head;
-      x.row = 128 * (tile % per_head);
+      x.row = kRows * (tile % per_head);
     }
     x.part = slice % p.n_split;
     x.kvh = slice / p.n_split % p.kv_heads;
@@ -178,7 +201,7 @@ struct Cursor {
     ++u;
     t = 0;
     same = true;
-    x.row += 128;
+    x.row += kRows;
     if (x.row < p.Lq) return;
     x.row = 0;
     x.g += p.pk;
@@ -230,13 +253,44 @@ __device__ __forceinline__ void exp2_quartic2(float x0, float x1, float& y0, flo
   y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+// An arrival on the MMA warp's barrier: this CTA's, or the even CTA's of the pair (whose address
+// `lead_bar` gives).
+template <bool kPair>
+__device__ __forceinline__ uint32_t lead_bar(uint64_t* bar) {
+  if constexpr (kPair) return mapa_shared(smem_u32(bar), 0);
+  return smem_u32(bar);
+}
+template <bool kPair>
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  if constexpr (kPair)
+    mbar_arrive_cluster(bar);
+  else
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A barrier that the pair's other CTA arrives on too is acquired at cluster scope.
+template <bool kPair>
+__device__ __forceinline__ bool wait_lead(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
+  if constexpr (kPair) return fwdp::warp_wait_cl(bar, parity, abort, site);
+  return fwd::warp_wait(bar, parity, abort, site);
+}
+
+// The products so far arrive on `bar` (of both CTAs of a pair) when they are done.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (kPair)
+    mma_commit_pair_warp(bar, fwdp::kBoth);
+  else
+    mma_commit_warp(bar);
+}
+
 // One step's softmax for this thread's NC score columns at tS: agrees on the row max with the
 // partner thread, writes P as packed bf16 at tP, updates the reference max and the row sum, and
 // returns whether the reference moved (alpha: the factor that the old O and l take).  Columns
 // from nvalid on hold no key.  With !ok (an earlier wait failed) the thread only takes part in
 // the exchange.
-template <int NC>
-__device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, uint64_t* loaded, float scale_log2,
+template <int NC, bool kPair>
+__device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, uint32_t loaded, float scale_log2,
                                              float& m_used, float& l, float& alpha, float* xbuf, int& xe, int i, int r,
                                              int bar_id, int nvalid) {
   uint32_t s[NC];
@@ -252,7 +306,7 @@ __device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, 
   if (ok) {
     tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(loaded);
+    if ((threadIdx.x & 31) == 0) arrive<kPair>(loaded);
   }
   float mxs[8];
 #pragma unroll
@@ -384,159 +438,257 @@ __device__ __forceinline__ Row unit_row(const CrossFwdParams& p, const Unit& x, 
 }
 }  // namespace crossf
 
+// kPair: launched as clusters of two.
+template <bool kPair>
 __global__ void __launch_bounds__(crossf::kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, CrossFwdParams p) {
   using namespace crossf;
   using fwd::desc_add;
   using fwd::warp_wait;
+  using M = Mem<kPair>;
+  using Cur = Cursor<kPair ? 256 : 128>;
+  constexpr int kCtas = kPair ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
-  if (pad + kSmemUsed > kSmemBytes) {  // uniform over the CTA: nothing has started yet
+  if (pad + kSmemUsed > kSmemBytes) {  // the same in every CTA: nothing has started yet
     if (threadIdx.x == 0) device_report(DSA_DEV_BOUNDS, 5);
     return;
   }
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw + pad;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* q_full = bars;
-  uint64_t* q_empty = bars + 1;
-  uint64_t* k_full = bars + 2;              // [kKStages]
-  uint64_t* k_empty = k_full + kKStages;
-  uint64_t* v_full = k_empty + kKStages;    // [kVStages]
-  uint64_t* v_empty = v_full + kVStages;
-  uint64_t* s_full = v_empty + kVStages;    // [2] scores of a step of parity e ready
-  uint64_t* s_read = s_full + 2;            // [2] loaded by the softmax warps (8)
-  uint64_t* p_full = s_full + 4;            // [2] P of a step of parity e written (8)
-  uint64_t* o_done = s_full + 6;            // the products of a step into O done
-  uint64_t* o_final = s_full + 7;           // the products of a unit done
-  uint64_t* o_free = s_full + 8;            // O of a unit read out (8)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
-  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 10);
+  uint64_t* q_full = bars;                // [kQ]
+  uint64_t* q_empty = q_full + M::kQ;
+  uint64_t* k_full = q_empty + M::kQ;     // [kK]
+  uint64_t* k_empty = k_full + M::kK;
+  uint64_t* v_land = k_empty + M::kK;     // [kV] the chunk has landed in this CTA
+  uint64_t* v_full = v_land + M::kV;      // [kV] handed over (by each CTA)
+  uint64_t* v_empty = v_full + M::kV;
+  uint64_t* s_full = v_empty + M::kV;     // [2] scores of a step of parity e ready
+  uint64_t* s_read = s_full + 2;          // [2] loaded by the softmax warps (8 per CTA)
+  uint64_t* p_full = s_full + 4;          // [2] P of a step of parity e written (8 per CTA)
+  uint64_t* o_done = s_full + 6;          // the products of a step into O done
+  uint64_t* o_final = s_full + 7;         // the products of a unit done
+  uint64_t* o_free = s_full + 8;          // O of a unit read out (8 per CTA)
+  uint64_t* drain = s_full + 9;           // every product issued has completed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 10);
+  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 10) + 1;
   int* range = reinterpret_cast<int*>(s_full + 11);  // [2]
-  static_assert(2 * (1 + kKStages + kVStages) + 12 <= 256 / 8, "barriers must fit their 256 bytes");
+  static_assert(2 * M::kQ + 2 * M::kK + 3 * M::kV + 12 <= 512 / 8, "barriers must fit their 512 bytes");
   float* xbuf = reinterpret_cast<float*>(smem + kOffX);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool lead = rank == 0;
   if (tid == 0) {
     tma_prefetch_map(&tmQ);
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    for (int s = 0; s < kKStages; ++s) {
+    for (int s = 0; s < M::kQ; ++s) {
+      mbar_init(q_full + s, 1);
+      mbar_init(q_empty + s, 1);
+    }
+    for (int s = 0; s < M::kK; ++s) {
       mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
     }
-    for (int s = 0; s < kVStages; ++s) {
-      mbar_init(v_full + s, 1);
+    for (int s = 0; s < M::kV; ++s) {
+      mbar_init(v_land + s, 1);
+      mbar_init(v_full + s, kCtas);
       mbar_init(v_empty + s, 1);
     }
     for (int e = 0; e < 2; ++e) {
       mbar_init(s_full + e, 1);
-      mbar_init(s_read + e, 8);
-      mbar_init(p_full + e, 8);
+      mbar_init(s_read + e, 8 * kCtas);
+      mbar_init(p_full + e, 8 * kCtas);
     }
     mbar_init(o_done, 1);
     mbar_init(o_final, 1);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 8 * kCtas);
+    mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
     int b, e;
-    unit_range(p, blockIdx.x, gridDim.x, b, e);
+    unit_range(p, blockIdx.x / kCtas, gridDim.x / kCtas, b, e);
     range[0] = b;
     range[1] = e;
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers are ready before either arrives on the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int begin = range[0], end = range[1];
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsAux>();
-    if (warp == kQWarp) {
-      // ------------------------------------------------------------------ TMA producer of Q
+    if (warp == kKWarp) {
+      // ------------------------------------------------------------------ TMA producer of K and Q
       if (lane == 0) {
-        Cursor c;
+        Cur c;
         c.start(p, begin, end);
-        int n = 0;
-        for (c.settle(p); c.valid(); c.next_unit(p), ++n) {
-          if (!mbar_wait(q_empty, (n & 1) ^ 1, abort, 140)) break;
-          mbar_arrive_expect_tx(q_full, p.q_bytes);
-          tma_load_5d(smem + kOffQ, &tmQ, q_full, 0, c.x.row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
-          tma_load_5d(smem + kOffQ + kHalf, &tmQ, q_full, 64, c.x.row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+        int ld = 0, un = 0;  // K ring entries loaded, units with keys
+        bool ok = true;
+        auto load_q = [&]() {
+          const int st = un % M::kQ;
+          ok = mbar_wait(q_empty + st, ((un / M::kQ) & 1) ^ 1, abort, 140);
+          ++un;
+          if (!ok) return;
+          uint8_t* dst = smem + st * kTile;
+          const int row = c.x.row + 128 * rank;  // (rows past Lq load as zeros)
+          if (lead) mbar_arrive_expect_tx(q_full + st, kCtas * p.q_bytes);
+          if constexpr (kPair) {
+            const uint32_t bar = lead_bar<kPair>(q_full + st);
+            tma_load_5d_pair(dst, &tmQ, bar, 0, row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+            tma_load_5d_pair(dst + kHalf, &tmQ, bar, 64, row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          } else {
+            tma_load_5d(dst, &tmQ, q_full + st, 0, row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+            tma_load_5d(dst + kHalf, &tmQ, q_full + st, 64, row, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          }
+        };
+        for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
+          if (c.reuse(M::kKChunks)) {  // K is still in shared memory
+            load_q();
+            continue;
+          }
+          // the first step's K, then Q (whose wait is for the previous unit's last scores, and K
+          // of a step does not wait for it), then the other steps' K
+          const int head = c.x.kvh * p.kh, b = c.x.b * p.kb;
+          const int n_loads = kPair ? (c.n + 1) / 2 : c.n, n_first = kPair ? 1 : min(c.n, 2);
+          for (int j = 0; j < n_loads && ok; ++j, ++ld) {
+            if (j == n_first) load_q();
+            const int st = ld % M::kK;
+            if (ok) ok = mbar_wait(k_empty + st, ((ld / M::kK) & 1) ^ 1, abort, 141);
+            if (!ok) break;
+            uint8_t* dst = smem + M::kOffK + st * kTile;
+            if constexpr (kPair) {
+              // a step of two chunks: this CTA's chunk; of one: this CTA's half of its columns
+              // (boxes of 64 keys)
+              c.t = j;
+              const bool two = c.in_step() == 2;
+              const int row = 128 * (c.c0 + 2 * j) + (two ? 128 : c.half_columns()) * rank;
+              if (lead) mbar_arrive_expect_tx(k_full + st, two ? 2 * kTile : kTile);
+              const uint32_t bar = lead_bar<kPair>(k_full + st);
+              for (int h = 0; h < (two ? 2 : 1); ++h) {
+                tma_load_4d_pair(dst + h * (kHalf / 2), &tmK, bar, 0, row + 64 * h, head, b);
+                tma_load_4d_pair(dst + kHalf + h * (kHalf / 2), &tmK, bar, 64, row + 64 * h, head, b);
+              }
+            } else {
+              mbar_arrive_expect_tx(k_full + st, kTile);
+              tma_load_4d(dst, &tmK, k_full + st, 0, 128 * (c.c0 + j), head, b);
+              tma_load_4d(dst + kHalf, &tmK, k_full + st, 64, 128 * (c.c0 + j), head, b);
+            }
+          }
+          if (ok && n_loads <= n_first) load_q();
         }
       }
-    } else if (warp == kKWarp || warp == kVWarp) {
-      // ------------------------------------------------------------------ TMA producers of K and V
+    } else if (warp == kVWarp) {
+      // ------------------------------------------------------------------ TMA producer of V
       if (lane == 0) {
-        const bool is_k = warp == kKWarp;
-        const CUtensorMap* map = is_k ? &tmK : &tmV;
-        const int stages = is_k ? kKStages : kVStages;
-        uint64_t* full0 = is_k ? k_full : v_full;
-        uint64_t* empty0 = is_k ? k_empty : v_empty;
-        uint8_t* base = smem + (is_k ? kOffK : kOffV);
-        Cursor c;
+        Cur c;
         int ld = 0;
         bool ok = true;
         c.start(p, begin, end);
         for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
-          if (c.reuse(stages)) continue;  // still in shared memory
-          const int head = c.x.kvh * (is_k ? p.kh : p.vh), b = c.x.b * (is_k ? p.kb : p.vb);
+          if (c.reuse(M::kVChunks)) continue;
+          const int head = c.x.kvh * p.vh, b = c.x.b * p.vb;
           for (int j = 0; j < c.n; ++j, ++ld) {
-            const int st = ld % stages;
-            ok = mbar_wait(empty0 + st, ((ld / stages) & 1) ^ 1, abort, is_k ? 141 : 142);
+            const int st = ld % M::kV;
+            ok = mbar_wait(v_empty + st, ((ld / M::kV) & 1) ^ 1, abort, 142);
             if (!ok) break;
-            mbar_arrive_expect_tx(full0 + st, kTile);
-            tma_load_4d(base + st * kTile, map, full0 + st, 0, 128 * (c.c0 + j), head, b);
-            tma_load_4d(base + st * kTile + kHalf, map, full0 + st, 64, 128 * (c.c0 + j), head, b);
+            uint8_t* dst = smem + M::kOffV + st * M::kVBytes;
+            mbar_arrive_expect_tx(v_land + st, M::kVBytes);
+            tma_load_4d(dst, &tmV, v_land + st, 64 * rank, 128 * (c.c0 + j), head, b);
+            if constexpr (!kPair) tma_load_4d(dst + kHalf, &tmV, v_land + st, 64, 128 * (c.c0 + j), head, b);
           }
         }
       }
-    } else {
+    } else if (warp == kHandWarp) {
+      // ------------------------------------------------------------------ V hand-over (whole warp)
+      Cur c;
+      int ld = 0;
+      bool ok = true;
+      c.start(p, begin, end);
+      for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
+        if (c.reuse(M::kVChunks)) continue;
+        for (int j = 0; j < c.n; ++j, ++ld) {
+          const int st = ld % M::kV;
+          ok = warp_wait(v_land + st, (ld / M::kV) & 1, abort, 143);
+          if (!ok) break;
+          const int keys = c.keys(j);
+          if (keys & 15) {  // rows [keys, next multiple of 16): zeros, whatever the padding holds
+            const int pad_rows = 16 - (keys & 15);
+            if constexpr (kPair) {
+              const uint32_t v0 = sbase + M::kOffV + st * M::kVBytes + (lane & 7) * 16;
+              for (int rr = lane >> 3; rr < pad_rows; rr += 4) st_shared_v4(v0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
+            } else {
+              const uint32_t v0 = sbase + M::kOffV + st * M::kVBytes + (lane >> 3 & 1) * kHalf + (lane & 7) * 16;
+              for (int rr = lane >> 4; rr < pad_rows; rr += 2) st_shared_v4(v0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (kPair)
+              mbar_arrive_release_cluster(lead_bar<kPair>(v_full + st));
+            else
+              mbar_arrive(v_full + st);
+          }
+        }
+      }
+    } else if (lead) {
       // ------------------------------------------------------------------ MMA issuer (whole warp)
-      const uint64_t dQ = smem_desc_sw128(sbase + kOffQ, 16, 1024);
-      const uint64_t dK = smem_desc_sw128(sbase + kOffK, 16, 1024);     // K-major
-      const uint64_t dV = smem_desc_sw128(sbase + kOffV, kHalf, 1024);  // MN-major
-      Cursor sc, pc;   // the steps whose scores and whose P V products come next
-      int ks = 0, vs = 0;  // ring positions of the current units' first chunks
-      int qn = 0;          // units whose Q was taken
-      int un = 0;          // units whose products into O were issued
+      const uint64_t dQ = smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dK = smem_desc_sw128(sbase + M::kOffK, 16, 1024);     // K-major
+      const uint64_t dV = smem_desc_sw128(sbase + M::kOffV, kHalf, 1024);  // MN-major
+      Cur sc, pc;          // the steps whose scores and whose P V products come next
+      int ks = 0, vs = 0;  // ring positions of the current units' first K stage and V entry
+      int qn = 0, un = 0;  // units whose Q was taken, units whose products into O were issued
       sc.start(p, begin, end);
       sc.settle(p);
       pc = sc;
-      // S of sc's step, the G-th, into the region pair of its parity
+      // S of sc's step, the G-th, into the region pair of its parity; only columns that hold keys,
+      // in sixteens (a pair's two-chunk step: all 256): the others are masked
       auto issue_s = [&](int G) -> bool {
-        const int e = G & 1;
-        if (sc.t == 0 && !warp_wait(q_full, qn & 1, abort, 150)) return false;
-        const int nb = sc.in_step();
-        const bool reuse = sc.reuse(kKStages), keep = sc.keep(p, kKStages);
-        for (int b = 0; b < nb; ++b) {
-          const int pos = ks + 2 * sc.t + b, st = pos % kKStages;
-          if (!reuse && !warp_wait(k_full + st, (pos / kKStages) & 1, abort, 151)) return false;
+        const int e = G & 1, qs = qn % M::kQ;
+        if (sc.t == 0 && !wait_lead<kPair>(q_full + qs, (qn / M::kQ) & 1, abort, 150)) return false;
+        const bool reuse = sc.reuse(M::kKChunks), keep = sc.keep(p, M::kKChunks);
+        const int nb = sc.in_step(), loads = kPair ? 1 : nb;
+        for (int b = 0; b < loads; ++b) {
+          const int pos = ks + (kPair ? sc.t : 2 * sc.t + b), st = pos % M::kK;
+          if (!reuse && !wait_lead<kPair>(k_full + st, (pos / M::kK) & 1, abort, 151)) return false;
           tc_fence_after();
-          // only the columns that hold keys, in sixteens: the others are masked
-          const uint32_t idesc = idesc_bf16_f32(128, (sc.keys(2 * sc.t + b) + 15) & ~15, 0, 0);
-          uint64_t q = dQ, k = desc_add(dK, st * kTile);
+          uint64_t q = desc_add(dQ, qs * kTile), k = desc_add(dK, st * kTile);
           fwd::opaque(q);
           fwd::opaque(k);
+          const uint32_t idesc = kPair ? idesc_bf16_f32(256, nb == 2 ? 256 : 2 * sc.half_columns(), 0, 0)
+                                       : idesc_bf16_f32(128, (sc.keys(2 * sc.t + b) + 15) & ~15, 0, 0);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ss_warp(tmem + fwd::col_s(e) + 128 * b, desc_add(q, (kk >> 2) * kHalf + (kk & 3) * 32),
-                        desc_add(k, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0);
-          if (!keep) mma_commit_warp(k_empty + st);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+            if constexpr (kPair)
+              mma_ss_pair_warp(tmem + fwd::col_s(e), desc_add(q, o), desc_add(k, o), idesc, kk > 0);
+            else
+              mma_ss_warp(tmem + fwd::col_s(e) + 128 * b, desc_add(q, o), desc_add(k, o), idesc, kk > 0);
+          }
+          if (!keep) commit<kPair>(k_empty + st);
         }
-        mma_commit_warp(s_full + e);
+        commit<kPair>(s_full + e);
         if (sc.last()) {
-          mma_commit_warp(q_empty);
+          commit<kPair>(q_empty + qs);
           ++qn;
-          if (!keep) ks += sc.n;
+          if (!keep) ks += kPair ? (sc.n + 1) / 2 : sc.n;
         }
         sc.next_step(p);
         return true;
@@ -545,50 +697,50 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       if (sc.valid()) ok = issue_s(0);
       for (int G = 0; ok && pc.valid(); ++G) {
         const int e = G & 1;
-        ok = warp_wait(s_read + e, (G >> 1) & 1, abort, 152);
+        ok = wait_lead<kPair>(s_read + e, (G >> 1) & 1, abort, 152);
         if (ok && sc.valid()) ok = issue_s(G + 1);
-        if (ok) ok = warp_wait(p_full + e, (G >> 1) & 1, abort, 153);
-        if (ok && pc.t == 0) ok = warp_wait(o_free, (un & 1) ^ 1, abort, 154);
+        if (ok) ok = wait_lead<kPair>(p_full + e, (G >> 1) & 1, abort, 153);
+        if (ok && pc.t == 0) ok = wait_lead<kPair>(o_free, (un & 1) ^ 1, abort, 154);
         if (!ok) break;
         const int nb = pc.in_step();
-        const bool reuse = pc.reuse(kVStages), keep = pc.keep(p, kVStages);
+        const bool reuse = pc.reuse(M::kVChunks), keep = pc.keep(p, M::kVChunks);
         for (int b = 0; b < nb && ok; ++b) {
-          const int pos = vs + 2 * pc.t + b, st = pos % kVStages;
-          const int keys = pc.keys(2 * pc.t + b);
-          if (!reuse) {
-            ok = warp_wait(v_full + st, (pos / kVStages) & 1, abort, 155);
-            if (!ok) break;
-            if (keys & 15) {
-              // rows past the last key up to the next multiple of 16 meet P = 0 in the product:
-              // zeros there, whatever the padding holds (0 * NaN is NaN)
-              const int pad_rows = 16 - (keys & 15);
-              const uint32_t v0 = sbase + kOffV + st * kTile + (lane >> 3 & 1) * kHalf + (lane & 7) * 16;
-              for (int rr = lane >> 4; rr < pad_rows; rr += 2) st_shared_v4(v0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
+          const int pos = vs + 2 * pc.t + b, st = pos % M::kV;
+          if (!reuse) ok = wait_lead<kPair>(v_full + st, (pos / M::kV) & 1, abort, 155);
+          if (!ok) break;
           tc_fence_after();
-          uint64_t v = desc_add(dV, st * kTile);
+          uint64_t v = desc_add(dV, st * M::kVBytes);
           fwd::opaque(v);
-          const int kk_n = (keys + 15) >> 4;
+          const int kk_n = (pc.keys(2 * pc.t + b) + 15) >> 4;
           const bool first = pc.t == 0 && b == 0;
+          const uint32_t tP = tmem + fwd::col_p(e) + 64 * b;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < kk_n)
-              mma_ts_warp(tmem + kColO, tmem + fwd::col_p(e) + 64 * b + 8 * kk, desc_add(v, kk * 2048), kIdescPV,
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk >= kk_n) continue;
+            if constexpr (kPair)
+              mma_ts_pair_warp(tmem + kColO, tP + 8 * kk, desc_add(v, kk * 2048), idesc_bf16_f32(256, 128, 0, 1),
+                               !first || kk > 0);
+            else
+              mma_ts_warp(tmem + kColO, tP + 8 * kk, desc_add(v, kk * 2048), idesc_bf16_f32(128, 128, 0, 1),
                           !first || kk > 0);
-          if (!keep) mma_commit_warp(v_empty + st);
+          }
+          if (!keep) commit<kPair>(v_empty + st);
         }
         if (!ok) break;
-        mma_commit_warp(o_done);
+        commit<kPair>(o_done);
         if (pc.last()) {
-          mma_commit_warp(o_final);
+          commit<kPair>(o_final);
           ++un;
           if (!keep) vs += pc.n;
         }
         pc.next_step(p);
       }
+      // every product issued has completed before the TMEM is released
+      if constexpr (kPair)
+        mma_commit_pair_warp(drain, 1);
+      else
+        mma_commit_warp(drain);
+      fwdp::drain_wait(drain, 0);
     }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
@@ -605,7 +757,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
     bool ok = true;
     // the unit whose output is still in TMEM
     bool pending = false;
-    Unit px;
+    Unit px;  // (row: this CTA's first)
     float p_inv = 0.f, p_lse = 0.f;
     auto write_out = [&]() {  // the un-th unit's
       ok = warp_wait(o_final, un & 1, abort, 162);
@@ -629,14 +781,16 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (lane == 0) arrive<kPair>(lead_bar<kPair>(o_free));
       ++un;
     };
-    Cursor c;
+    Cur c;
     c.start(p, begin, end);
     for (; c.valid(); c.advance(p)) {
       if (c.n == 0) {  // no keys: O = 0, LSE = ln 0
-        const Row y = unit_row(p, c.x, r);
+        Unit x = c.x;
+        x.row += 128 * rank;
+        const Row y = unit_row(p, x, r);
         if (y.ok) {
           const int64_t row = (static_cast<int64_t>(c.x.b) * p.heads + y.head) * p.Lq + y.q;
           if (p.n_split > 1) {
@@ -654,17 +808,17 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       float m_used = -INFINITY, l = 0.f;
       for (c.t = 0; 2 * c.t < c.n; ++c.t, ++G) {
         const int e = G & 1;
-        if (ok) ok = warp_wait(s_full + e, (G >> 1) & 1, abort, 160);
+        if (ok) ok = warp_wait(s_full + e, (G >> 1) & 1, abort, 160);  // (committed to this CTA too)
         if (ok) tc_fence_after();
         float alpha;
         bool need;
         if (c.in_step() == 2)
-          need = softmax_step<128>(ok, tmem + fwd::col_s(e) + 128 * i + lane_off, tmem + fwd::col_p(e) + 64 * i + lane_off,
-                                   s_read + e, p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
+          need = softmax_step<128, kPair>(ok, tmem + fwd::col_s(e) + 128 * i + lane_off, tmem + fwd::col_p(e) + 64 * i + lane_off,
+                                   lead_bar<kPair>(s_read + e), p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
                                    c.keys(2 * c.t + i));
         else
-          need = softmax_step<64>(ok, tmem + fwd::col_s(e) + 64 * i + lane_off, tmem + fwd::col_p(e) + 32 * i + lane_off,
-                                  s_read + e, p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
+          need = softmax_step<64, kPair>(ok, tmem + fwd::col_s(e) + 64 * i + lane_off, tmem + fwd::col_p(e) + 32 * i + lane_off,
+                                  lead_bar<kPair>(s_read + e), p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
                                   min(max(c.keys(2 * c.t) - 64 * i, 0), 64));
         if (ok && c.t == 0 && pending) write_out();
         if (ok && c.t > 0 && __any_sync(0xffffffffu, need)) {
@@ -678,11 +832,12 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + e);
+          if (lane == 0) arrive<kPair>(lead_bar<kPair>(p_full + e));
         }
       }
       const float l_all = l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, l);
       px = c.x;
+      px.row += 128 * rank;
       p_inv = 1.f / l_all;
       p_lse = (m_used + __log2f(l_all)) * 0.69314718055994531f;
       pending = true;
@@ -692,9 +847,20 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort && tid == 0) {
+    // after a failed wait, give loads already issued time to land before the CTA leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) {
+    }
+  }
+  __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA leaves while the other may still reach into it
   if (warp == kMmaWarp) {
     __syncwarp();
-    tmem_dealloc(tmem, kTmemCols);
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, kTmemCols);
+    else
+      tmem_dealloc(tmem, kTmemCols);
   }
 }
 
