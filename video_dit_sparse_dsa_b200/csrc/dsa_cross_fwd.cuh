@@ -284,6 +284,15 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
     mma_commit_warp(bar);
 }
 
+// O (+)= P V over 16 keys: P at tP, V at the descriptor.
+template <bool kPair>
+__device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t tP, uint64_t v, bool accumulate) {
+  if constexpr (kPair)
+    mma_ts_pair_warp(tmem + kColO, tP, v, idesc_bf16_f32(256, 128, 0, 1), accumulate);
+  else
+    mma_ts_warp(tmem + kColO, tP, v, idesc_bf16_f32(128, 128, 0, 1), accumulate);
+}
+
 // One step's softmax for this thread's NC score columns at tS: agrees on the row max with the
 // partner thread, writes P as packed bf16 at tP, updates the reference max and the row sum, and
 // returns whether the reference moved (alpha: the factor that the old O and l take).  Columns
@@ -714,15 +723,12 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           const int kk_n = (pc.keys(2 * pc.t + b) + 15) >> 4;
           const bool first = pc.t == 0 && b == 0;
           const uint32_t tP = tmem + fwd::col_p(e) + 64 * b;
+          if (kk_n == 8) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            if (kk >= kk_n) continue;
-            if constexpr (kPair)
-              mma_ts_pair_warp(tmem + kColO, tP + 8 * kk, desc_add(v, kk * 2048), idesc_bf16_f32(256, 128, 0, 1),
-                               !first || kk > 0);
-            else
-              mma_ts_warp(tmem + kColO, tP + 8 * kk, desc_add(v, kk * 2048), idesc_bf16_f32(128, 128, 0, 1),
-                          !first || kk > 0);
+            for (int kk = 0; kk < 8; ++kk) issue_pv<kPair>(tmem, tP + 8 * kk, desc_add(v, kk * 2048), !first || kk > 0);
+          } else {  // the last chunk: only the sixteens that hold keys
+#pragma unroll 1
+            for (int kk = 0; kk < kk_n; ++kk) issue_pv<kPair>(tmem, tP + 8 * kk, desc_add(v, kk * 2048), !first || kk > 0);
           }
           if (!keep) commit<kPair>(v_empty + st);
         }
