@@ -180,7 +180,7 @@ dsa_status_t persistent_grid(K kernel, uint32_t smem, int regs, int64_t units, u
 
 // The pair form: as many clusters of two as stay resident, looked up once per device.
 dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const dsa::CrossFwdParams& fp, cudaStream_t s) {
+                               const CUtensorMap& to, const dsa::CrossFwdParams& fp, cudaStream_t s) {
   static std::atomic<int> cache[kPairMaxDevices] = {};
   auto kernel = dsa::cross_fwd_kernel<true>;
   unsigned grid = 0;
@@ -210,7 +210,7 @@ dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, con
     if (cached) cache[dev].store(n, std::memory_order_relaxed);
   }
   cfg.gridDim.x = 2u * static_cast<unsigned>(fp.n_units < n ? fp.n_units : n);
-  if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, fp) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, to, fp) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
@@ -428,13 +428,16 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     if (c.pair) {
       fp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
       fp.n_units = p->B * p->kv_heads * fp.tiles;
-      return launch_cross_pair(tq, tk, tv, fp, s);
+      CUtensorMap to;
+      int mo[3];
+      if (!make_view_map(&to, out, p->B, p->heads, c.group, p->Lq, 32, 1, mo)) return DSA_ERR_CUDA;
+      return launch_cross_pair(tq, tk, tv, to, fp, s);
     }
     unsigned grid = 0;
     st = persistent_grid(dsa::cross_fwd_kernel<false>, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, fp.n_units,
                          &grid);
     if (st != DSA_OK) return st;
-    dsa::cross_fwd_kernel<false><<<grid, dsa::crossf::kThreads, dsa::crossf::kSmemBytes, s>>>(tq, tk, tv, fp);
+    dsa::cross_fwd_kernel<false><<<grid, dsa::crossf::kThreads, dsa::crossf::kSmemBytes, s>>>(tq, tk, tv, tq, fp);
     st = launch_status();
     if (st != DSA_OK || c.split_q == 1) return st;
   }

@@ -80,17 +80,17 @@ constexpr int kRegsSoftmax = 216, kRegsAux = 72;
 constexpr int kRegsAtLaunch = (2 * 128 * kRegsSoftmax + 128 * kRegsAux) / kThreads;  // 168
 static_assert(kRegsAtLaunch * kThreads == 2 * 128 * kRegsSoftmax + 128 * kRegsAux, "split must use the launch registers");
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;  // 128 rows x 128 channels; 64 channels
-// Shared memory: 224 KB of Q tiles, K stages and V entries, the barriers, the exchange buffer.
-// Single: Q 1, K 3 and V 3 chunks.  Pair (per CTA): Q 3; K 2 steps, this CTA's half of the keys of
-// each; V 4 chunks of this CTA's 64 channels: both hold four chunks, 512 keys.
+// Shared memory: 224 KB of tiles, the barriers, the exchange buffer.
+// Single: Q 1, K 3 and V 3 chunks.  Pair (per CTA): Q 2; K 2 steps, this CTA's half of the keys of
+// each; V 4 chunks of this CTA's 64 channels (both hold four chunks, 512 keys); 32 KB of output.
 template <bool kPair>
 struct Mem {
-  static constexpr int kQ = kPair ? 3 : 1, kK = kPair ? 2 : 3, kV = kPair ? 4 : 3;
+  static constexpr int kQ = kPair ? 2 : 1, kK = kPair ? 2 : 3, kV = kPair ? 4 : 3;
   static constexpr uint32_t kVBytes = kPair ? kHalf : kTile;
-  static constexpr uint32_t kOffK = kQ * kTile, kOffV = kOffK + kK * kTile;
+  static constexpr uint32_t kOffK = kQ * kTile, kOffV = kOffK + kK * kTile, kOffOut = kOffV + kV * kVBytes;
   // chunks of a unit whose K, and whose V, fit
   static constexpr int kKChunks = kPair ? 2 * kK : kK, kVChunks = kV;
-  static_assert(kOffV + kV * kVBytes == 7 * kTile, "both forms use 224 KB");
+  static_assert(kOffOut + (kPair ? kTile : 0) == 7 * kTile, "both forms use 224 KB");
 };
 constexpr uint32_t kOffBar = 7 * kTile;
 constexpr uint32_t kOffX = kOffBar + 512;
@@ -384,44 +384,23 @@ __device__ __forceinline__ void store_o_f32(uint32_t tO, float inv, float4* dst,
   }
 }
 
-// Writes a warp's 32 rows x 64 channels of O, from TMEM times inv (of the lane's own row), as
-// bf16 to rows dst + r * ld, r < n_rows.  A lane holds one row as eight 16-byte vectors; three
-// exchanges within groups of 8 lanes transpose them, so that 8 lanes write one row's 128 bytes
-// together: stores of a lane's own vectors, 32 rows to an instruction, took 22 of 90 us of the
-// 77-key and 86 of 343 us of the 203 + 512-key workload.
-__device__ __forceinline__ void store_o_rows(uint32_t tO, float inv, __nv_bfloat16* dst, int64_t ld, int n_rows) {
-  const int lane = threadIdx.x & 31;
-  uint32_t w[8][4];
+// A warp's 32 rows x 64 channels of O, from TMEM times inv (of the lane's own row), as bf16 to
+// shared memory, 128-byte swizzled (16-byte vector c of row r at c ^ (r % 8)) as a TMA store
+// reads them.
+__device__ __forceinline__ void stage_o(uint32_t tO, float inv, uint32_t stage) {
+  const uint32_t lane = threadIdx.x & 31, row = stage + lane * 128;
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
+  for (uint32_t g = 0; g < 2; ++g) {
     uint32_t o[32];
     tmem_ld32_wait(tO + 32 * g, o);
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      w[4 * g + e / 4][e % 4] = pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-  }
+    for (uint32_t c = 0; c < 4; ++c) {
+      uint32_t w[4];
 #pragma unroll
-  for (int k = 1; k < 8; k <<= 1) {
-    const bool hi = lane & k;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c & k) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? w[c][e] : w[c | k][e], k);
-        if (hi)
-          w[c][e] = got;
-        else
-          w[c | k][e] = got;
-      }
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+      st_shared_v4(row + (((4 * g + c) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
     }
-  }
-  // w[i]: vector (lane & 7) of row (lane & ~7) + i
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = (lane & ~7) + i;
-    if (r < n_rows)
-      *(reinterpret_cast<uint4*>(dst + r * ld) + (lane & 7)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
   }
 }
 
@@ -451,7 +430,8 @@ __device__ __forceinline__ Row unit_row(const CrossFwdParams& p, const Unit& x, 
 template <bool kPair>
 __global__ void __launch_bounds__(crossf::kThreads, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, CrossFwdParams p) {
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                     CrossFwdParams p) {
   using namespace crossf;
   using fwd::desc_add;
   using fwd::warp_wait;
@@ -495,6 +475,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
     tma_prefetch_map(&tmQ);
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
+    if constexpr (kPair) tma_prefetch_map(&tmO);
     for (int s = 0; s < M::kQ; ++s) {
       mbar_init(q_full + s, 1);
       mbar_init(q_empty + s, 1);
@@ -766,28 +747,44 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
     Unit px;  // (row: this CTA's first)
     float p_inv = 0.f, p_lse = 0.f;
     auto write_out = [&]() {  // the un-th unit's
+      if constexpr (kPair) {
+        if (lane == 0) tma_store_wait_read();  // the unit before has left the buffer
+      }
       ok = warp_wait(o_final, un & 1, abort, 162);
       if (!ok) return;
       tc_fence_after();
       const Row y = unit_row(p, px, r);
       const int64_t row = (static_cast<int64_t>(px.b) * p.heads + (y.ok ? y.head : 0)) * p.Lq + (y.ok ? y.q : 0);
-      if (p.n_split > 1) {
-        const int64_t at = px.part * rows + row;
-        store_o_f32(tO, p_inv, reinterpret_cast<float4*>(p.part_o + at * 128) + 16 * i, y.ok);
-        if (i == 0 && y.ok) p.part_lse[at] = p_lse;
-      } else {
-        if (p.pk > 1) {
-          const int64_t at = px.b * p.ob + (y.ok ? y.head * p.oh + y.q * p.ol : 0);
-          fwd::store_o(tO, 2, p_inv, reinterpret_cast<uint4*>(p.out + at) + 8 * i, y.ok);
-        } else {
-          const int r0 = px.row + (r & ~31);  // the warp's first row
-          store_o_rows(tO, p_inv, p.out + px.b * p.ob + y.head * p.oh + r0 * p.ol + 64 * i, p.ol, p.Lq - r0);
+      if constexpr (kPair) {
+        // through shared memory and a TMA store of the warp's 32 rows x 64 channels, 4 KB each
+        const uint32_t off = M::kOffOut + warp * 4096;
+        stage_o(tO, p_inv, sbase + off);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          arrive<kPair>(lead_bar<kPair>(o_free));
+          const int r0 = px.row + 32 * (warp & 3);
+          if (r0 < p.Lq) {  // (rows past Lq are not written)
+            tma_store_5d(&tmO, smem + off, 64 * i, r0, px.g, px.kvh, px.b);
+            tma_store_commit();
+          }
         }
         if (i == 0 && y.ok) p.lse[row] = p_lse;
+      } else {
+        if (p.n_split > 1) {
+          const int64_t at = px.part * rows + row;
+          store_o_f32(tO, p_inv, reinterpret_cast<float4*>(p.part_o + at * 128) + 16 * i, y.ok);
+          if (i == 0 && y.ok) p.part_lse[at] = p_lse;
+        } else {
+          const int64_t at = px.b * p.ob + (y.ok ? y.head * p.oh + y.q * p.ol : 0);
+          fwd::store_o(tO, 2, p_inv, reinterpret_cast<uint4*>(p.out + at) + 8 * i, y.ok);
+          if (i == 0 && y.ok) p.lse[row] = p_lse;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive<kPair>(lead_bar<kPair>(o_free));
       ++un;
     };
     Cur c;
@@ -849,6 +846,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       pending = true;
     }
     if (ok && pending) write_out();
+    if (kPair && lane == 0) tma_store_wait_read();
   }
 
   tc_fence_before();
