@@ -688,12 +688,13 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       for (int G = 0; ok && pc.valid(); ++G) {
         const int e = G & 1;
         ok = wait_lead<kPair>(s_read + e, (G >> 1) & 1, abort, 152);
+        const Cur ahead = sc;  // the step after pc's
         if (ok && sc.valid()) ok = issue_s(G + 1);
-        if (ok) ok = wait_lead<kPair>(p_full + e, (G >> 1) & 1, abort, 153);
-        if (ok && pc.t == 0) ok = wait_lead<kPair>(o_free, (un & 1) ^ 1, abort, 154);
-        if (!ok) break;
         const int nb = pc.in_step();
         const bool reuse = pc.reuse(M::kVChunks), keep = pc.keep(p, M::kVChunks);
+        if (ok && pc.t == 0) ok = wait_lead<kPair>(o_free, (un & 1) ^ 1, abort, 154);
+        if (ok) ok = wait_lead<kPair>(p_full + e, (G >> 1) & 1, abort, 153);
+        if (!ok) break;
         for (int b = 0; b < nb && ok; ++b) {
           const int pos = vs + 2 * pc.t + b, st = pos % M::kV;
           if (!reuse) ok = wait_lead<kPair>(v_full + st, (pos / M::kV) & 1, abort, 155);
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           ++un;
           if (!keep) vs += pc.n;
         }
-        pc.next_step(p);
+        pc = ahead;
       }
       // every product issued has completed before the TMEM is released
       if constexpr (kPair)
