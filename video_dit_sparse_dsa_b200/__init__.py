@@ -555,39 +555,44 @@ def _dtype_of(t: torch.Tensor, name: str) -> int:
 class _On:
     """Runs a call on a tensor's device and on ``stream`` (default: that device's current
     stream).  Scratch taken here is tied to that stream, so its memory is not reused while the
-    call's kernels run."""
+    call's kernels run.  (The raw stream and device lookups: a Stream object and a device guard
+    cost a small call more host time than its kernel takes.)"""
+    __slots__ = ("device", "index", "stream", "guard", "ptr", "other")
 
     def __init__(self, t: torch.Tensor, stream):
         if not t.is_cuda:
             raise ValueError("tensors must be CUDA tensors")
-        self.device = t.device
-        self.guard = torch.cuda.device(t.device)
-        self.stream = stream
+        self.device, self.index, self.stream = t.device, t.get_device(), stream
 
     def __enter__(self):
-        self.guard.__enter__()
-        self.handle = _stream(self.stream)
-        self.ptr = ctypes.c_void_p(self.handle)
+        self.guard = None
+        if torch._C._cuda_getDevice() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        own = torch._C._cuda_getCurrentRawStream(self.index)
+        self.ptr = own if self.stream is None else _stream(self.stream)
+        self.other = self.ptr != own
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
     def scratch(self, n_bytes: int):
         if n_bytes == 0:
             return None
-        t = torch.empty(n_bytes, dtype=torch.uint8, device=self.device)
-        self.keep(t)
+        return self.keep(torch.empty(n_bytes, dtype=torch.uint8, device=self.device))
+
+    def keep(self, t: torch.Tensor) -> torch.Tensor:
+        """A tensor allocated by the call on the current stream, used on ``stream``."""
+        if self.other:
+            t.record_stream(torch.cuda.ExternalStream(self.ptr, device=self.device) if self.ptr else
+                            torch.cuda.default_stream(self.device))
         return t
 
-    def keep(self, *tensors):
-        """Tensors allocated by the call on the current stream, used on ``stream``."""
-        if self.handle != torch.cuda.current_stream(self.device).cuda_stream:
-            s = torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else \
-                torch.cuda.default_stream(self.device)
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(s)
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _like(t: torch.Tensor, name: str, ref: torch.Tensor, shape=None, dtype=None):
@@ -595,51 +600,44 @@ def _like(t: torch.Tensor, name: str, ref: torch.Tensor, shape=None, dtype=None)
         raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
 
 
 def _ws(ws: Optional[torch.Tensor], n_bytes: int, on: _On, ref: torch.Tensor):
     if ws is None:
-        ws = on.scratch(n_bytes)
-    elif ws.device != ref.device or not ws.is_contiguous():
+        return on.scratch(n_bytes), n_bytes
+    if ws.device != ref.device or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {ref.device}")
-    return ws, 0 if ws is None else ws.numel() * ws.element_size()
+    return ws, ws.numel() * ws.element_size()
 
 
 def _rows_view(t: torch.Tensor, name: str) -> View:
     """A [B, heads, rows, d] tensor as dsa_view_t."""
-    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the channels must be contiguous")
-    v = View()
-    v.data = t.data_ptr()
-    for a in range(3):
-        v.stride[a] = t.stride(a)
-    return v
+    return View(t.data_ptr(), s[:3])
 
 
 def _cross(q, k, v, kv_len, scale) -> Cross:
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B, heads, Lq, d], k and v [B, kv_heads, Lk, d]")
     B, heads, Lq, d = q.shape
-    kv_heads, Lk = k.shape[1], k.shape[2]
+    _, kv_heads, Lk, _ = k.shape
     _like(k, "k", q, (B, kv_heads, Lk, d), q.dtype)
     _like(v, "v", q, k.shape, q.dtype)
     if kv_len is not None:
         _like(kv_len, "kv_len", q, (B,), torch.int32)
         if not kv_len.is_contiguous():
             raise ValueError("kv_len must be contiguous")
-    p = Cross()
-    p.B, p.heads, p.kv_heads, p.d, p.Lq, p.Lk = B, heads, kv_heads, d, Lq, Lk
-    p.scale = float(1.0 / math.sqrt(d)) if scale is None else float(scale)
-    p.dtype = _dtype_of(q, "q")
-    return p
+    return Cross(B, heads, kv_heads, d, Lq, Lk, 1.0 / math.sqrt(d) if scale is None else scale, _dtype_of(q, "q"))
 
 
-def _out_like(t: torch.Tensor, name: str, ref: torch.Tensor) -> torch.Tensor:
+def _out_like(t: Optional[torch.Tensor], name: str, ref: torch.Tensor, on: _On) -> torch.Tensor:
     """`t`, or a new tensor of ref's shape and dimension order."""
     if t is None:
-        return torch.empty_like(ref)
+        return on.keep(torch.empty_like(ref))
     _like(t, name, ref, ref.shape, ref.dtype)
     return t
 
@@ -658,19 +656,15 @@ def forward_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Opt
     lib = load_library()
     p = _cross(q, k, v, kv_len, scale)
     with _On(q, stream) as on:
-        new_out, new_lse = out is None, lse is None
-        out = _out_like(out, "out", q)
-        if new_lse:
-            lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        out = _out_like(out, "out", q, on)
+        if lse is None:
+            lse = on.keep(torch.empty(q.shape[:3], dtype=torch.float32, device=q.device))
         _like(lse, "lse", q, q.shape[:3], torch.float32)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
         ws, n_ws = _ws(ws, cross_workspace_size(p), on, q)
-        on.keep(out if new_out else None, lse if new_lse else None)
-        views = [_rows_view(t, n) for t, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"))]
-        r = [ctypes.byref(x) for x in views]
-        _check(lib.dsa_fwd_cross(ctypes.byref(p), r[0], r[1], r[2], _ptr(kv_len), r[3], _ptr(lse), _ptr(ws), n_ws,
-                                 on.ptr), "dsa_fwd_cross")
+        _check(lib.dsa_fwd_cross(p, _rows_view(q, "q"), _rows_view(k, "k"), _rows_view(v, "v"), _addr(kv_len),
+                                 _rows_view(out, "out"), lse.data_ptr(), _addr(ws), n_ws, on.ptr), "dsa_fwd_cross")
     return out, lse
 
 
@@ -687,15 +681,11 @@ def backward_cross(q, k, v, out, lse, dout, kv_len: Optional[torch.Tensor] = Non
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
     with _On(q, stream) as on:
-        fresh = [g is None for g in (dq, dk, dv)]
-        dq, dk, dv = _out_like(dq, "dq", q), _out_like(dk, "dk", k), _out_like(dv, "dv", v)
+        dq, dk, dv = _out_like(dq, "dq", q, on), _out_like(dk, "dk", k, on), _out_like(dv, "dv", v, on)
         ws, n_ws = _ws(ws, cross_workspace_size(p, backward=True), on, q)
-        on.keep(*(g for g, f in zip((dq, dk, dv), fresh) if f))
-        names = ("q", "k", "v", "out", "dout", "dq", "dk", "dv")
-        views = [_rows_view(t, n) for t, n in zip((q, k, v, out, dout, dq, dk, dv), names)]
-        r = [ctypes.byref(x) for x in views]
-        _check(lib.dsa_bwd_cross(ctypes.byref(p), r[0], r[1], r[2], r[3], _ptr(lse), r[4], _ptr(kv_len), r[5], r[6],
-                                 r[7], _ptr(ws), n_ws, on.ptr), "dsa_bwd_cross")
+        _check(lib.dsa_bwd_cross(p, _rows_view(q, "q"), _rows_view(k, "k"), _rows_view(v, "v"), _rows_view(out, "out"),
+                                 lse.data_ptr(), _rows_view(dout, "dout"), _addr(kv_len), _rows_view(dq, "dq"),
+                                 _rows_view(dk, "dk"), _rows_view(dv, "dv"), _addr(ws), n_ws, on.ptr), "dsa_bwd_cross")
     return dq, dk, dv
 
 
@@ -720,23 +710,21 @@ def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0,
         on.keep(table)
         i3, d3 = ctypes.c_int32 * 3, ctypes.c_double * 3
         _check(lib.dsa_rope_table(i3(*(int(g) for g in grid)), i3(*axes), d3(*(float(x) for x in start)),
-                                  d3(*(float(x) for x in step)), float(theta), _ptr(table), on.ptr), "dsa_rope_table")
+                                  d3(*(float(x) for x in step)), float(theta), table.data_ptr(), on.ptr),
+               "dsa_rope_table")
     return table
 
 
 def _grid_view(t: torch.Tensor, name: str) -> View:
     """A [B, heads, T, H, W, d] tensor whose (T, H, W) are one token dimension."""
-    B, h, T, H, W, d = t.shape
-    if t.numel() > 0 and d > 1 and t.stride(5) != 1:
+    _, _, T, H, W, d = t.shape
+    sb, sh, st, sy, sx, sd = t.stride()
+    if sd != 1 and d > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the channels must be contiguous")
-    token = next((t.stride(a) // n for a, n in ((4, 1), (3, W), (2, H * W)) if t.shape[a] > 1), 0)
-    for a, n in ((4, 1), (3, W), (2, H * W)):
-        if t.shape[a] > 1 and t.stride(a) != n * token:
-            raise ValueError(f"{name}: (T, H, W) must be one dimension of tokens in raster order")
-    v = View()
-    v.data = t.data_ptr()
-    v.stride[0], v.stride[1], v.stride[2] = t.stride(0), t.stride(1), token
-    return v
+    token = sx if W > 1 else sy if H > 1 else st if T > 1 else 0
+    if (H > 1 and sy != W * token) or (T > 1 and st != H * W * token):
+        raise ValueError(f"{name}: (T, H, W) must be one dimension of tokens in raster order")
+    return View(t.data_ptr(), (sb, sh, token))
 
 
 def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: Sequence[int],
@@ -751,41 +739,42 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: 
     if q.dim() != 6:
         raise ValueError("q must be [B, heads, T, H, W, d]")
     axes = _axes(axes)
-    p = Rope()
-    p.B, p.heads, p.T, p.H, p.W, p.d = q.shape
-    for a in range(3):
-        p.axes[a] = axes[a]
-    p.interleaved, p.inverse = int(bool(interleaved)), int(bool(inverse))
-    p.dtype = _dtype_of(q, "q")
+    B, heads, T, H, W, d = q.shape
+    p = Rope(B, heads, d, T, H, W, tuple(axes), 1 if interleaved else 0, 1 if inverse else 0, _dtype_of(q, "q"))
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    n = p.T * (axes[0] // 2) + p.H * (axes[1] // 2) + p.W * (axes[2] // 2)
-    _like(table, "table", q, (n, 2), torch.float32)
+    _like(table, "table", q, (T * (axes[0] // 2) + H * (axes[1] // 2) + W * (axes[2] // 2), 2), torch.float32)
     if not table.is_contiguous():
         raise ValueError("table must be contiguous")
+
+    def result(x, y, name):
+        _like(x, name, q, q.shape, q.dtype)
+        if y is None:
+            return on.keep(torch.empty(x.shape, dtype=x.dtype, device=x.device))
+        _like(y, name + "_out", q, q.shape, q.dtype)
+        return y
+
     with _On(q, stream) as on:
-        refs, outs = [], []
-        for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-            if x is None:
-                refs += [None, None]
-                outs.append(None)
-                continue
-            _like(x, name, q, q.shape, q.dtype)
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-                on.keep(y)
-            _like(y, name + "_out", q, q.shape, q.dtype)
-            refs += [ctypes.byref(_grid_view(x, name)), ctypes.byref(_grid_view(y, name + "_out"))]
-            outs.append(y)
-        _check(lib.dsa_rope(ctypes.byref(p), _ptr(table), *refs, on.ptr), "dsa_rope")
-    return outs[0], outs[1]
+        q_out = result(q, q_out, "q")
+        kv = ko = None
+        if k is not None:
+            k_out = result(k, k_out, "k")
+            kv, ko = _grid_view(k, "k"), _grid_view(k_out, "k_out")
+        _check(lib.dsa_rope(p, table.data_ptr(), _grid_view(q, "q"), _grid_view(q_out, "q_out"), kv, ko, on.ptr),
+               "dsa_rope")
+    return q_out, k_out
 
 
 def _rows(t: torch.Tensor, name: str):
     """(rows, C, row stride) of a [..., C] tensor whose leading dimensions are one of rows."""
-    if t.dim() == 0 or (t.shape[-1] > 1 and t.numel() > 0 and t.stride(-1) != 1):
+    if t.dim() == 0:
+        raise ValueError(f"{name}: a tensor of rows has at least one dimension")
+    C = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // C if C else 0), C, C
+    if C > 1 and t.numel() > 0 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the channels must be contiguous")
-    C, rows, ld = t.shape[-1], 1, 0
+    rows, ld = 1, 0
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n != 1 and t.numel() > 0:
             if rows > 1 and s != rows * ld:
@@ -798,20 +787,18 @@ def _rows(t: torch.Tensor, name: str):
 
 def _norm(x: torch.Tensor, weight, eps: float):
     rows, C, ld = _rows(x, "x")
-    p = Norm()
-    p.rows, p.C, p.eps, p.dtype = rows, C, float(eps), _dtype_of(x, "x")
     if weight is not None:
         _like(weight, "weight", x, (C,), x.dtype)
         if not weight.is_contiguous():
             raise ValueError("weight must be contiguous")
-    return p, ld
+    return Norm(rows, C, eps, _dtype_of(x, "x")), ld
 
 
 def _contiguous_out(t, name: str, ref: torch.Tensor, on: _On, dtype=None):
+    dtype = dtype or ref.dtype
     if t is None:
-        t = torch.empty(ref.shape, dtype=dtype or ref.dtype, device=ref.device)
-        on.keep(t)
-    _like(t, name, ref, ref.shape, dtype or ref.dtype)
+        return on.keep(torch.empty(ref.shape, dtype=dtype, device=ref.device))
+    _like(t, name, ref, ref.shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
@@ -849,18 +836,17 @@ def _rms_norm(x, weight, eps, residual, out, scales, sum_out, dtype8, stream):
     with _On(x, stream) as on:
         y = _contiguous_out(out, "out", x, on, dtype8)
         h = _contiguous_out(sum_out, "sum_out", x, on) if residual is not None else None
-        args = [ctypes.byref(p), _ptr(x), x_ld, _ptr(residual), r_ld, _ptr(weight), _ptr(y)]
+        args = (p, x.data_ptr(), x_ld, _addr(residual), r_ld, _addr(weight), y.data_ptr())
         if dtype8 is None:
-            _check(lib.dsa_rmsnorm(*args, _ptr(h), on.ptr), "dsa_rmsnorm")
+            _check(lib.dsa_rmsnorm(*args, _addr(h), on.ptr), "dsa_rmsnorm")
         else:
             shape = x.shape[:-1] + ((p.C + 127) // 128,)
             if scales is None:
-                scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-                on.keep(scales)
+                scales = on.keep(torch.empty(shape, dtype=torch.float32, device=x.device))
             _like(scales, "scales", x, shape, torch.float32)
             if not scales.is_contiguous():
                 raise ValueError("scales must be contiguous")
-            _check(lib.dsa_rmsnorm_fp8(*args, _ptr(scales), _ptr(h), on.ptr), "dsa_rmsnorm_fp8")
+            _check(lib.dsa_rmsnorm_fp8(*args, scales.data_ptr(), _addr(h), on.ptr), "dsa_rmsnorm_fp8")
     return y, x if h is None else h, scales
 
 
@@ -883,10 +869,10 @@ def rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], dy: torch
         dx = _contiguous_out(dx, "dx", h, on)
         if weight is not None:
             dweight = _contiguous_out(dweight, "dweight", weight, on)
-        size = int(lib.dsa_rmsnorm_bwd_workspace_size(ctypes.byref(p))) if weight is not None else 0
+        size = int(lib.dsa_rmsnorm_bwd_workspace_size(p)) if weight is not None else 0
         ws, n_ws = _ws(ws, size, on, h)
-        _check(lib.dsa_rmsnorm_bwd(ctypes.byref(p), _ptr(h), h_ld, _ptr(weight), _ptr(dy), dy_ld, _ptr(dh), dh_ld,
-                                   _ptr(dx), _ptr(dweight), _ptr(ws), n_ws, on.ptr), "dsa_rmsnorm_bwd")
+        _check(lib.dsa_rmsnorm_bwd(p, h.data_ptr(), h_ld, _addr(weight), dy.data_ptr(), dy_ld, _addr(dh), dh_ld,
+                                   dx.data_ptr(), _addr(dweight), _addr(ws), n_ws, on.ptr), "dsa_rmsnorm_bwd")
     return dx, dweight
 
 
