@@ -70,7 +70,8 @@ struct CrossPlan {
   int chunks;             // 128-key chunks of Lk
   int64_t rows;           // B * heads * Lq
   int split_q;            // parts of the keys (forward, and dQ)
-  int split_kv;           // parts of the query chunks (dK, dV)
+  int per_unit;           // 64-row query chunks of a 128-key unit (dK, dV)
+  int64_t kv_units;       // such units, at most
   int Lp;                 // Lq rounded up to 64
 };
 
@@ -107,23 +108,10 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
   }
   // more than one 128-row tile per head, and not in parts: a cluster of two CTAs per 256 rows
   c->pair = c->split_q == 1 && p->Lq > 128;
-  // dK, dV: a unit is 128 keys of one kv head over every query chunk of its group; the query
-  // chunks are cut so that the units fill whole waves of SMs (the smallest estimate of waves x
-  // (chunks of a part + 4 for the part's own start and end), parts of at least 8 chunks).
-  const int64_t kv_units = slices * (c->chunks > 0 ? c->chunks : 1);
-  const int64_t q_chunks = static_cast<int64_t>(c->group) * (c->Lp / 64);
-  if (kv_units > INT32_MAX / 64 || q_chunks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  c->split_kv = 1;
-  int64_t best = -1;
-  for (int64_t s = 1; s <= 64 && (s == 1 || s * 8 <= q_chunks); ++s) {
-    const int64_t per = (q_chunks + s - 1) / s, waves = (kv_units * s + kPlanSms - 1) / kPlanSms;
-    const int64_t cost = waves * (per + 4);
-    if (best < 0 || cost < best) {
-      best = cost;
-      c->split_kv = static_cast<int>((q_chunks + per - 1) / (per > 0 ? per : 1));
-      if (c->split_kv < 1) c->split_kv = 1;
-    }
-  }
+  c->kv_units = slices * c->chunks;
+  const int64_t per_unit = static_cast<int64_t>(c->group) * (c->Lp / 64);
+  if (c->kv_units > INT32_MAX || per_unit > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  c->per_unit = static_cast<int>(per_unit);
   return DSA_OK;
 }
 
@@ -143,7 +131,6 @@ CrossWorkspace cross_workspace(const dsa_cross_t* p, const CrossPlan& c, int kin
     off += round_up(sizeof(float) * floats, kAlign);
     return at;
   };
-  const size_t kv_rows = static_cast<size_t>(p->B) * p->kv_heads * p->Lk;
   if (kind == DSA_WS_FWD) {
     if (c.split_q > 1) {
       w.part_o = take(static_cast<size_t>(c.split_q) * c.rows * 128);
@@ -153,10 +140,9 @@ CrossWorkspace cross_workspace(const dsa_cross_t* p, const CrossPlan& c, int kin
     w.delta = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
     w.lse_pad = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
     if (c.split_q > 1) w.dq_part = take(static_cast<size_t>(c.split_q) * c.rows * 128);
-    if (c.split_kv > 1) {
-      w.dk_part = take(c.split_kv * kv_rows * 128);
-      w.dv_part = take(c.split_kv * kv_rows * 128);
-    }
+    // the pieces of the 128-key units that are cut between CTAs: at most two per CTA
+    w.dk_part = take(2 * kPlanSms * 128 * 128);
+    w.dv_part = take(2 * kPlanSms * 128 * 128);
   }
   w.bytes = off;
   return w;
@@ -217,11 +203,9 @@ dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, con
   return launch_status();
 }
 
-dsa_status_t launch_combine(const dsa::CrossCombineParams& cp, cudaStream_t s) {
-  const int64_t threads = static_cast<int64_t>(cp.B) * cp.heads * cp.L * 32;
-  if (threads == 0) return DSA_OK;
-  const dim3 grid(static_cast<unsigned>((threads + 255) / 256), static_cast<unsigned>(cp.n_out));
-  dsa::cross_combine<<<grid, 256, 0, s>>>(cp);
+dsa_status_t launch_dq_combine(const dsa::CrossDqCombineParams& cp, cudaStream_t s) {
+  const int64_t threads = static_cast<int64_t>(cp.B) * cp.heads * cp.Lq * 32;
+  dsa::cross_dq_combine<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, s>>>(cp);
   return launch_status();
 }
 
@@ -464,38 +448,41 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   if (ws.bytes > 0 && (workspace == nullptr || ws_bytes < ws.bytes || !aligned(workspace, kAlign)))
     return DSA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the sums of the parts; with no queries or no keys they write the zero gradients
-  dsa::CrossCombineParams ckv, cq;
-  std::memset(&ckv, 0, sizeof(ckv));
+  dsa::CrossDqCombineParams cq;
   std::memset(&cq, 0, sizeof(cq));
-  ckv.B = cq.B = p->B;
-  ckv.heads = p->kv_heads;
-  ckv.L = p->Lk;
-  ckv.len = kv_len;
-  ckv.part_stride = static_cast<int64_t>(p->B) * p->kv_heads * p->Lk * 128;
-  ckv.n_out = 2;
-  ckv.part[0] = ws.dk_part;
-  ckv.part[1] = ws.dv_part;
-  ckv.scale[0] = p->scale;
-  ckv.scale[1] = 1.f;
+  cq.B = p->B;
   cq.heads = p->heads;
-  cq.L = p->Lq;
-  cq.part_stride = c.rows * 128;
-  cq.n_out = 1;
-  cq.part[0] = ws.dq_part;
-  cq.scale[0] = 1.f;
-  if (p->Lk > 0) {
-    ckv.out[0] = static_cast<__nv_bfloat16*>(dk->data);
-    ckv.out[1] = static_cast<__nv_bfloat16*>(dv->data);
-    copy_strides(ckv.s[0], dk);
-    copy_strides(ckv.s[1], dv);
-  }
+  cq.Lq = p->Lq;
+  cq.part = ws.dq_part;
   if (p->Lq > 0) {
-    cq.out[0] = static_cast<__nv_bfloat16*>(dq->data);
-    copy_strides(cq.s[0], dq);
+    cq.dq = static_cast<__nv_bfloat16*>(dq->data);
+    copy_strides(cq.s, dq);
   }
-  if (p->Lq == 0) return launch_combine(ckv, s);
-  if (p->Lk == 0) return launch_combine(cq, s);
+  if (p->Lk == 0) return p->Lq > 0 ? launch_dq_combine(cq, s) : DSA_OK;  // no keys: dq = 0
+
+  dsa::BwdBf16Params bp;
+  std::memset(&bp, 0, sizeof(bp));
+  bp.dk = static_cast<__nv_bfloat16*>(dk->data);
+  bp.dv = static_cast<__nv_bfloat16*>(dv->data);
+  copy_strides(bp.dk_s, dk);
+  copy_strides(bp.dv_s, dv);
+  bp.scale = p->scale;
+  bp.scale_log2 = p->scale * 1.4426950408889634f;
+  bp.Lk = p->Lk;
+  bp.Nq = p->Lq;
+  bp.dk_part = ws.dk_part;
+  bp.dv_part = ws.dv_part;
+  bp.kv_len = kv_len;
+  bp.B = p->B;
+  bp.kv_heads = p->kv_heads;
+  bp.group = c.group;
+  bp.per_unit = c.per_unit;
+  bp.G1 = bp.G2 = bp.tt = bp.th = bp.tw = bp.T = bp.H = bp.W = bp.KU = bp.QS = bp.n_tiles = bp.n_split = 1;
+  const dim3 kv_grid(static_cast<unsigned>(c.kv_units), 2, 1);
+  if (p->Lq == 0) {  // no queries: dk = dv = 0
+    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(bp, 1);
+    return launch_status();
+  }
 
   dsa::CrossPrepParams pp;
   pp.o = static_cast<const __nv_bfloat16*>(out->data);
@@ -523,23 +510,6 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
       !make_vec_map(&tdel, ws.delta, BH, c.Lp))
     return DSA_ERR_CUDA;
   {
-    dsa::BwdBf16Params bp;
-    std::memset(&bp, 0, sizeof(bp));
-    bp.dk = static_cast<__nv_bfloat16*>(dk->data);
-    bp.dv = static_cast<__nv_bfloat16*>(dv->data);
-    copy_strides(bp.dk_s, dk);
-    copy_strides(bp.dv_s, dv);
-    bp.scale = p->scale;
-    bp.scale_log2 = p->scale * 1.4426950408889634f;
-    bp.Lk = p->Lk;
-    bp.Nq = p->Lq;
-    bp.n_split = c.split_kv;
-    bp.dk_part = ws.dk_part;
-    bp.dv_part = ws.dv_part;
-    bp.part_stride = ckv.part_stride;
-    bp.kv_len = kv_len;
-    bp.kv_heads = p->kv_heads;
-    bp.group = c.group;
     bp.qg = mq[0];
     bp.qk = mq[1];
     bp.qb = mq[2];
@@ -550,59 +520,68 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     bp.kb = mk[2];
     bp.vh = mv[1];
     bp.vb = mv[2];
-    bp.n_units = static_cast<int>(static_cast<int64_t>(p->B) * p->kv_heads * c.chunks * c.split_kv);
-    bp.G1 = bp.G2 = bp.tt = bp.th = bp.tw = bp.T = bp.H = bp.W = bp.KU = bp.QS = bp.n_tiles = 1;
+    // one CTA per SM (two slots of the workspace each), no more than query chunks
     auto kernel = dsa::bwd_bf16_kernel<true, false, true>;
+    const int64_t work = c.kv_units * c.per_unit;
     unsigned grid = 0;
-    st = persistent_grid(kernel, dsa::bwd::kSmemBytes, 0, bp.n_units, &grid);
+    st = persistent_grid(kernel, dsa::bwd::kSmemBytes, 0, work < kPlanSms ? work : kPlanSms, &grid);
     if (st != DSA_OK) return st;
+    // pieces of a CTA's range: whole units, and one cut at either end
+    bp.n_units = static_cast<int>(grid * (work / grid / c.per_unit + 3));
     kernel<<<grid, dsa::bwd::kThreads, dsa::bwd::kSmemBytes, s>>>(tq, tk, tv, tdo, tlse, tdel, tq, tdo, tlse, tdel, bp);
     st = launch_status();
     if (st != DSA_OK) return st;
-    if (c.split_kv > 1) {
-      ckv.n_part = c.split_kv;
-      st = launch_combine(ckv, s);
-      if (st != DSA_OK) return st;
-    }
+    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(bp, static_cast<int>(grid));
+    st = launch_status();
+    if (st != DSA_OK) return st;
   }
-  dsa::BwdDqParams dp;
+  dsa::CrossDqParams dp;
   std::memset(&dp, 0, sizeof(dp));
-  dp.q = static_cast<const __nv_bfloat16*>(q->data);
-  dp.dout = static_cast<const __nv_bfloat16*>(dout->data);
-  dp.dq = static_cast<__nv_bfloat16*>(dq->data);
-  copy_strides(dp.q_s, q);
-  copy_strides(dp.do_s, dout);
-  copy_strides(dp.dq_s, dq);
+  dp.kv_len = kv_len;
+  dp.B = p->B;
+  dp.heads = p->heads;
+  dp.kv_heads = p->kv_heads;
+  dp.group = c.group;
+  dp.Lq = p->Lq;
+  dp.Lk = p->Lk;
+  dp.pk = c.pk;
+  dp.tiles = c.tiles;
+  dp.n_split = c.split_q;
+  dp.n_units = static_cast<int>(c.units * c.split_q);
   dp.lse = ws.lse_pad;
   dp.delta = ws.delta;
   dp.ld_rows = c.Lp;
-  dp.Lq = p->Lq;
-  dp.Lk = p->Lk;
-  dp.n_split = c.split_q;
+  dp.dq = static_cast<__nv_bfloat16*>(dq->data);
+  copy_strides(dp.dq_s, dq);
   dp.dq_part = ws.dq_part;
-  dp.part_stride = c.rows * 128;
-  dp.n_units = static_cast<int>(c.units * c.split_q);
   dp.scale = p->scale;
   dp.scale_log2 = p->scale * 1.4426950408889634f;
-  dp.kv_len = kv_len;
-  dp.kv_heads = p->kv_heads;
-  dp.group = c.group;
-  dp.tiles = c.tiles;
-  dp.pk = c.pk;
+  CUtensorMap uq, udo, udq;
+  int mdq[3];
+  const int box_rows = c.pk > 1 ? p->Lq : 128;
+  if (!make_view_map(&uq, q, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mq) ||
+      !make_view_map(&udo, dout, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mdo) ||
+      !make_view_map(&udq, dq, p->B, p->heads, c.group, p->Lq, 32, 1, mdq))
+    return DSA_ERR_CUDA;
+  dp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;
+  dp.qg = mq[0];
+  dp.qk = mq[1];
+  dp.qb = mq[2];
+  dp.dg = mdo[0];
+  dp.dk = mdo[1];
+  dp.db = mdo[2];
   dp.kh = mk[1];
   dp.kb = mk[2];
   dp.vh = mv[1];
   dp.vb = mv[2];
-  dp.tt = dp.th = dp.tw = dp.T = dp.H = dp.W = dp.S = dp.KS = 1;
-  auto kernel = dsa::bwd_dq_kernel<true, false, true>;
   unsigned grid = 0;
-  st = persistent_grid(kernel, dsa::bdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
+  st = persistent_grid(dsa::cross_dq_kernel, dsa::crossdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
   if (st != DSA_OK) return st;
-  kernel<<<grid, dsa::bdq::kThreads, dsa::bdq::kSmemBytes, s>>>(tk, tv, tk, tv, dp);
+  dsa::cross_dq_kernel<<<grid, dsa::crossdq::kThreads, dsa::crossdq::kSmemBytes, s>>>(uq, udo, tk, tv, udq, dp);
   st = launch_status();
   if (st != DSA_OK || c.split_q == 1) return st;
   cq.n_part = c.split_q;
-  return launch_combine(cq, s);
+  return launch_dq_combine(cq, s);
 }
 
 dsa_status_t dsa_rope_table(const int32_t* grid, const int32_t* axes, const double* start, const double* step,

@@ -52,10 +52,14 @@ struct BwdBf16Params {
   int64_t part_stride;
   // cross mode: the keys are an encoder's states, Lk rows of kv head kvh of batch entry b of
   // which the first kv_len[b] (null: Lk) count; the queries are the Nq rows of each of the
-  // `group` heads that share the kv head; LSE and D are padded to [B * heads, Lp].  With
-  // n_split = 1 dk and dv are written as bf16 through their strides (batch, head, row).
+  // `group` heads that share the kv head; LSE and D are padded to [B * heads, Lp].  The work is
+  // the 64-row query chunks of every unit (128 keys that hold some of kv head, `per_unit` query
+  // chunks each) in one sequence, cut into a range of equal length per CTA.  A unit that lies in
+  // one CTA's range is written as bf16 through the strides (batch, head, row) of dk and dv; of a
+  // unit that is cut, each CTA writes its piece's fp32 sums to slot 2 cta (its range's first
+  // piece) or 2 cta + 1 of dk_part and dv_part (128 x 128 each).
   const int32_t* kv_len;
-  int kv_heads, group;
+  int B, kv_heads, group, per_unit;
   int qb, qk, qg, db, dkv, dg, kb, kh, vb, vh;  // 1, or 0 for a broadcast (stride 0) dimension of q, dO, k, v
   int64_t dk_s[3], dv_s[3];
 };
@@ -122,22 +126,60 @@ struct BwdChunks {
   int row0, c0, nm, nx;
 };
 
-// Cross mode: keys of batch entry b.
-__device__ __forceinline__ int bwd_kv_length(const BwdBf16Params& p, int bh) {
-  return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + bh / p.kv_heads), 0), p.Lk);
+// Cross mode: keys of batch entry b, and its 128-key chunks.
+__device__ __forceinline__ int bwd_kv_length(const BwdBf16Params& p, int b) {
+  return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + b), 0), p.Lk);
 }
 
-template <bool kFlatK, bool kExtra, bool kCross = false>
+__device__ __forceinline__ int bwd_kv_chunks(const BwdBf16Params& p, int b) { return (bwd_kv_length(p, b) + 127) / 128; }
+
+// Cross mode: the CTA's range [lo, hi) of the sequence of query chunks (whole warp).
+struct BwdRange {
+  int64_t lo, hi;
+};
+
+__device__ __forceinline__ BwdRange bwd_range(const BwdBf16Params& p) {
+  int64_t units = 0;
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) units += static_cast<int64_t>(bwd_kv_chunks(p, b)) * p.kv_heads;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
+  const int64_t all = units * p.per_unit;
+  BwdRange r;
+  r.lo = all * blockIdx.x / gridDim.x;
+  r.hi = all * (blockIdx.x + 1) / gridDim.x;
+  return r;
+}
+
+// The k-th piece of the range: its unit (part: 1 where it is not the CTA's first piece) and query
+// chunks; nm = 0 past the end.
+__device__ __forceinline__ void bwd_piece(const BwdBf16Params& p, const BwdRange& r, int k, BwdUnit& x, BwdChunks& q) {
+  const int64_t u0 = r.lo / p.per_unit, v = u0 + k, start = k == 0 ? r.lo : v * p.per_unit;
+  q.row0 = 0;
+  q.nx = 0;
+  q.c0 = static_cast<int>(start - v * p.per_unit);
+  q.nm = static_cast<int>(max(min((v + 1) * p.per_unit, r.hi) - start, static_cast<int64_t>(0)));
+  x.ku = 0;
+  x.part = k > 0;
+  x.bh = x.kt = 0;
+  if (q.nm == 0) return;
+  int64_t rem = v;
+  for (int b = 0; b < p.B; ++b) {
+    const int c = bwd_kv_chunks(p, b);
+    const int64_t n = static_cast<int64_t>(c) * p.kv_heads;
+    if (rem < n) {
+      x.bh = b * p.kv_heads + static_cast<int>(rem / c);
+      x.kt = static_cast<int>(rem % c);
+      return;
+    }
+    rem -= n;
+  }
+}
+
+template <bool kFlatK, bool kExtra>
 __device__ __forceinline__ BwdChunks bwd_chunks(const BwdBf16Params& p, const BwdUnit& x) {
   BwdChunks q;
   const int nx = kExtra ? (p.Lxq + 63) / 64 : 0;
-  if constexpr (kCross) {  // the group's heads in turn, each head's rows in 64-row chunks
-    const int nqm = p.group * ((p.Nq + 63) / 64), per = (nqm + p.n_split - 1) / p.n_split;
-    q.row0 = 0;
-    q.c0 = x.part * per;
-    q.nm = 128 * x.kt < bwd_kv_length(p, x.bh) ? max(min(per, nqm - q.c0), 0) : 0;
-    q.nx = 0;
-  } else if constexpr (kFlatK) {
+  if constexpr (kFlatK) {
     const int nqm = (p.Nq + 63) / 64, per = (nqm + p.n_split - 1) / p.n_split;
     q.row0 = 0;
     q.c0 = x.part * per;
@@ -342,6 +384,17 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  BwdRange range = {0, 0};
+  if constexpr (kCross) range = bwd_range(p);
+  // the CTA's unit u: (batch, head) and keys, and its query chunks
+  auto unit_of = [&](int u, BwdUnit& x, BwdChunks& q) {
+    if constexpr (kCross) {
+      bwd_piece(p, range, (u - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x), x, q);
+    } else {
+      x = bwd_unit<kFlatK>(p, u);
+      q = bwd_chunks<kFlatK, kExtra>(p, x);
+    }
+  };
   const uint32_t tDV = tmem, tDK = tmem + 128, tS = tmem + 256, tDP = tmem + 384;
 
   if (warp == kProducerWarp) {
@@ -350,8 +403,9 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       int ld = 0, uc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        const BwdUnit x = bwd_unit<kFlatK>(p, u);
-        const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, x);
+        BwdUnit x;
+        BwdChunks qc;
+        unit_of(u, x, qc);
         const int bh = x.bh, n = qc.nm + qc.nx;
         const int b = kCross ? bh / p.kv_heads : 0, kvh = kCross ? bh % p.kv_heads : 0;
         if (n == 0) continue;
@@ -426,7 +480,9 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       int ld = 0, uc = 0, sc = 0, pc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, bwd_unit<kFlatK>(p, u));
+        BwdUnit x;
+        BwdChunks qc;
+        unit_of(u, x, qc);
         const int n = qc.nm + qc.nx;
         if (n == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(kv_full, uc & 1, abort, 60));
@@ -493,11 +549,13 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
     int cc = 0, ld = 0, uc = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-      const BwdUnit x = bwd_unit<kFlatK>(p, u);
-      const BwdChunks qc = bwd_chunks<kFlatK, kExtra, kCross>(p, x);
+      BwdUnit x;
+      BwdChunks qc;
+      unit_of(u, x, qc);
       const int n = qc.nm + qc.nx;
+      if (kCross && n == 0) break;  // past the CTA's range
       // flat keys: this thread's key row may lie past the end (zeros, no gradient)
-      const bool k_ok = !kFlatK || 128 * x.kt + m < (kCross ? bwd_kv_length(p, x.bh) : p.Lk);
+      const bool k_ok = !kFlatK || 128 * x.kt + m < (kCross ? bwd_kv_length(p, x.bh / p.kv_heads) : p.Lk);
       for (int c = 0; c < n; ++c, ++cc, ++ld) {
         const int nvq = bwd_qvalid<kFlatK, kExtra, kCross>(p, qc, c) - 32 * h;  // valid queries of this half
         const bool masked = !k_ok || nvq < 32;  // P = dS = 0 for missing keys and queries
@@ -569,7 +627,9 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       }
       float4* dstp = nullptr;
       if constexpr (kFlatK) {
-        const int64_t o = static_cast<int64_t>(x.part) * p.part_stride + (static_cast<int64_t>(x.bh) * p.Lk + ktok) * 128;
+        const int64_t o = kCross ? (2 * static_cast<int64_t>(blockIdx.x) + x.part) * 16384 + m * 128
+                                 : static_cast<int64_t>(x.part) * p.part_stride +
+                                       (static_cast<int64_t>(x.bh) * p.Lk + ktok) * 128;
         dstp = reinterpret_cast<float4*>((h ? p.dk_part : p.dv_part) + o);
       }
       if (n > 0) {
@@ -593,7 +653,7 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
             for (int j = 0; j < 32; ++j) a[j] = 0u;
           }
         }
-        if (kFlatK && (!kCross || p.n_split > 1)) {
+        if (kFlatK && (!kCross || n < p.per_unit)) {
           if (k_row_ok && (!kCross || k_ok)) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)

@@ -83,14 +83,6 @@ struct BwdDqParams {
   float* dq_part;
   int64_t part_stride;
   int ld_rows;              // flat mode: rows per (batch, head) of lse and delta (>= Lq)
-  // cross mode (with the flat mode's Lq, Lk, n_split, ld_rows): the keys are an encoder's
-  // states, of which the first kv_len[b] (null: Lk) of batch entry b count; a kv head's
-  // `group` heads' rows make `tiles` units of 128 rows (pk > 1: pk heads of Lq rows each in
-  // one unit).  q, dout and (n_split = 1) dq have strides (batch, head, row).
-  const int32_t* kv_len;
-  int kv_heads, group, tiles, pk;
-  int kb, kh, vb, vh;       // 1, or 0 for a broadcast (stride 0) dimension of k, v
-  int64_t q_s[3], do_s[3], dq_s[3];
 };
 
 namespace bdq {
@@ -137,16 +129,6 @@ __device__ __forceinline__ void issue_dq(uint32_t d_tmem, uint32_t ds_tmem, uint
                 accumulate || kk > 0);
 }
 
-// issue_dq over the first 16 * n16 keys of the step.
-__device__ __forceinline__ void issue_dq_keys(uint32_t d_tmem, uint32_t ds_tmem, uint64_t k_desc, bool accumulate,
-                                              int n16) {
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    if (kk < n16)
-      mma_ts_warp(d_tmem, ds_tmem + 64 * (kk >> 2) + 8 * (kk & 3), desc_add(k_desc, kk * 2048), kIdescDQ,
-                  accumulate || kk > 0);
-}
-
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, site));
 }
@@ -158,15 +140,10 @@ struct Unit {
 // Window / list form: units run (batch*head, tile, chunk).  Flat form: (batch*head, part,
 // query chunk), so the query chunks that read the same keys are neighbours; tile = the query
 // chunk, sub = the part.
-// Cross form: bh counts kv heads, the units of a kv head run (part, tile).
-template <bool kFlat, bool kCross = false>
+template <bool kFlat>
 __device__ __forceinline__ Unit decode(const BwdDqParams& p, int u) {
   Unit x;
-  if constexpr (kCross) {
-    x.tile = u % p.tiles;
-    x.sub = u / p.tiles % p.n_split;
-    x.bh = u / p.tiles / p.n_split;
-  } else if constexpr (kFlat) {
+  if constexpr (kFlat) {
     const int nq = (p.Lq + 127) / 128, per_bh = nq * p.n_split;
     x.bh = u / per_bh;
     const int rem = u % per_bh;
@@ -188,16 +165,12 @@ struct Chunks {
   int c0, nm, nx;
 };
 
-__device__ __forceinline__ int kv_length(const BwdDqParams& p, int bh) {
-  return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + bh / p.kv_heads), 0), p.Lk);
-}
-
-template <bool kFlat, bool kExtra, bool kCross = false>
+template <bool kFlat, bool kExtra>
 __device__ __forceinline__ Chunks unit_chunks(const BwdDqParams& p, const Unit& x, int n_list) {
   Chunks k;
   const int nx = kExtra ? (p.Lx + 127) / 128 : 0;
   if constexpr (kFlat) {
-    const int n_main = ((kCross ? kv_length(p, x.bh) : p.Lk) + 127) / 128, per = (n_main + p.n_split - 1) / p.n_split;
+    const int n_main = (p.Lk + 127) / 128, per = (n_main + p.n_split - 1) / p.n_split;
     k.c0 = x.sub * per;
     k.nm = max(min(per, n_main - k.c0), 0);
     k.nx = x.sub == 0 ? nx : 0;
@@ -211,10 +184,9 @@ __device__ __forceinline__ Chunks unit_chunks(const BwdDqParams& p, const Unit& 
 
 // Keys present in local chunk j: the last chunk of a flat sequence and of the extra keys can
 // be partial.
-template <bool kFlat, bool kExtra, bool kCross = false>
-__device__ __forceinline__ int chunk_valid(const BwdDqParams& p, const Unit& x, const Chunks& k, int j) {
+template <bool kFlat, bool kExtra>
+__device__ __forceinline__ int chunk_valid(const BwdDqParams& p, const Chunks& k, int j) {
   if (!kFlat && !kExtra) return 128;
-  if constexpr (kCross) return min(kv_length(p, x.bh) - 128 * (k.c0 + j), 128);
   if (j < k.nm) return kFlat ? min(p.Lk - 128 * (k.c0 + j), 128) : 128;
   return min(p.Lx - 128 * (j - k.nm), 128);
 }
@@ -243,11 +215,8 @@ __device__ __forceinline__ int64_t chunk_token(const BwdDqParams& p, int tile, i
 
 // kFlat: flat query rows over flat key rows in parts (rank-3 maps; rows past the end load as
 // zeros, keys past the end are masked, rows past the end are not written).  kExtra: the
-// extra keys (maps tmKx, tmVx) follow every unit's own.  kCross (with kFlat): an encoder's
-// states as the keys (rank-4 maps), the rows of q, dO and dQ through strides.  The rows past the
-// last key of a batch entry may hold anything: their dS is set to zero rather than computed, and
-// those that its product still reads (up to the next multiple of 16) are zeroed in shared memory.
-template <bool kFlat, bool kExtra, bool kCross = false>
+// extra keys (maps tmKx, tmVx) follow every unit's own.
+template <bool kFlat, bool kExtra>
 __global__ void __launch_bounds__(bdq::kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const __grid_constant__ CUtensorMap tmKx, const __grid_constant__ CUtensorMap tmVx, BwdDqParams p) {
@@ -322,10 +291,10 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
         int ld = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-          const Unit x = decode<kFlat, kCross>(p, u);
+          const Unit x = decode<kFlat>(p, u);
           int n_list = 0;
           const int32_t* kv = kFlat ? nullptr : unit_keys(p, x.bh, x.tile, n_list);
-          const Chunks ck = unit_chunks<kFlat, kExtra, kCross>(p, x, n_list);
+          const Chunks ck = unit_chunks<kFlat, kExtra>(p, x, n_list);
           const int n_steps = ck.nm + ck.nx;
           if (n_steps == 0) continue;  // no keys: the elementwise warps write dQ = 0
           const int n_st = is_k ? kKStages : kVStages;
@@ -336,12 +305,7 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
             uint64_t* full = (is_k ? k_full : v_full) + st;
             uint8_t* dst = smem + (is_k ? kOffK : kOffV) + st * kKTileBytes;
             mbar_arrive_expect_tx(full, kKTileBytes);
-            if constexpr (kCross) {
-              const CUtensorMap* m = is_k ? &tmK : &tmV;
-              const int head = x.bh % p.kv_heads * (is_k ? p.kh : p.vh), b = x.bh / p.kv_heads * (is_k ? p.kb : p.vb);
-              tma_load_4d(dst, m, full, 0, 128 * (ck.c0 + j), head, b);
-              tma_load_4d(dst + kKHalfBytes, m, full, 64, 128 * (ck.c0 + j), head, b);
-            } else if (kExtra && j >= ck.nm) {  // extra keys (rows past Lx load as zeros and are masked)
+            if (kExtra && j >= ck.nm) {  // extra keys (rows past Lx load as zeros and are masked)
               const CUtensorMap* m = is_k ? &tmKx : &tmVx;
               tma_load_3d(dst, m, full, 0, 128 * (j - ck.nm), x.bh);
               tma_load_3d(dst + kKHalfBytes, m, full, 64, 128 * (j - ck.nm), x.bh);
@@ -369,10 +333,9 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
         int n_list = 0;
-        const Unit x = decode<kFlat, kCross>(p, u);
+        const Unit x = decode<kFlat>(p, u);
         if constexpr (!kFlat) unit_keys(p, x.bh, x.tile, n_list);
-        const Chunks ck = unit_chunks<kFlat, kExtra, kCross>(p, x, n_list);
-        const int n_steps = ck.nm + ck.nx;
+        const int n_steps = unit_chunks<kFlat, kExtra>(p, x, n_list).nm + unit_chunks<kFlat, kExtra>(p, x, n_list).nx;
         if (n_steps == 0) continue;
         ok = warp_wait(qa_full, uc & 1, abort, 120);
         if (!ok) break;
@@ -381,16 +344,6 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
         auto issue_s = [&](int G) -> bool {
           if (G >= 1 && !warp_wait(s_read, (G - 1) & 1, abort, 126)) return false;
           if (!warp_wait(k_full + ks % kKStages, (ks / kKStages) & 1, abort, 121)) return false;
-          if constexpr (kCross) {
-            const int keys = chunk_valid<kFlat, kExtra, kCross>(p, x, ck, G - g);
-            if (keys & 15) {  // rows the dQ product reads against dS = 0 (0 * NaN is NaN)
-              const int pad_rows = 16 - (keys & 15);
-              const uint32_t k0 = sbase + kOffK + (ks % kKStages) * kKTileBytes + (lane >> 3 & 1) * kKHalfBytes + (lane & 7) * 16;
-              for (int rr = lane >> 4; rr < pad_rows; rr += 2) st_shared_v4(k0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
           tc_fence_after();
           issue_qk(tmem + kColS, tmem + kColQ, desc_add(dKk, (ks % kKStages) * kKTileBytes));
           mma_commit_warp(s_full);
@@ -412,11 +365,7 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
           if (!warp_wait(ds_full, G & 1, abort, 124)) return false;
           if (first && !warp_wait(dq_free, (uc & 1) ^ 1, abort, 125)) return false;
           tc_fence_after();
-          if constexpr (kCross)
-            issue_dq_keys(tmem + kColDQ, tmem + kColDP, desc_add(dKm, (kd % kKStages) * kKTileBytes), !first,
-                          (chunk_valid<kFlat, kExtra, kCross>(p, x, ck, G - g) + 15) >> 4);
-          else
-            issue_dq(tmem + kColDQ, tmem + kColDP, desc_add(dKm, (kd % kKStages) * kKTileBytes), !first);
+          issue_dq(tmem + kColDQ, tmem + kColDP, desc_add(dKm, (kd % kKStages) * kKTileBytes), !first);
           mma_commit_warp(k_empty + kd % kKStages);
           ++kd;
           return true;
@@ -449,41 +398,21 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
     int g = 0, uc = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-      const Unit x = decode<kFlat, kCross>(p, u);
+      const Unit x = decode<kFlat>(p, u);
       int n_list = 0;
       if constexpr (!kFlat) unit_keys(p, x.bh, x.tile, n_list);
-      const Chunks ck = unit_chunks<kFlat, kExtra, kCross>(p, x, n_list);
+      const Chunks ck = unit_chunks<kFlat, kExtra>(p, x, n_list);
       const int n_steps = ck.nm + ck.nx;
       // the row: a token of the tile (window / list form) or of the flat query sequence (rows
       // past Lq of the last chunk have no gradient; their Q and dO load as zeros)
-      int64_t qrow = kFlat ? 128 * static_cast<int64_t>(x.tile) + r : chunk_token(p, x.tile, x.sub, r);
-      int gh = 0;  // cross mode: head within the group
-      bool row_ok = !kFlat || qrow < p.Lq;
-      if constexpr (kCross) {
-        if (p.pk > 1) {
-          gh = x.tile * p.pk + r / p.Lq;
-          qrow = r % p.Lq;
-          row_ok = r < p.pk * p.Lq && gh < p.group;
-        } else {
-          const int per_head = (p.Lq + 127) / 128;
-          gh = x.tile / per_head;
-          qrow = 128 * (x.tile % per_head) + r;
-          row_ok = qrow < p.Lq;
-        }
-        if (!row_ok) gh = 0;
-      }
-      const int64_t bh = kCross ? static_cast<int64_t>(x.bh) * p.group + gh : x.bh;  // (batch, head) of the row
-      const int64_t row = bh * (kFlat ? p.Lq : p.N) + (row_ok ? qrow : 0);
-      auto at = [&](const int64_t* s) -> int64_t {  // element offset of the row
-        if constexpr (!kCross) return row * 128;
-        const int64_t head = static_cast<int64_t>(x.bh % p.kv_heads) * p.group + gh;
-        return x.bh / p.kv_heads * s[0] + head * s[1] + (row_ok ? qrow : 0) * s[2];
-      };
-      uint4* dst = reinterpret_cast<uint4*>(p.dq + at(p.dq_s)) + 8 * h;
+      const int64_t qrow = kFlat ? 128 * static_cast<int64_t>(x.tile) + r : chunk_token(p, x.tile, x.sub, r);
+      const bool row_ok = !kFlat || qrow < p.Lq;
+      const int64_t row = static_cast<int64_t>(x.bh) * (kFlat ? p.Lq : p.N) + (row_ok ? qrow : 0);
+      uint4* dst = reinterpret_cast<uint4*>(p.dq + row * 128) + 8 * h;
       float4* dstp = kFlat ? reinterpret_cast<float4*>(p.dq_part + x.sub * p.part_stride + row * 128) + 16 * h : nullptr;
       if (n_steps == 0) {  // no keys: no gradient
         if (row_ok) {
-          if (kFlat && (!kCross || p.n_split > 1)) {
+          if constexpr (kFlat) {
 #pragma unroll
             for (int c = 0; c < 16; ++c) dstp[c] = make_float4(0.f, 0.f, 0.f, 0.f);
           } else {
@@ -493,13 +422,13 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
         }
         continue;
       }
-      const int64_t lrow = kFlat ? bh * p.ld_rows + qrow : row;
+      const int64_t lrow = kFlat ? static_cast<int64_t>(x.bh) * p.ld_rows + qrow : row;
       const float neg_lse2 = row_ok ? -p.lse[lrow] * kLog2e : 0.f, dd = row_ok ? p.delta[lrow] : 0.f;
       {
         // the unit's row of Q (h = 0) or dO (h = 1), 256 bytes from global memory, into TMEM as
         // packed bf16 pairs (rows past Lq of a flat chunk: zeros).  The previous unit's
         // products have all completed: this warp has seen its last scores and dP.
-        const uint4* srcq = reinterpret_cast<const uint4*>((h ? p.dout : p.q) + at(h ? p.do_s : p.q_s));
+        const uint4* srcq = reinterpret_cast<const uint4*>((h ? p.dout : p.q) + row * 128);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t w[32];
@@ -532,7 +461,7 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
           if (lane == 0) mbar_arrive(s_read);  // the scores may take S(t + 1)
           // keys of this thread's 64 columns present in the chunk (a flat sequence's or the
           // extra keys' last chunk may be partial): the others get P = dS = 0
-          const int nv = chunk_valid<kFlat, kExtra, kCross>(p, x, ck, t) - 64 * h;
+          const int nv = chunk_valid<kFlat, kExtra>(p, ck, t) - 64 * h;
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
             float x0, x1;
@@ -551,14 +480,6 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
         tc_fence_after();
         uint32_t dp[64];
         tmem_ld64_wait(tmem + kColDP + 64 * h + lane_off, dp);
-        if constexpr (kCross) {  // a padding key's dP may be anything: 0 * (D - D)
-          const int nv = chunk_valid<kFlat, kExtra, kCross>(p, x, ck, t) - 64 * h;
-          if (nv < 64) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= nv) dp[c] = __float_as_uint(dd);
-          }
-        }
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 64; c += 2) {  // dS = P (dP - D), paired fp32 arithmetic
@@ -584,7 +505,7 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(dq_free);
-      if (kFlat && (!kCross || p.n_split > 1)) {  // this part's fp32 share of scale * dQ
+      if constexpr (kFlat) {  // this part's fp32 share of scale * dQ
         if (row_ok) {
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -595,7 +516,7 @@ __global__ void __launch_bounds__(bdq::kThreads, 1)
             dstp[8 + c] = make_float4(__uint_as_float(c2[4 * c]) * p.scale, __uint_as_float(c2[4 * c + 1]) * p.scale,
                                       __uint_as_float(c2[4 * c + 2]) * p.scale, __uint_as_float(c2[4 * c + 3]) * p.scale);
         }
-      } else if (row_ok) {
+      } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint4 v;

@@ -1,10 +1,11 @@
 // The kernels around the two tensor-core passes of the cross attention's backward (the cross
-// modes of bwd_bf16_kernel, key-major, for dK and dV, and of bwd_dq_kernel, query-major, for dQ):
+// mode of bwd_bf16_kernel, key-major, for dK and dV, and cross_dq_kernel, query-major, for dQ):
 // D = rowsum(dO * O) before them, and the sums of their parts after them.  All bound by memory.
 #pragma once
 
 #include <stdint.h>
 
+#include "dsa_bwd_bf16.cuh"
 #include "sm100.cuh"
 
 namespace dsa {
@@ -47,42 +48,84 @@ __global__ void __launch_bounds__(256) cross_preprocess(CrossPrepParams p) {
   }
 }
 
-struct CrossCombineParams {
-  const float* part[2];      // [n_part, rows, 128] fp32
-  __nv_bfloat16* out[2];     // through strides (batch, head, row)
-  int64_t s[2][3];
-  float scale[2];
-  int n_part, n_out;         // n_out: 1 or 2 tensors
-  int64_t part_stride;       // rows * 128
-  int B, heads, L;
-  const int32_t* len;        // rows from len[b] on are zero and have no parts; null: L
-};
-
-// out = scale * sum of the parts in part order, as bf16 (no parts: zeros).  A thread takes 4
-// channels of one row; blockIdx.y is the tensor.
-__global__ void __launch_bounds__(256) cross_combine(CrossCombineParams p) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t row = id / 32, bh = row / p.L;
-  if (bh >= static_cast<int64_t>(p.B) * p.heads) return;
-  const int c = static_cast<int>(id % 32), l = static_cast<int>(row % p.L), k = blockIdx.y;
-  const int64_t b = bh / p.heads, h = bh % p.heads;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.len == nullptr || l < p.len[b]) {
-    const float4* src = reinterpret_cast<const float4*>((k ? p.part[1] : p.part[0]) + row * 128) + c;
-#pragma unroll 4
-    for (int j = 0; j < p.n_part; ++j) {
-      const float4 x = src[j * (p.part_stride / 4)];
+// dK and dV of the 128-key units that were cut between CTAs: scale * (for dK) the sum of the
+// pieces' fp32 sums, in CTA order, as bf16; and zeros for the padding's rows.  A block takes one
+// 128-key chunk of one kv head (blockIdx.x) of dk or dv (blockIdx.y); n_cta: the key-major pass'
+// grid.
+__global__ void __launch_bounds__(256) cross_kv_combine(BwdBf16Params p, int n_cta) {
+  const int chunks = (p.Lk + 127) / 128, kt = blockIdx.x % chunks, bh = blockIdx.x / chunks, b = bh / p.kv_heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, len = bwd_kv_length(p, b), kv_c = (len + 127) / 128;
+  const bool is_dk = blockIdx.y == 0;
+  const int64_t* s = is_dk ? p.dk_s : p.dv_s;
+  __nv_bfloat16* out = (is_dk ? p.dk : p.dv) + b * s[0] + (bh % p.kv_heads) * s[1];
+  // units before this one, and in all (every warp adds them up)
+  int64_t before = 0, units = 0;
+  for (int i = lane; i < p.B; i += 32) {
+    const int64_t n = static_cast<int64_t>(bwd_kv_chunks(p, i)) * p.kv_heads;
+    units += n;
+    if (i < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  int i0 = 0, i1 = -1;  // the CTAs that hold pieces of this unit
+  int64_t start = 0, all = units * p.per_unit;
+  if (kt < kv_c && p.per_unit > 0) {
+    start = (before + static_cast<int64_t>(bh % p.kv_heads) * kv_c + kt) * p.per_unit;
+    i0 = static_cast<int>(((start + 1) * n_cta - 1) / all);
+    i1 = static_cast<int>(((start + p.per_unit) * n_cta - 1) / all);
+  }
+  const float f = is_dk ? p.scale : 1.f;
+  const float* part = is_dk ? p.dk_part : p.dv_part;
+  for (int r = warp; r < 128; r += 8) {
+    const int l = 128 * kt + r;
+    if (l >= p.Lk) break;
+    if (l < len && i0 == i1) continue;  // one CTA's own: written by it
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = i0; i <= i1 && l < len; ++i) {
+      const int64_t lo = all * i / n_cta;
+      if (lo == all * (i + 1) / n_cta) continue;  // an empty range (fewer query chunks than CTAs)
+      const float4 x = reinterpret_cast<const float4*>(part + (2 * static_cast<int64_t>(i) + (lo < start)) * 16384 + r * 128)[lane];
       a.x += x.x;
       a.y += x.y;
       a.z += x.z;
       a.w += x.w;
     }
+    reinterpret_cast<uint2*>(out + l * s[2])[lane] =
+        make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
   }
-  const float f = k ? p.scale[1] : p.scale[0];
-  __nv_bfloat16* out = k ? p.out[1] + b * p.s[1][0] + h * p.s[1][1] + l * p.s[1][2]
-                         : p.out[0] + b * p.s[0][0] + h * p.s[0][1] + l * p.s[0][2];
-  reinterpret_cast<uint2*>(out)[c] =
-      make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+}
+
+struct CrossDqCombineParams {
+  const float* part;         // [n_part, rows, 128] fp32
+  __nv_bfloat16* dq;         // through strides (batch, head, row)
+  int64_t s[3];
+  int n_part;
+  int B, heads, Lq;
+};
+
+// dQ = the sum of the parts in part order, as bf16 (no parts: zeros).  A thread takes 4 channels
+// of one row.
+__global__ void __launch_bounds__(256) cross_dq_combine(CrossDqCombineParams p) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t row = id / 32, bh = row / p.Lq, rows = static_cast<int64_t>(p.B) * p.heads * p.Lq;
+  if (row >= rows) return;
+  const int c = static_cast<int>(id % 32), q = static_cast<int>(row % p.Lq);
+  const int64_t b = bh / p.heads, h = bh % p.heads;
+  const float4* src = reinterpret_cast<const float4*>(p.part + row * 128) + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = 0; j < p.n_part; ++j) {
+    const float4 x = src[j * rows * 32];
+    a.x += x.x;
+    a.y += x.y;
+    a.z += x.z;
+    a.w += x.w;
+  }
+  reinterpret_cast<uint2*>(p.dq + b * p.s[0] + h * p.s[1] + q * p.s[2])[c] =
+      make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 
 }  // namespace dsa

@@ -1,0 +1,471 @@
+// dQ of the cross attention's backward, query-major: for query row n with the len_b keys of its
+// batch entry
+//   P_nm = exp(scale q_n.k_m - LSE_n),  dS_nm = P_nm (dO_n.v_m - D_n),  dQ_n = scale sum_m dS_nm k_m.
+//
+// As bwd_dq_kernel (the window backward's dQ pass) it recomputes S = Q K^T and dP = dO V^T on the
+// tensor cores 128 keys at a time, forms dS in registers and accumulates dQ += dS K in TMEM, with
+// Q and dO as TMEM operands.  What differs is the unit: a window holds thousands of keys, a
+// prompt one to four steps' worth, so here the time goes where units meet (that kernel took 9700
+// clocks per step on a 203 + 512-key pair of prompts, 1540 of them products):
+//   * Q and dO of the next unit are loaded by TMA during this one into a 64 KB staging buffer, and
+//     copied into TMEM by the elementwise warps (a row per thread) when this unit's last dS is
+//     written, while its last dQ product runs;
+//   * a unit's dQ is read out and written after that copy, while the next unit's first scores are
+//     computed, through Q's half of the staging buffer and TMA stores (rows packed from several
+//     heads, and fp32 parts, are stored directly);
+//   * K of up to 384 and V of up to 256 keys stay in shared memory for all consecutive units of
+//     their kv head; a CTA's units are a contiguous range of equal cost, as in the forward, whose
+//     units these are.
+//
+// Persistent and warp-specialised, one CTA per SM, 384 threads:
+//   warp 8      TMA producer of K (128-key chunks, 3 entries: read by the scores of its step,
+//               issued a step early, and by its dQ product)
+//   warp 10     TMA producer of V (2 entries) and of Q and dO
+//   warp 11     takes each K chunk as it lands, zeroes the rows past the last key that the dQ
+//               product will read (against dS = 0, but 0 * NaN is NaN) and hands it over
+//   warp 9      MMA issuer, per step t: S(t + 1) once the elementwise warps hold S(t) in
+//               registers; dQ += dS(t) K(t) once dS(t) is written; then dP(t + 1)
+//   warps 0-7   elementwise, two threads per row: thread h takes keys [64h, 64h + 64) of a step
+// TMEM (512 columns): Q [0, 64) and dO [64, 128) as packed bf16 pairs, scores [128, 256), dP (then
+// dS) [256, 384), dQ [384, 512).
+#pragma once
+
+#include <stdint.h>
+
+#include "dsa_bwd_dq.cuh"
+#include "dsa_cross_fwd.cuh"
+#include "sm100.cuh"
+
+namespace dsa {
+
+struct CrossDqParams : CrossShape {
+  const float* lse;    // [B * heads, ld_rows]
+  const float* delta;
+  int ld_rows;
+  __nv_bfloat16* dq;   // through strides (batch, head, row)
+  int64_t dq_s[3];
+  float* dq_part;      // n_split > 1: [n_split, B * heads * Lq, 128]
+  uint32_t q_bytes;    // bytes a unit's Q (or dO) boxes load
+  int qb, qk, qg, db, dk, dg, kb, kh, vb, vh;  // 1, or 0 for a broadcast (stride 0) dimension of q, dO, k, v
+  float scale, scale_log2;
+};
+
+namespace crossdq {
+constexpr int kThreads = bdq::kThreads;
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kHandWarp = 11;
+constexpr int kK = 3, kV = 2;
+constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
+constexpr uint32_t kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kK * kTile;
+constexpr uint32_t kOffBar = kOffV + kV * kTile;
+constexpr uint32_t kSmemUsed = kOffBar + 256;
+constexpr uint32_t kSmemBytes = 227 * 1024;
+static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
+using Cur = crossf::Cursor<128>;
+
+// A lane's row (32 q + lane, 256 bytes in two swizzled 64-channel halves at `tile`) into TMEM as
+// packed bf16 pairs.
+__device__ __forceinline__ void copy_row(uint32_t tile, int row, uint32_t t_dst) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t w[32];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t at = tile + half * kHalf + row * 128 + ((c ^ (row & 7)) << 4);
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                   : "r"(at)
+                   : "memory");
+    }
+    tmem_st32(t_dst + 32 * half, w);
+  }
+}
+}  // namespace crossdq
+
+__global__ void __launch_bounds__(crossdq::kThreads, 1)
+    cross_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmDQ, CrossDqParams p) {
+  using namespace crossdq;
+  using bdq::kColDO;
+  using bdq::kColDP;
+  using bdq::kColDQ;
+  using bdq::kColQ;
+  using bdq::kColS;
+  using fwd::desc_add;
+  using fwd::warp_wait;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+  if (pad + kSmemUsed > kSmemBytes) {  // uniform over the CTA: nothing has started yet
+    if (threadIdx.x == 0) device_report(DSA_DEV_BOUNDS, 6);
+    return;
+  }
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* qd_full = bars;              // Q and dO of a unit have landed in the staging buffer
+  uint64_t* q_free = bars + 1;           // Q's half may be loaded again (8)
+  uint64_t* do_free = bars + 2;          // dO's half (4)
+  uint64_t* k_land = bars + 3;           // [kK]
+  uint64_t* k_full = k_land + kK;        // [kK] handed over
+  uint64_t* k_empty = k_full + kK;       // [kK]
+  uint64_t* v_full = k_empty + kK;       // [kV]
+  uint64_t* v_empty = v_full + kV;       // [kV]
+  uint64_t* s_full = v_empty + kV;       // S of a step ready
+  uint64_t* s_read = s_full + 1;         // loaded (8)
+  uint64_t* dp_full = s_full + 2;        // dP of a step ready
+  uint64_t* ds_full = s_full + 3;        // dS written (8)
+  uint64_t* dq_done = s_full + 4;        // every dQ product of a unit done
+  uint64_t* dq_free = s_full + 5;        // dQ read out (8)
+  uint64_t* qa_full = s_full + 6;        // the unit's Q and dO are in TMEM (8)
+  uint64_t* q_copied = s_full + 7;       // its Q has been read from the staging buffer (4)
+  uint64_t* drain = s_full + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
+  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 9) + 1;
+  int* range = reinterpret_cast<int*>(s_full + 10);  // [2]
+  static_assert(3 + 3 * kK + 2 * kV + 11 <= 256 / 8, "barriers must fit their 256 bytes");
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmDO);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+    mbar_init(qd_full, 1);
+    mbar_init(q_free, 8);
+    mbar_init(do_free, 4);
+    for (int s = 0; s < kK; ++s) {
+      mbar_init(k_land + s, 1);
+      mbar_init(k_full + s, 1);
+      mbar_init(k_empty + s, 1);
+    }
+    for (int s = 0; s < kV; ++s) {
+      mbar_init(v_full + s, 1);
+      mbar_init(v_empty + s, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 8);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_full, 8);
+    mbar_init(dq_done, 1);
+    mbar_init(dq_free, 8);
+    mbar_init(qa_full, 8);
+    mbar_init(q_copied, 4);
+    mbar_init(drain, 1);
+    *abort = 0;
+    fence_mbar_init();
+    int b, e;
+    crossf::unit_range(p, blockIdx.x, gridDim.x, b, e);
+    range[0] = b;
+    range[1] = e;
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, bdq::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int begin = range[0], end = range[1];
+
+  if (warp >= 8) {
+    setmaxnreg_dec<bdq::kRegsAux>();
+    if (warp == kKWarp) {
+      // ------------------------------------------------------------------ TMA producer of K
+      if (lane == 0) {
+        Cur c;
+        c.start(p, begin, end);
+        int ld = 0;
+        bool ok = true;
+        for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
+          if (c.reuse(kK)) continue;
+          for (int j = 0; j < c.n; ++j, ++ld) {
+            const int st = ld % kK;
+            ok = mbar_wait(k_empty + st, ((ld / kK) & 1) ^ 1, abort, 171);
+            if (!ok) break;
+            uint8_t* dst = smem + kOffK + st * kTile;
+            mbar_arrive_expect_tx(k_land + st, kTile);
+            tma_load_4d(dst, &tmK, k_land + st, 0, 128 * (c.c0 + j), c.x.kvh * p.kh, c.x.b * p.kb);
+            tma_load_4d(dst + kHalf, &tmK, k_land + st, 64, 128 * (c.c0 + j), c.x.kvh * p.kh, c.x.b * p.kb);
+          }
+        }
+      }
+    } else if (warp == kHandWarp) {
+      // ------------------------------------------------------------------ K hand-over (whole warp)
+      Cur c;
+      c.start(p, begin, end);
+      int ld = 0;
+      bool ok = true;
+      for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
+        if (c.reuse(kK)) continue;
+        for (int j = 0; j < c.n; ++j, ++ld) {
+          const int st = ld % kK;
+          ok = warp_wait(k_land + st, (ld / kK) & 1, abort, 172);
+          if (!ok) break;
+          const int keys = c.keys(j);
+          if (keys & 15) {
+            const int pad_rows = 16 - (keys & 15);
+            const uint32_t k0 = sbase + kOffK + st * kTile + (lane >> 3 & 1) * kHalf + (lane & 7) * 16;
+            for (int rr = lane >> 4; rr < pad_rows; rr += 2) st_shared_v4(k0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full + st);
+        }
+      }
+    } else if (warp == kVWarp) {
+      // ------------------------------------------------------------------ TMA producer of V, Q and dO
+      if (lane == 0) {
+        Cur c;
+        c.start(p, begin, end);
+        int ld = 0, un = 0;
+        bool ok = true;
+        for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
+          ok = mbar_wait(do_free, (un & 1) ^ 1, abort, 173);
+          if (!ok) break;
+          const int g = c.x.g, row = c.x.row;
+          mbar_arrive_expect_tx(qd_full, 2 * p.q_bytes);
+          tma_load_5d(smem + kOffDO, &tmDO, qd_full, 0, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
+          tma_load_5d(smem + kOffDO + kHalf, &tmDO, qd_full, 64, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
+          ok = mbar_wait(q_free, (un & 1) ^ 1, abort, 174);
+          if (!ok) break;
+          tma_load_5d(smem + kOffQ, &tmQ, qd_full, 0, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          tma_load_5d(smem + kOffQ + kHalf, &tmQ, qd_full, 64, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          if (c.reuse(kV)) continue;
+          for (int j = 0; j < c.n; ++j, ++ld) {
+            const int st = ld % kV;
+            ok = mbar_wait(v_empty + st, ((ld / kV) & 1) ^ 1, abort, 175);
+            if (!ok) break;
+            uint8_t* dst = smem + kOffV + st * kTile;
+            mbar_arrive_expect_tx(v_full + st, kTile);
+            tma_load_4d(dst, &tmV, v_full + st, 0, 128 * (c.c0 + j), c.x.kvh * p.vh, c.x.b * p.vb);
+            tma_load_4d(dst + kHalf, &tmV, v_full + st, 64, 128 * (c.c0 + j), c.x.kvh * p.vh, c.x.b * p.vb);
+          }
+        }
+      }
+    } else {
+      // ------------------------------------------------------------------ MMA issuer (whole warp)
+      const uint64_t dKk = smem_desc_sw128(sbase + kOffK, 16, 1024);     // K-major
+      const uint64_t dKm = smem_desc_sw128(sbase + kOffK, kHalf, 1024);  // MN-major
+      const uint64_t dVk = smem_desc_sw128(sbase + kOffV, 16, 1024);
+      Cur c;
+      c.start(p, begin, end);
+      int ks = 0, vs = 0, un = 0, G = 0;  // ring positions of the unit's first chunk; units, steps before
+      bool ok = true;
+      for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
+        const bool k_reuse = c.reuse(kK), k_keep = c.keep(p, kK), v_reuse = c.reuse(kV), v_keep = c.keep(p, kV);
+        const int n = c.n;
+        ok = warp_wait(qa_full, un & 1, abort, 180);
+        if (!ok) break;
+        auto issue_s = [&](int t) -> bool {  // once S of the step before has been loaded
+          const int st = (ks + t) % kK;
+          if (!k_reuse && !warp_wait(k_full + st, ((ks + t) / kK) & 1, abort, 181)) return false;
+          if (G + t > 0 && !warp_wait(s_read, (G + t - 1) & 1, abort, 182)) return false;
+          tc_fence_after();
+          bdq::issue_qk(tmem + kColS, tmem + kColQ, desc_add(dKk, st * kTile));
+          mma_commit_warp(s_full);
+          return true;
+        };
+        auto issue_dp = [&](int t) -> bool {  // after the dQ product that read dS(t - 1) from its columns
+          const int st = (vs + t) % kV;
+          if (!v_reuse && !warp_wait(v_full + st, ((vs + t) / kV) & 1, abort, 183)) return false;
+          tc_fence_after();
+          bdq::issue_qk(tmem + kColDP, tmem + kColDO, desc_add(dVk, st * kTile));
+          mma_commit_warp(dp_full);
+          if (!v_keep) mma_commit_warp(v_empty + st);
+          return true;
+        };
+        ok = issue_s(0) && issue_dp(0);
+        for (int t = 0; t < n && ok; ++t) {
+          if (t + 1 < n) ok = issue_s(t + 1);
+          const int st = (ks + t) % kK, n16 = (c.keys(t) + 15) >> 4;
+          if (ok && t == 0) ok = warp_wait(dq_free, (un & 1) ^ 1, abort, 185);
+          if (ok) ok = warp_wait(ds_full, (G + t) & 1, abort, 184);
+          if (!ok) break;
+          tc_fence_after();
+          if (n16 == 8) {
+            bdq::issue_dq(tmem + kColDQ, tmem + kColDP, desc_add(dKm, st * kTile), t > 0);
+          } else {  // the last chunk: only the sixteens that hold keys
+#pragma unroll 1
+            for (int kk = 0; kk < n16; ++kk)
+              mma_ts_warp(tmem + kColDQ, tmem + kColDP + 64 * (kk >> 2) + 8 * (kk & 3),
+                          desc_add(dKm, st * kTile + kk * 2048), bdq::kIdescDQ, t > 0 || kk > 0);
+          }
+          if (!k_keep) mma_commit_warp(k_empty + st);
+          if (t + 1 < n) ok = issue_dp(t + 1);
+        }
+        if (!ok) break;
+        mma_commit_warp(dq_done);
+        G += n;
+        if (!k_keep) ks += n;
+        if (!v_keep) vs += n;
+      }
+      mma_commit_warp(drain);
+      fwdp::drain_wait(drain, 0);
+    }
+  } else {
+    setmaxnreg_inc<bdq::kRegsElem>();
+    // ------------------------------------------------------------------ elementwise and output
+    const int h = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const float kLog2e = 1.4426950408889634f;
+    const bool staged = p.n_split == 1 && p.pk == 1;  // dQ through the staging buffer
+    int G = 0, un = 0;
+    bool ok = true, stored = false;  // stored: this lane has a TMA store that may still read the buffer
+    crossf::Unit px = {};            // the unit whose dQ is still in TMEM
+    // dQ = scale * accumulator, channels [64h, 64h + 64) of this thread's row of unit px
+    auto write_out = [&](int unit) -> bool {
+      if (!warp_wait(dq_done, unit & 1, abort, 190)) return false;
+      tc_fence_after();
+      const uint32_t tD = tmem + kColDQ + 64 * h + lane_off;
+      if (staged) {
+        const uint32_t off = kOffQ + h * kHalf + quarter * 4096;
+        crossf::stage_o(tD, p.scale, sbase + off);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(dq_free);
+          const int r0 = px.row + 32 * quarter;
+          if (r0 < p.Lq) {
+            tma_store_5d(&tmDQ, smem + off, 64 * h, r0, px.g, px.kvh, px.b);
+            tma_store_commit();
+          }
+        }
+      } else {
+        const crossf::Row y = crossf::unit_row(p, px, r);
+        if (p.n_split > 1) {
+          const int64_t rows = static_cast<int64_t>(p.B) * p.heads * p.Lq;
+          const int64_t row = (static_cast<int64_t>(px.b) * p.heads + y.head) * p.Lq + y.q;
+          crossf::store_o_f32(tD, p.scale,
+                              reinterpret_cast<float4*>(p.dq_part + (y.ok ? px.part * rows + row : 0) * 128) + 16 * h, y.ok);
+        } else {
+          const int64_t at = y.ok ? px.b * p.dq_s[0] + y.head * p.dq_s[1] + y.q * p.dq_s[2] : 0;
+          fwd::store_o(tD, 2, p.scale, reinterpret_cast<uint4*>(p.dq + at) + 8 * h, y.ok);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dq_free);
+      }
+      return true;
+    };
+    Cur c;
+    c.start(p, begin, end);
+    for (; ok && c.valid(); c.advance(p)) {
+      const crossf::Row y = crossf::unit_row(p, c.x, r);
+      const int64_t bh = static_cast<int64_t>(c.x.b) * p.heads + y.head;
+      if (c.n == 0) {  // no keys: no gradient
+        if (y.ok) {
+          if (p.n_split > 1) {
+            float4* dst = reinterpret_cast<float4*>(
+                p.dq_part + (c.x.part * static_cast<int64_t>(p.B) * p.heads * p.Lq + bh * p.Lq + y.q) * 128) + 16 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(p.dq + c.x.b * p.dq_s[0] + y.head * p.dq_s[1] + y.q * p.dq_s[2]) + 8 * h;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        continue;
+      }
+      const int64_t lrow = bh * p.ld_rows + y.q;
+      const float neg_lse2 = y.ok ? -p.lse[lrow] * kLog2e : 0.f, dd = y.ok ? p.delta[lrow] : 0.f;
+      // Q (h = 0) or dO (h = 1) of the row into TMEM; the previous unit's products that read them
+      // have completed: this warp has seen its last scores and dP
+      ok = warp_wait(qd_full, un & 1, abort, 191);
+      if (!ok) break;
+      copy_row(sbase + (h ? kOffDO : kOffQ), r, tmem + (h ? kColDO : kColQ) + lane_off);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(qa_full);
+        mbar_arrive(h ? do_free : q_copied);
+      }
+      if (un > 0) {
+        // (these rows of dQ go where the other warp's Q was)
+        if (h) ok = warp_wait(q_copied, un & 1, abort, 194);
+        if (ok) ok = write_out(un - 1);
+        if (!ok) break;
+        stored = staged;
+      }
+      if (!stored && lane == 0) mbar_arrive(q_free);
+      for (c.t = 0; c.t < c.n; ++c.t, ++G) {
+        const int nv = c.keys(c.t) - 64 * h;  // keys of this thread's 64 columns
+        ok = warp_wait(s_full, G & 1, abort, 192);
+        if (!ok) break;
+        tc_fence_after();
+        float pf[64];
+        {
+          uint32_t s[64];
+          tmem_ld64_wait(tmem + kColS + 64 * h + lane_off, s);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_read);
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            float x0, x1;
+            ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), p.scale_log2, p.scale_log2, neg_lse2,
+                  neg_lse2);
+            pf[e] = ex2_approx(x0);
+            pf[e + 1] = ex2_approx(x1);
+          }
+        }
+        if (stored) {  // dQ of the previous unit has left the buffer by now: Q may be loaded
+          if (lane == 0) {
+            tma_store_wait_read();
+            mbar_arrive(q_free);
+          }
+          stored = false;
+        }
+        ok = warp_wait(dp_full, G & 1, abort, 193);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dp[64];
+        tmem_ld64_wait(tmem + kColDP + 64 * h + lane_off, dp);
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          float a0, a1, d0, d1;
+          fadd2(a0, a1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), -dd, -dd);
+          ffma2(d0, d1, a0, a1, pf[e], pf[e + 1], 0.f, 0.f);
+          w[e >> 1] = pack_bf16x2(d0, d1);
+        }
+        if (nv < 64) {  // no key in these columns: their P and dP may be anything, dS is zero
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (2 * e >= nv) w[e] = 0u;
+            else if (2 * e + 1 >= nv) w[e] &= 0xffffu;
+          }
+        }
+        tmem_st32(tmem + kColDP + 64 * h + lane_off, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      px = c.x;
+      ++un;
+    }
+    if (ok && un > 0) write_out(un - 1);
+    if (lane == 0) tma_store_wait_read();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort && tid == 0) {
+    // after a failed wait, give loads already issued time to land before the CTA leaves
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 100000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tmem, bdq::kTmemCols);
+  }
+}
+
+}  // namespace dsa

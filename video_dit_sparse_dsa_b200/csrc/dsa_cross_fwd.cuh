@@ -56,18 +56,22 @@
 
 namespace dsa {
 
-struct CrossFwdParams {
+// What a cross attention's units are cut from (the forward's and the query-major backward's).
+struct CrossShape {
   const int32_t* kv_len;  // [B] valid keys of each batch entry, or null: Lk
+  int B, heads, kv_heads, group, Lq, Lk;
+  int pk;                 // heads packed into a unit (Lq * pk <= 128), or 1
+  int tiles;              // units per kv head and part
+  int n_split;            // parts of the keys
+  int n_units;            // B * kv_heads * n_split * tiles
+};
+
+struct CrossFwdParams : CrossShape {
   __nv_bfloat16* out;
   int64_t ob, oh, ol;     // strides of out in elements
   float* lse;             // [B, heads, Lq]
   float* part_o;          // n_split > 1: [n_split, B * heads * Lq, 128] and [n_split, B * heads * Lq]
   float* part_lse;
-  int B, heads, kv_heads, group, Lq, Lk;
-  int pk;                 // heads packed into a unit (Lq * pk <= 128), or 1
-  int tiles;              // units per kv head and part
-  int n_split;
-  int n_units;            // B * kv_heads * n_split * tiles
   uint32_t q_bytes;       // bytes a unit's Q boxes load
   int qb, qk, qg, kb, kh, vb, vh;  // 1, or 0 for a broadcast (stride 0) dimension
   float scale_log2;
@@ -102,23 +106,23 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 256, as in the wi
 // column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
 constexpr uint32_t kPolyMask = 0x22u;
 
-__device__ __forceinline__ int kv_length(const CrossFwdParams& p, int b) {
+__device__ __forceinline__ int kv_length(const CrossShape& p, int b) {
   return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + b), 0), p.Lk);
 }
 
 // Chunks per part of a sequence of `chunks`: even, so that parts are whole steps.
-__device__ __forceinline__ int chunks_per_part(const CrossFwdParams& p, int chunks) {
+__device__ __forceinline__ int chunks_per_part(const CrossShape& p, int chunks) {
   const int per = (chunks + p.n_split - 1) / p.n_split;
   return p.n_split > 1 ? (per + 1) & ~1 : per;
 }
 
 // The CTA's units [begin, end): the sequence is cut at equal cost, a unit costing its chunks and
 // a constant (about half a chunk's) for its own start and end.
-__device__ __forceinline__ int64_t unit_cost(const CrossFwdParams& p, int b) {
+__device__ __forceinline__ int64_t unit_cost(const CrossShape& p, int b) {
   return 2 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + 1;
 }
 
-__device__ __forceinline__ void unit_range(const CrossFwdParams& p, int cta, int n_cta, int& begin, int& end) {
+__device__ __forceinline__ void unit_range(const CrossShape& p, int cta, int n_cta, int& begin, int& end) {
   const int64_t per_b = static_cast<int64_t>(p.kv_heads) * p.n_split * p.tiles;
   int64_t total = 0;
   for (int b = 0; b < p.B; ++b) total += per_b * unit_cost(p, b);
@@ -167,11 +171,11 @@ struct Cursor {
   // The unit's K (or V) is still in the ring, which holds `chunks`, from the previous unit; the
   // next unit will find it there too.
   __device__ __forceinline__ bool reuse(int chunks) const { return same && n <= chunks; }
-  __device__ __forceinline__ bool keep(const CrossFwdParams& p, int chunks) const {
+  __device__ __forceinline__ bool keep(const CrossShape& p, int chunks) const {
     return n <= chunks && u + 1 < end && (x.row + kRows < p.Lq || x.g + p.pk < p.group);
   }
 
-  __device__ __forceinline__ void start(const CrossFwdParams& p, int begin, int end_) {
+  __device__ __forceinline__ void start(const CrossShape& p, int begin, int end_) {
     u = begin;
     end = end_;
     const int tile = u % p.tiles, slice = u / p.tiles;
@@ -190,14 +194,14 @@ struct Cursor {
     t = 0;
     if (valid()) chunks(p);
   }
-  __device__ __forceinline__ void chunks(const CrossFwdParams& p) {
+  __device__ __forceinline__ void chunks(const CrossShape& p) {
     len = kv_length(p, x.b);
     const int all = (len + 127) / 128, per = chunks_per_part(p, all);
     c0 = x.part * per;
     n = max(min(per, all - c0), 0);
   }
   // The next unit, with or without keys.
-  __device__ __forceinline__ void advance(const CrossFwdParams& p) {
+  __device__ __forceinline__ void advance(const CrossShape& p) {
     ++u;
     t = 0;
     same = true;
@@ -218,14 +222,14 @@ struct Cursor {
     if (valid()) chunks(p);
   }
   // This unit, or the next one that has keys.
-  __device__ __forceinline__ void settle(const CrossFwdParams& p) {
+  __device__ __forceinline__ void settle(const CrossShape& p) {
     while (valid() && n == 0) advance(p);
   }
-  __device__ __forceinline__ void next_unit(const CrossFwdParams& p) {
+  __device__ __forceinline__ void next_unit(const CrossShape& p) {
     advance(p);
     settle(p);
   }
-  __device__ __forceinline__ void next_step(const CrossFwdParams& p) {
+  __device__ __forceinline__ void next_step(const CrossShape& p) {
     if (last())
       next_unit(p);
     else
@@ -410,7 +414,7 @@ struct Row {
   int head, q;
 };
 
-__device__ __forceinline__ Row unit_row(const CrossFwdParams& p, const Unit& x, int r) {
+__device__ __forceinline__ Row unit_row(const CrossShape& p, const Unit& x, int r) {
   Row y;
   int g = x.g;
   if (p.pk > 1) {  // row r = (head in the pack) * Lq + position
