@@ -478,7 +478,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   bp.group = c.group;
   bp.per_unit = c.per_unit;
   bp.G1 = bp.G2 = bp.tt = bp.th = bp.tw = bp.T = bp.H = bp.W = bp.KU = bp.QS = bp.n_tiles = bp.n_split = 1;
-  const dim3 kv_grid(static_cast<unsigned>(c.kv_units), 2, 1);
+  const dim3 kv_grid(static_cast<unsigned>(c.kv_units), 2, 8);
   if (p->Lq == 0) {  // no queries: dk = dv = 0
     dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(bp, 1);
     return launch_status();
@@ -497,7 +497,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   pp.Lq = p->Lq;
   pp.Lp = c.Lp;
   const int64_t BH = static_cast<int64_t>(p->B) * p->heads;
-  dsa::cross_preprocess<<<static_cast<unsigned>((BH * c.Lp * 16 + 255) / 256), 256, 0, s>>>(pp);
+  dsa::cross_preprocess<<<static_cast<unsigned>((BH * c.Lp + 63) / 64), 256, 0, s>>>(pp);
   st = launch_status();
   if (st != DSA_OK) return st;
 

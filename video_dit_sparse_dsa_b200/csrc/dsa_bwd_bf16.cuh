@@ -196,12 +196,37 @@ __device__ __forceinline__ BwdChunks bwd_chunks(const BwdBf16Params& p, const Bw
 }
 
 // Query rows present in the unit's chunk c (a flat sequence's last chunk can be partial).
-template <bool kFlatK, bool kExtra, bool kCross = false>
+template <bool kFlatK, bool kExtra>
 __device__ __forceinline__ int bwd_qvalid(const BwdBf16Params& p, const BwdChunks& q, int c) {
   if (!kFlatK && !kExtra) return 64;
-  if constexpr (kCross) return min(p.Nq - 64 * ((q.c0 + c) % ((p.Nq + 63) / 64)), 64);
   if (c < q.nm) return kFlatK ? min(p.Nq - 64 * (q.c0 + c), 64) : 64;
   return min(p.Lxq - 64 * (c - q.nm), 64);
+}
+
+// Cross mode: 32 queries' P^T = exp2(S^T * scale * log2 e - LSE_n * log2 e) and dS^T = P^T (dP^T -
+// D_n), packed to bf16, in paired fp32 arithmetic.
+__device__ __forceinline__ void cross_p_ds(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float4* lse4,
+                                           const float4* dd4, float scale_log2, uint32_t (&pk)[16],
+                                           uint32_t (&ds)[16]) {
+  const float kLog2e = 1.4426950408889634f;
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const float4 lv = lse4[g], dv = dd4[g];
+    const float nl[4] = {lv.x * -kLog2e, lv.y * -kLog2e, lv.z * -kLog2e, lv.w * -kLog2e};
+    const float dd[4] = {-dv.x, -dv.y, -dv.z, -dv.w};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int n0 = 4 * g + 2 * e;
+      float x0, x1, a0, a1, d0, d1;
+      ffma2(x0, x1, __uint_as_float(sr[n0]), __uint_as_float(sr[n0 + 1]), scale_log2, scale_log2, nl[2 * e],
+            nl[2 * e + 1]);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      fadd2(a0, a1, __uint_as_float(dr[n0]), __uint_as_float(dr[n0 + 1]), dd[2 * e], dd[2 * e + 1]);
+      ffma2(d0, d1, a0, a1, p0, p1, 0.f, 0.f);
+      pk[2 * g + e] = pack_bf16x2(p0, p1);
+      ds[2 * g + e] = pack_bf16x2(d0, d1);
+    }
+  }
 }
 
 __device__ __forceinline__ int64_t chunk_row_token(int r, int t0, int h0, int w0, int th, int tw, int H, int W) {
@@ -431,6 +456,12 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
           tma_load_5d(smem + kOffV, &tmV, kv_full, 0, k_w0, k_h0, k_t0, bh);
           tma_load_5d(smem + kOffV + kKHalf, &tmV, kv_full, 64, k_w0, k_h0, k_t0, bh);
         }
+        int hg = 0, hc = 0, hn = 1;  // cross mode: head in the group, chunk within the head, chunks per head
+        if constexpr (kCross) {
+          hn = (p.Nq + 63) / 64;
+          hg = qc.c0 / hn;
+          hc = qc.c0 % hn;
+        }
         for (int c = 0; c < n && ok; ++c, ++ld) {
           const int st = ld % kStages;
           ok = mbar_wait(ld_empty + st, ((ld / kStages) & 1) ^ 1, abort, 51);
@@ -438,13 +469,17 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
           uint8_t* dst = smem + kOffStage + st * kStageBytes;
           mbar_arrive_expect_tx(ld_full + st, 2 * kQBytes + 512);
           if constexpr (kCross) {
-            const int nqc = (p.Nq + 63) / 64, hg = (qc.c0 + c) / nqc, row = 64 * ((qc.c0 + c) % nqc);
+            const int row = 64 * hc;
             tma_load_5d(dst, &tmQ, ld_full + st, 0, row, hg * p.qg, kvh * p.qk, b * p.qb);
             tma_load_5d(dst + kQHalf, &tmQ, ld_full + st, 64, row, hg * p.qg, kvh * p.qk, b * p.qb);
             tma_load_5d(dst + kQBytes, &tmDO, ld_full + st, 0, row, hg * p.dg, kvh * p.dkv, b * p.db);
             tma_load_5d(dst + kQBytes + kQHalf, &tmDO, ld_full + st, 64, row, hg * p.dg, kvh * p.dkv, b * p.db);
             tma_load_2d(dst + 2 * kQBytes, &tmLse, ld_full + st, row, bh * p.group + hg);
             tma_load_2d(dst + 2 * kQBytes + 512, &tmD, ld_full + st, row, bh * p.group + hg);
+            if (++hc == hn) {
+              hc = 0;
+              ++hg;
+            }
           } else if ((kExtra && c >= qc.nm) || kFlatK) {  // flat rows (past the end: zeros)
             const bool extra = c >= qc.nm;
             const int row = extra ? 64 * (c - qc.nm) : 64 * (qc.c0 + c);
@@ -555,9 +590,20 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       const int n = qc.nm + qc.nx;
       if (kCross && n == 0) break;  // past the CTA's range
       // flat keys: this thread's key row may lie past the end (zeros, no gradient)
+      int hc = 0, hn = 1;  // cross mode: the chunk within its head, chunks per head
+      if constexpr (kCross) {
+        hn = (p.Nq + 63) / 64;
+        hc = qc.c0 % hn - 1;
+      }
       const bool k_ok = !kFlatK || 128 * x.kt + m < (kCross ? bwd_kv_length(p, x.bh / p.kv_heads) : p.Lk);
       for (int c = 0; c < n; ++c, ++cc, ++ld) {
-        const int nvq = bwd_qvalid<kFlatK, kExtra, kCross>(p, qc, c) - 32 * h;  // valid queries of this half
+        int nvq;  // valid queries of this half
+        if constexpr (kCross) {
+          hc = hc + 1 == hn ? 0 : hc + 1;
+          nvq = min(p.Nq - 64 * hc, 64) - 32 * h;
+        } else {
+          nvq = bwd_qvalid<kFlatK, kExtra>(p, qc, c) - 32 * h;
+        }
         const bool masked = !k_ok || nvq < 32;  // P = dS = 0 for missing keys and queries
         const int b = cc & 1;
         ok = mbar_wait(s_full + b, (cc >> 1) & 1, abort, 70);
@@ -572,6 +618,18 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
         tmem_ld32_wait(tS + lane_off + b * 64 + 32 * h, sr);
         tmem_ld32_wait(tDP + lane_off + b * 64 + 32 * h, dr);
         uint32_t pk[16], dk2[16];
+        if constexpr (kCross) {
+          cross_p_ds(sr, dr, lse4, dd4, p.scale_log2, pk, dk2);
+          if (__any_sync(0xffffffffu, masked)) {  // a padding key's P and dP may be anything: both are zero
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int nv = k_ok ? nvq - 2 * e : 0;
+              const uint32_t keep = nv >= 2 ? 0xffffffffu : nv == 1 ? 0xffffu : 0u;
+              pk[e] &= keep;
+              dk2[e] &= keep;
+            }
+          }
+        } else
 #pragma unroll
         for (int g = 0; g < 8; ++g) {  // queries 32h + 4g .. 32h + 4g + 3
           const float4 lv = lse4[g], dv = dd4[g];
@@ -585,10 +643,6 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
             if (masked) {
               if (!k_ok || n0 >= nvq) p0 = 0.f;
               if (!k_ok || n0 + 1 >= nvq) p1 = 0.f;
-              if constexpr (kCross) {  // a padding key's dP may be anything: 0 * (D - D)
-                if (!k_ok || n0 >= nvq) dr[n0] = __float_as_uint(dq4[2 * e]);
-                if (!k_ok || n0 + 1 >= nvq) dr[n0 + 1] = __float_as_uint(dq4[2 * e + 1]);
-              }
             }
             pk[2 * g + e] = pack_bf16x2(p0, p1);
             dk2[2 * g + e] = pack_bf16x2(p0 * (__uint_as_float(dr[n0]) - dq4[2 * e]),
