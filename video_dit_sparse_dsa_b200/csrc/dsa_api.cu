@@ -15,6 +15,7 @@
 #include "dsa_cross_bwd.cuh"
 #include "dsa_cross_dq.cuh"
 #include "dsa_cross_fwd.cuh"
+#include "dsa_cross_kv.cuh"
 #include "dsa_device_status.cuh"
 #include "dsa_fwd_bf16.cuh"
 #include "dsa_fwd_f32.cuh"

@@ -70,9 +70,7 @@ struct CrossPlan {
   int chunks;             // 128-key chunks of Lk
   int64_t rows;           // B * heads * Lq
   int split_q;            // parts of the keys (forward, and dQ)
-  int per_unit;           // 64-row query chunks of a 128-key unit (dK, dV)
-  int64_t kv_units;       // such units, at most
-  int Lp;                 // Lq rounded up to 64
+  int64_t kv_units;       // 128-key units of kv heads (dK, dV), at most; `tiles` query chunks each
 };
 
 dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
@@ -90,12 +88,11 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
   c->rows = static_cast<int64_t>(p->B) * p->heads * p->Lq;
   // unit and row indices are 32 bits in the kernels
   if (p->Lq > INT32_MAX - 128 || p->Lk > INT32_MAX - 128 || tiles > INT32_MAX || slices > INT32_MAX ||
-      slices * tiles > INT32_MAX || c->rows > INT32_MAX - 64 * slices * c->group)
+      slices * tiles > INT32_MAX || c->rows > INT32_MAX)
     return DSA_ERR_UNSUPPORTED;
   c->tiles = static_cast<int>(tiles);
   c->units = slices * tiles;
   c->chunks = (p->Lk + 127) / 128;
-  c->Lp = (p->Lq + 63) / 64 * 64;
   // Too few units to fill the GPU: the keys are cut into parts of at least four chunks (two
   // steps), for about four units per SM.
   c->split_q = 1;
@@ -109,15 +106,13 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
   // more than one 128-row tile per head, and not in parts: a cluster of two CTAs per 256 rows
   c->pair = c->split_q == 1 && p->Lq > 128;
   c->kv_units = slices * c->chunks;
-  const int64_t per_unit = static_cast<int64_t>(c->group) * (c->Lp / 64);
-  if (c->kv_units > INT32_MAX || per_unit > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  c->per_unit = static_cast<int>(per_unit);
+  if (c->kv_units > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
 struct CrossWorkspace {
   float *part_o, *part_lse;                       // forward, split_q > 1
-  float *delta, *lse_pad, *dq_part, *dk_part, *dv_part;  // backward
+  float *delta, *dq_part, *dk_part, *dv_part;     // backward
   size_t bytes;
 };
 
@@ -137,8 +132,7 @@ CrossWorkspace cross_workspace(const dsa_cross_t* p, const CrossPlan& c, int kin
       w.part_lse = take(static_cast<size_t>(c.split_q) * c.rows);
     }
   } else {
-    w.delta = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
-    w.lse_pad = take(static_cast<size_t>(p->B) * p->heads * c.Lp);
+    w.delta = take(static_cast<size_t>(c.rows));
     if (c.split_q > 1) w.dq_part = take(static_cast<size_t>(c.split_q) * c.rows * 128);
     // the pieces of the 128-key units that are cut between CTAs: at most two per CTA
     w.dk_part = take(2 * kPlanSms * 128 * 128);
@@ -460,27 +454,37 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   }
   if (p->Lk == 0) return p->Lq > 0 ? launch_dq_combine(cq, s) : DSA_OK;  // no keys: dq = 0
 
-  dsa::BwdBf16Params bp;
-  std::memset(&bp, 0, sizeof(bp));
-  bp.dk = static_cast<__nv_bfloat16*>(dk->data);
-  bp.dv = static_cast<__nv_bfloat16*>(dv->data);
-  copy_strides(bp.dk_s, dk);
-  copy_strides(bp.dv_s, dv);
-  bp.scale = p->scale;
-  bp.scale_log2 = p->scale * 1.4426950408889634f;
-  bp.Lk = p->Lk;
-  bp.Nq = p->Lq;
-  bp.dk_part = ws.dk_part;
-  bp.dv_part = ws.dv_part;
-  bp.kv_len = kv_len;
-  bp.B = p->B;
-  bp.kv_heads = p->kv_heads;
-  bp.group = c.group;
-  bp.per_unit = c.per_unit;
-  bp.G1 = bp.G2 = bp.tt = bp.th = bp.tw = bp.T = bp.H = bp.W = bp.KU = bp.QS = bp.n_tiles = bp.n_split = 1;
+  dsa::CrossShape shape;
+  std::memset(&shape, 0, sizeof(shape));
+  shape.kv_len = kv_len;
+  shape.B = p->B;
+  shape.heads = p->heads;
+  shape.kv_heads = p->kv_heads;
+  shape.group = c.group;
+  shape.Lq = p->Lq;
+  shape.Lk = p->Lk;
+  shape.pk = c.pk;
+  shape.tiles = c.tiles;
+  shape.n_split = c.split_q;
+  shape.n_units = static_cast<int>(c.units * c.split_q);
+
+  dsa::CrossKvParams kp;
+  std::memset(&kp, 0, sizeof(kp));
+  static_cast<dsa::CrossShape&>(kp) = shape;
+  kp.per_unit = c.tiles;
+  kp.lse = lse;
+  kp.delta = ws.delta;
+  kp.dk = static_cast<__nv_bfloat16*>(dk->data);
+  kp.dv = static_cast<__nv_bfloat16*>(dv->data);
+  copy_strides(kp.dk_s, dk);
+  copy_strides(kp.dv_s, dv);
+  kp.dk_part = ws.dk_part;
+  kp.dv_part = ws.dv_part;
+  kp.scale = p->scale;
+  kp.scale_log2 = p->scale * 1.4426950408889634f;
   const dim3 kv_grid(static_cast<unsigned>(c.kv_units), 2, 8);
   if (p->Lq == 0) {  // no queries: dk = dv = 0
-    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(bp, 1);
+    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(kp, 1);
     return launch_status();
   }
 
@@ -489,81 +493,59 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   pp.dout = static_cast<const __nv_bfloat16*>(dout->data);
   copy_strides(pp.o_s, out);
   copy_strides(pp.do_s, dout);
-  pp.lse = lse;
-  pp.delta_pad = ws.delta;
-  pp.lse_pad = ws.lse_pad;
+  pp.delta = ws.delta;
   pp.B = p->B;
   pp.heads = p->heads;
   pp.Lq = p->Lq;
-  pp.Lp = c.Lp;
-  const int64_t BH = static_cast<int64_t>(p->B) * p->heads;
-  dsa::cross_preprocess<<<static_cast<unsigned>((BH * c.Lp + 63) / 64), 256, 0, s>>>(pp);
+  dsa::cross_preprocess<<<static_cast<unsigned>((c.rows + 63) / 64), 256, 0, s>>>(pp);
   st = launch_status();
   if (st != DSA_OK) return st;
 
-  CUtensorMap tq, tdo, tk, tv, tlse, tdel;
-  int mq[3], mdo[3], mk[3], mv[3];
-  if (!make_view_map(&tq, q, p->B, p->heads, c.group, p->Lq, 64, 1, mq) ||
-      !make_view_map(&tdo, dout, p->B, p->heads, c.group, p->Lq, 64, 1, mdo) ||
+  CUtensorMap tq, tdo, tk, tv, tdq;
+  int mq[3], mdo[3], mk[3], mv[3], mdq[3];
+  const int box_rows = c.pk > 1 ? p->Lq : 128;
+  if (!make_view_map(&tq, q, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mq) ||
+      !make_view_map(&tdo, dout, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mdo) ||
       !make_view_map(&tk, k, p->B, p->kv_heads, 0, p->Lk, 128, 1, mk) ||
-      !make_view_map(&tv, v, p->B, p->kv_heads, 0, p->Lk, 128, 1, mv) || !make_vec_map(&tlse, ws.lse_pad, BH, c.Lp) ||
-      !make_vec_map(&tdel, ws.delta, BH, c.Lp))
+      !make_view_map(&tv, v, p->B, p->kv_heads, 0, p->Lk, 128, 1, mv) ||
+      !make_view_map(&tdq, dq, p->B, p->heads, c.group, p->Lq, 32, 1, mdq))
     return DSA_ERR_CUDA;
   {
-    bp.qg = mq[0];
-    bp.qk = mq[1];
-    bp.qb = mq[2];
-    bp.dg = mdo[0];
-    bp.dkv = mdo[1];
-    bp.db = mdo[2];
-    bp.kh = mk[1];
-    bp.kb = mk[2];
-    bp.vh = mv[1];
-    bp.vb = mv[2];
+    kp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;
+    kp.qg = mq[0];
+    kp.qk = mq[1];
+    kp.qb = mq[2];
+    kp.dg = mdo[0];
+    kp.dkv = mdo[1];
+    kp.db = mdo[2];
+    kp.kh = mk[1];
+    kp.kb = mk[2];
+    kp.vh = mv[1];
+    kp.vb = mv[2];
     // one CTA per SM (two slots of the workspace each), no more than query chunks
-    auto kernel = dsa::bwd_bf16_kernel<true, false, true>;
-    const int64_t work = c.kv_units * c.per_unit;
+    const int64_t work = c.kv_units * c.tiles;
     unsigned grid = 0;
-    st = persistent_grid(kernel, dsa::bwd::kSmemBytes, 0, work < kPlanSms ? work : kPlanSms, &grid);
+    st = persistent_grid(dsa::cross_kv_kernel, dsa::crosskv::kSmemBytes, dsa::crosskv::kRegsAtLaunch,
+                         work < kPlanSms ? work : kPlanSms, &grid);
     if (st != DSA_OK) return st;
-    // pieces of a CTA's range: whole units, and one cut at either end
-    bp.n_units = static_cast<int>(grid * (work / grid / c.per_unit + 3));
-    kernel<<<grid, dsa::bwd::kThreads, dsa::bwd::kSmemBytes, s>>>(tq, tk, tv, tdo, tlse, tdel, tq, tdo, tlse, tdel, bp);
+    dsa::cross_kv_kernel<<<grid, dsa::crosskv::kThreads, dsa::crosskv::kSmemBytes, s>>>(tq, tdo, tk, tv, kp);
     st = launch_status();
     if (st != DSA_OK) return st;
-    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(bp, static_cast<int>(grid));
+    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(kp, static_cast<int>(grid));
     st = launch_status();
     if (st != DSA_OK) return st;
   }
   dsa::CrossDqParams dp;
   std::memset(&dp, 0, sizeof(dp));
-  dp.kv_len = kv_len;
-  dp.B = p->B;
-  dp.heads = p->heads;
-  dp.kv_heads = p->kv_heads;
-  dp.group = c.group;
-  dp.Lq = p->Lq;
-  dp.Lk = p->Lk;
-  dp.pk = c.pk;
-  dp.tiles = c.tiles;
-  dp.n_split = c.split_q;
-  dp.n_units = static_cast<int>(c.units * c.split_q);
-  dp.lse = ws.lse_pad;
+  static_cast<dsa::CrossShape&>(dp) = shape;
+  dp.lse = lse;
   dp.delta = ws.delta;
-  dp.ld_rows = c.Lp;
   dp.dq = static_cast<__nv_bfloat16*>(dq->data);
   copy_strides(dp.dq_s, dq);
   dp.dq_part = ws.dq_part;
   dp.scale = p->scale;
   dp.scale_log2 = p->scale * 1.4426950408889634f;
-  CUtensorMap uq, udo, udq;
-  int mdq[3];
-  const int box_rows = c.pk > 1 ? p->Lq : 128;
-  if (!make_view_map(&uq, q, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mq) ||
-      !make_view_map(&udo, dout, p->B, p->heads, c.group, p->Lq, box_rows, c.pk, mdo) ||
-      !make_view_map(&udq, dq, p->B, p->heads, c.group, p->Lq, 32, 1, mdq))
-    return DSA_ERR_CUDA;
-  dp.q_bytes = static_cast<uint32_t>(box_rows * c.pk) * 256;
+  dp.q_bytes = kp.q_bytes;
   dp.qg = mq[0];
   dp.qk = mq[1];
   dp.qb = mq[2];
@@ -577,7 +559,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   unsigned grid = 0;
   st = persistent_grid(dsa::cross_dq_kernel, dsa::crossdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
   if (st != DSA_OK) return st;
-  dsa::cross_dq_kernel<<<grid, dsa::crossdq::kThreads, dsa::crossdq::kSmemBytes, s>>>(uq, udo, tk, tv, udq, dp);
+  dsa::cross_dq_kernel<<<grid, dsa::crossdq::kThreads, dsa::crossdq::kSmemBytes, s>>>(tq, tdo, tk, tv, tdq, dp);
   st = launch_status();
   if (st != DSA_OK || c.split_q == 1) return st;
   cq.n_part = c.split_q;

@@ -50,18 +50,6 @@ struct BwdBf16Params {
   float* dk_part;
   float* dv_part;
   int64_t part_stride;
-  // cross mode: the keys are an encoder's states, Lk rows of kv head kvh of batch entry b of
-  // which the first kv_len[b] (null: Lk) count; the queries are the Nq rows of each of the
-  // `group` heads that share the kv head; LSE and D are padded to [B * heads, Lp].  The work is
-  // the 64-row query chunks of every unit (128 keys that hold some of kv head, `per_unit` query
-  // chunks each) in one sequence, cut into a range of equal length per CTA.  A unit that lies in
-  // one CTA's range is written as bf16 through the strides (batch, head, row) of dk and dv; of a
-  // unit that is cut, each CTA writes its piece's fp32 sums to slot 2 cta (its range's first
-  // piece) or 2 cta + 1 of dk_part and dv_part (128 x 128 each).
-  const int32_t* kv_len;
-  int B, kv_heads, group, per_unit;
-  int qb, qk, qg, db, dkv, dg, kb, kh, vb, vh;  // 1, or 0 for a broadcast (stride 0) dimension of q, dO, k, v
-  int64_t dk_s[3], dv_s[3];
 };
 
 namespace bwd {
@@ -126,55 +114,6 @@ struct BwdChunks {
   int row0, c0, nm, nx;
 };
 
-// Cross mode: keys of batch entry b, and its 128-key chunks.
-__device__ __forceinline__ int bwd_kv_length(const BwdBf16Params& p, int b) {
-  return p.kv_len == nullptr ? p.Lk : min(max(__ldg(p.kv_len + b), 0), p.Lk);
-}
-
-__device__ __forceinline__ int bwd_kv_chunks(const BwdBf16Params& p, int b) { return (bwd_kv_length(p, b) + 127) / 128; }
-
-// Cross mode: the CTA's range [lo, hi) of the sequence of query chunks (whole warp).
-struct BwdRange {
-  int64_t lo, hi;
-};
-
-__device__ __forceinline__ BwdRange bwd_range(const BwdBf16Params& p) {
-  int64_t units = 0;
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) units += static_cast<int64_t>(bwd_kv_chunks(p, b)) * p.kv_heads;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) units += __shfl_xor_sync(0xffffffffu, units, o);
-  const int64_t all = units * p.per_unit;
-  BwdRange r;
-  r.lo = all * blockIdx.x / gridDim.x;
-  r.hi = all * (blockIdx.x + 1) / gridDim.x;
-  return r;
-}
-
-// The k-th piece of the range: its unit (part: 1 where it is not the CTA's first piece) and query
-// chunks; nm = 0 past the end.
-__device__ __forceinline__ void bwd_piece(const BwdBf16Params& p, const BwdRange& r, int k, BwdUnit& x, BwdChunks& q) {
-  const int64_t u0 = r.lo / p.per_unit, v = u0 + k, start = k == 0 ? r.lo : v * p.per_unit;
-  q.row0 = 0;
-  q.nx = 0;
-  q.c0 = static_cast<int>(start - v * p.per_unit);
-  q.nm = static_cast<int>(max(min((v + 1) * p.per_unit, r.hi) - start, static_cast<int64_t>(0)));
-  x.ku = 0;
-  x.part = k > 0;
-  x.bh = x.kt = 0;
-  if (q.nm == 0) return;
-  int64_t rem = v;
-  for (int b = 0; b < p.B; ++b) {
-    const int c = bwd_kv_chunks(p, b);
-    const int64_t n = static_cast<int64_t>(c) * p.kv_heads;
-    if (rem < n) {
-      x.bh = b * p.kv_heads + static_cast<int>(rem / c);
-      x.kt = static_cast<int>(rem % c);
-      return;
-    }
-    rem -= n;
-  }
-}
-
 template <bool kFlatK, bool kExtra>
 __device__ __forceinline__ BwdChunks bwd_chunks(const BwdBf16Params& p, const BwdUnit& x) {
   BwdChunks q;
@@ -201,32 +140,6 @@ __device__ __forceinline__ int bwd_qvalid(const BwdBf16Params& p, const BwdChunk
   if (!kFlatK && !kExtra) return 64;
   if (c < q.nm) return kFlatK ? min(p.Nq - 64 * (q.c0 + c), 64) : 64;
   return min(p.Lxq - 64 * (c - q.nm), 64);
-}
-
-// Cross mode: 32 queries' P^T = exp2(S^T * scale * log2 e - LSE_n * log2 e) and dS^T = P^T (dP^T -
-// D_n), packed to bf16, in paired fp32 arithmetic.
-__device__ __forceinline__ void cross_p_ds(const uint32_t (&sr)[32], const uint32_t (&dr)[32], const float4* lse4,
-                                           const float4* dd4, float scale_log2, uint32_t (&pk)[16],
-                                           uint32_t (&ds)[16]) {
-  const float kLog2e = 1.4426950408889634f;
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    const float4 lv = lse4[g], dv = dd4[g];
-    const float nl[4] = {lv.x * -kLog2e, lv.y * -kLog2e, lv.z * -kLog2e, lv.w * -kLog2e};
-    const float dd[4] = {-dv.x, -dv.y, -dv.z, -dv.w};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int n0 = 4 * g + 2 * e;
-      float x0, x1, a0, a1, d0, d1;
-      ffma2(x0, x1, __uint_as_float(sr[n0]), __uint_as_float(sr[n0 + 1]), scale_log2, scale_log2, nl[2 * e],
-            nl[2 * e + 1]);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      fadd2(a0, a1, __uint_as_float(dr[n0]), __uint_as_float(dr[n0 + 1]), dd[2 * e], dd[2 * e + 1]);
-      ffma2(d0, d1, a0, a1, p0, p1, 0.f, 0.f);
-      pk[2 * g + e] = pack_bf16x2(p0, p1);
-      ds[2 * g + e] = pack_bf16x2(d0, d1);
-    }
-  }
 }
 
 __device__ __forceinline__ int64_t chunk_row_token(int r, int t0, int h0, int w0, int th, int tw, int H, int W) {
@@ -334,12 +247,7 @@ __global__ void __launch_bounds__(256) bwd_kv_combine(const float* __restrict__ 
 // the end of either load as zeros and get P = dS = 0, and their gradients are not written.
 // kExtra: extra queries (p.Lxq of them, flat maps tmQx, tmDOx, tmLsex, tmDx) follow every
 // unit's own.
-// kCross (with kFlatK): the keys are an encoder's states that the heads of a group share; a
-// unit walks the query chunks of every head of the group, so the shared head's gradient is
-// summed in one accumulator.  Rank-5 maps (channel, row, head in the group, kv head, batch) of
-// q and dO, rank-4 maps of k and v.  Keys past the batch entry's length may hold anything:
-// their P and dS are set to zero rather than computed.
-template <bool kFlatK, bool kExtra, bool kCross = false>
+template <bool kFlatK, bool kExtra>
 __global__ void __launch_bounds__(bwd::kThreads, 1)
     bwd_bf16_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -409,17 +317,6 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  BwdRange range = {0, 0};
-  if constexpr (kCross) range = bwd_range(p);
-  // the CTA's unit u: (batch, head) and keys, and its query chunks
-  auto unit_of = [&](int u, BwdUnit& x, BwdChunks& q) {
-    if constexpr (kCross) {
-      bwd_piece(p, range, (u - static_cast<int>(blockIdx.x)) / static_cast<int>(gridDim.x), x, q);
-    } else {
-      x = bwd_unit<kFlatK>(p, u);
-      q = bwd_chunks<kFlatK, kExtra>(p, x);
-    }
-  };
   const uint32_t tDV = tmem, tDK = tmem + 128, tS = tmem + 256, tDP = tmem + 384;
 
   if (warp == kProducerWarp) {
@@ -428,22 +325,15 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       int ld = 0, uc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        BwdUnit x;
-        BwdChunks qc;
-        unit_of(u, x, qc);
+        const BwdUnit x = bwd_unit<kFlatK>(p, u);
+        const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, x);
         const int bh = x.bh, n = qc.nm + qc.nx;
-        const int b = kCross ? bh / p.kv_heads : 0, kvh = kCross ? bh % p.kv_heads : 0;
         if (n == 0) continue;
         ok = mbar_wait(kv_free, (uc & 1) ^ 1, abort, 50);
         if (!ok) break;
         ++uc;
         mbar_arrive_expect_tx(kv_full, 2 * kKBytes);
-        if constexpr (kCross) {
-          tma_load_4d(smem + kOffK, &tmK, kv_full, 0, 128 * x.kt, kvh * p.kh, b * p.kb);
-          tma_load_4d(smem + kOffK + kKHalf, &tmK, kv_full, 64, 128 * x.kt, kvh * p.kh, b * p.kb);
-          tma_load_4d(smem + kOffV, &tmV, kv_full, 0, 128 * x.kt, kvh * p.vh, b * p.vb);
-          tma_load_4d(smem + kOffV + kKHalf, &tmV, kv_full, 64, 128 * x.kt, kvh * p.vh, b * p.vb);
-        } else if constexpr (kFlatK) {  // rows past Lk load as zeros
+        if constexpr (kFlatK) {  // rows past Lk load as zeros
           tma_load_3d(smem + kOffK, &tmK, kv_full, 0, 128 * x.kt, bh);
           tma_load_3d(smem + kOffK + kKHalf, &tmK, kv_full, 64, 128 * x.kt, bh);
           tma_load_3d(smem + kOffV, &tmV, kv_full, 0, 128 * x.kt, bh);
@@ -456,31 +346,13 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
           tma_load_5d(smem + kOffV, &tmV, kv_full, 0, k_w0, k_h0, k_t0, bh);
           tma_load_5d(smem + kOffV + kKHalf, &tmV, kv_full, 64, k_w0, k_h0, k_t0, bh);
         }
-        int hg = 0, hc = 0, hn = 1;  // cross mode: head in the group, chunk within the head, chunks per head
-        if constexpr (kCross) {
-          hn = (p.Nq + 63) / 64;
-          hg = qc.c0 / hn;
-          hc = qc.c0 % hn;
-        }
         for (int c = 0; c < n && ok; ++c, ++ld) {
           const int st = ld % kStages;
           ok = mbar_wait(ld_empty + st, ((ld / kStages) & 1) ^ 1, abort, 51);
           if (!ok) break;
           uint8_t* dst = smem + kOffStage + st * kStageBytes;
           mbar_arrive_expect_tx(ld_full + st, 2 * kQBytes + 512);
-          if constexpr (kCross) {
-            const int row = 64 * hc;
-            tma_load_5d(dst, &tmQ, ld_full + st, 0, row, hg * p.qg, kvh * p.qk, b * p.qb);
-            tma_load_5d(dst + kQHalf, &tmQ, ld_full + st, 64, row, hg * p.qg, kvh * p.qk, b * p.qb);
-            tma_load_5d(dst + kQBytes, &tmDO, ld_full + st, 0, row, hg * p.dg, kvh * p.dkv, b * p.db);
-            tma_load_5d(dst + kQBytes + kQHalf, &tmDO, ld_full + st, 64, row, hg * p.dg, kvh * p.dkv, b * p.db);
-            tma_load_2d(dst + 2 * kQBytes, &tmLse, ld_full + st, row, bh * p.group + hg);
-            tma_load_2d(dst + 2 * kQBytes + 512, &tmD, ld_full + st, row, bh * p.group + hg);
-            if (++hc == hn) {
-              hc = 0;
-              ++hg;
-            }
-          } else if ((kExtra && c >= qc.nm) || kFlatK) {  // flat rows (past the end: zeros)
+          if ((kExtra && c >= qc.nm) || kFlatK) {  // flat rows (past the end: zeros)
             const bool extra = c >= qc.nm;
             const int row = extra ? 64 * (c - qc.nm) : 64 * (qc.c0 + c);
             const CUtensorMap* mq = extra ? &tmQx : &tmQ;
@@ -515,9 +387,7 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       int ld = 0, uc = 0, sc = 0, pc = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        BwdUnit x;
-        BwdChunks qc;
-        unit_of(u, x, qc);
+        const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, bwd_unit<kFlatK>(p, u));
         const int n = qc.nm + qc.nx;
         if (n == 0) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(kv_full, uc & 1, abort, 60));
@@ -584,26 +454,13 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
     int cc = 0, ld = 0, uc = 0;
     bool ok = true;
     for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-      BwdUnit x;
-      BwdChunks qc;
-      unit_of(u, x, qc);
+      const BwdUnit x = bwd_unit<kFlatK>(p, u);
+      const BwdChunks qc = bwd_chunks<kFlatK, kExtra>(p, x);
       const int n = qc.nm + qc.nx;
-      if (kCross && n == 0) break;  // past the CTA's range
       // flat keys: this thread's key row may lie past the end (zeros, no gradient)
-      int hc = 0, hn = 1;  // cross mode: the chunk within its head, chunks per head
-      if constexpr (kCross) {
-        hn = (p.Nq + 63) / 64;
-        hc = qc.c0 % hn - 1;
-      }
-      const bool k_ok = !kFlatK || 128 * x.kt + m < (kCross ? bwd_kv_length(p, x.bh / p.kv_heads) : p.Lk);
+      const bool k_ok = !kFlatK || 128 * x.kt + m < p.Lk;
       for (int c = 0; c < n; ++c, ++cc, ++ld) {
-        int nvq;  // valid queries of this half
-        if constexpr (kCross) {
-          hc = hc + 1 == hn ? 0 : hc + 1;
-          nvq = min(p.Nq - 64 * hc, 64) - 32 * h;
-        } else {
-          nvq = bwd_qvalid<kFlatK, kExtra>(p, qc, c) - 32 * h;
-        }
+        const int nvq = bwd_qvalid<kFlatK, kExtra>(p, qc, c) - 32 * h;  // valid queries of this half
         const bool masked = !k_ok || nvq < 32;  // P = dS = 0 for missing keys and queries
         const int b = cc & 1;
         ok = mbar_wait(s_full + b, (cc >> 1) & 1, abort, 70);
@@ -618,18 +475,6 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
         tmem_ld32_wait(tS + lane_off + b * 64 + 32 * h, sr);
         tmem_ld32_wait(tDP + lane_off + b * 64 + 32 * h, dr);
         uint32_t pk[16], dk2[16];
-        if constexpr (kCross) {
-          cross_p_ds(sr, dr, lse4, dd4, p.scale_log2, pk, dk2);
-          if (__any_sync(0xffffffffu, masked)) {  // a padding key's P and dP may be anything: both are zero
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int nv = k_ok ? nvq - 2 * e : 0;
-              const uint32_t keep = nv >= 2 ? 0xffffffffu : nv == 1 ? 0xffffu : 0u;
-              pk[e] &= keep;
-              dk2[e] &= keep;
-            }
-          }
-        } else
 #pragma unroll
         for (int g = 0; g < 8; ++g) {  // queries 32h + 4g .. 32h + 4g + 3
           const float4 lv = lse4[g], dv = dd4[g];
@@ -675,15 +520,9 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
       __nv_bfloat16* outp = h ? p.dk : p.dv;
       const float sc_out = h ? p.scale : 1.f;
       uint4* dst = reinterpret_cast<uint4*>(outp + (slice + ktok) * 128);
-      if constexpr (kCross) {
-        const int64_t* s = h ? p.dk_s : p.dv_s;
-        dst = reinterpret_cast<uint4*>(outp + (x.bh / p.kv_heads) * s[0] + (x.bh % p.kv_heads) * s[1] + ktok * s[2]);
-      }
       float4* dstp = nullptr;
       if constexpr (kFlatK) {
-        const int64_t o = kCross ? (2 * static_cast<int64_t>(blockIdx.x) + x.part) * 16384 + m * 128
-                                 : static_cast<int64_t>(x.part) * p.part_stride +
-                                       (static_cast<int64_t>(x.bh) * p.Lk + ktok) * 128;
+        const int64_t o = static_cast<int64_t>(x.part) * p.part_stride + (static_cast<int64_t>(x.bh) * p.Lk + ktok) * 128;
         dstp = reinterpret_cast<float4*>((h ? p.dk_part : p.dv_part) + o);
       }
       if (n > 0) {
@@ -701,20 +540,14 @@ __global__ void __launch_bounds__(bwd::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) a[j] = 0u;
         }
-        if constexpr (kCross) {
-          if (!k_ok) {  // padding: no gradient
-#pragma unroll
-            for (int j = 0; j < 32; ++j) a[j] = 0u;
-          }
-        }
-        if (kFlatK && (!kCross || n < p.per_unit)) {
-          if (k_row_ok && (!kCross || k_ok)) {
+        if constexpr (kFlatK) {
+          if (k_row_ok) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               dstp[g * 8 + j] = make_float4(__uint_as_float(a[4 * j]), __uint_as_float(a[4 * j + 1]),
                                             __uint_as_float(a[4 * j + 2]), __uint_as_float(a[4 * j + 3]));
           }
-        } else if (k_row_ok) {
+        } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint4 y;

@@ -39,9 +39,8 @@
 namespace dsa {
 
 struct CrossDqParams : CrossShape {
-  const float* lse;    // [B * heads, ld_rows]
+  const float* lse;    // [B, heads, Lq]
   const float* delta;
-  int ld_rows;
   __nv_bfloat16* dq;   // through strides (batch, head, row)
   int64_t dq_s[3];
   float* dq_part;      // n_split > 1: [n_split, B * heads * Lq, 128]
@@ -61,6 +60,8 @@ constexpr uint32_t kSmemUsed = kOffBar + 256;
 constexpr uint32_t kSmemBytes = 227 * 1024;
 static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
 using Cur = crossf::Cursor<128>;
+// column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
+constexpr uint32_t kPolyMask = 0x22u;
 
 // A lane's row (32 q + lane, 256 bytes in two swizzled 64-channel halves at `tile`) into TMEM as
 // packed bf16 pairs.
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
         }
         continue;
       }
-      const int64_t lrow = bh * p.ld_rows + y.q;
+      const int64_t lrow = bh * p.Lq + y.q;
       const float neg_lse2 = y.ok ? -p.lse[lrow] * kLog2e : 0.f, dd = y.ok ? p.delta[lrow] : 0.f;
       // Q (h = 0) or dO (h = 1) of the row into TMEM; the previous unit's products that read them
       // have completed: this warp has seen its last scores and dP
@@ -397,6 +398,13 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
         ok = warp_wait(s_full, G & 1, abort, 192);
         if (!ok) break;
         tc_fence_after();
+        if (stored) {  // dQ of the previous unit has left the buffer by now: Q may be loaded
+          if (lane == 0) {
+            tma_store_wait_read();
+            mbar_arrive(q_free);
+          }
+          stored = false;
+        }
         float pf[64];
         {
           uint32_t s[64];
@@ -409,16 +417,13 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
             float x0, x1;
             ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), p.scale_log2, p.scale_log2, neg_lse2,
                   neg_lse2);
-            pf[e] = ex2_approx(x0);
-            pf[e + 1] = ex2_approx(x1);
+            if ((kPolyMask >> (e / 2 & 7)) & 1u) {
+              exp2_poly2(x0, x1, pf[e], pf[e + 1]);
+            } else {
+              pf[e] = ex2_approx(x0);
+              pf[e + 1] = ex2_approx(x1);
+            }
           }
-        }
-        if (stored) {  // dQ of the previous unit has left the buffer by now: Q may be loaded
-          if (lane == 0) {
-            tma_store_wait_read();
-            mbar_arrive(q_free);
-          }
-          stored = false;
         }
         ok = warp_wait(dp_full, G & 1, abort, 193);
         if (!ok) break;
