@@ -232,14 +232,16 @@ bool vec_ok(const void* ptr, int64_t ld, const dsa_norm_t* p) {
 }
 
 struct NormShape {
-  int NV, W, R;  // vectors per thread, warps per row, rows per block
+  int NV, tpr, R;  // vectors per thread, threads per row, rows per block
 };
 
 // Fewest idle lanes; among equals the widest NV up to nv_pref (fewer warps meet at the row's
 // barrier).
 NormShape norm_shape(int C, int nv_pref, int threads) {
   const int nvec = (C + dsa::norm::kVec - 1) / dsa::norm::kVec;
-  NormShape best = {0, 0, 0};
+  NormShape best = {1, 16, threads / 16};
+  if (nvec <= 16) return best;  // up to 128 channels: two rows to a warp
+  best.NV = 0;
   int waste = INT32_MAX;
   for (int pass = 0; pass < 2 && best.NV == 0; ++pass) {
     for (int nv = pass == 0 ? nv_pref : dsa::norm::kMaxNV; nv >= 1; --nv) {
@@ -249,17 +251,17 @@ NormShape norm_shape(int C, int nv_pref, int threads) {
       if (idle < waste) {
         waste = idle;
         best.NV = nv;
-        best.W = W;
+        best.tpr = 32 * W;
       }
     }
   }
-  best.R = threads / (32 * best.W) > 1 ? threads / (32 * best.W) : 1;
+  best.R = threads / best.tpr > 1 ? threads / best.tpr : 1;
   return best;
 }
 
 template <typename T, bool kFp8>
 dsa_status_t launch_norm(const dsa::NormParams& np, const NormShape& sh, bool vec, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((np.rows + sh.R - 1) / sh.R), threads = 32 * sh.W * sh.R;
+  const unsigned grid = static_cast<unsigned>((np.rows + sh.R - 1) / sh.R), threads = sh.tpr * sh.R;
 #define DSA_NORM_CASE(NV)                                                              \
   case NV:                                                                             \
     if (vec)                                                                           \
@@ -302,7 +304,7 @@ dsa_status_t norm_fwd(const dsa_norm_t* p, const void* x, int64_t x_ld, const vo
   np.C = p->C;
   np.eps = p->eps;
   const NormShape sh = norm_shape(p->C, 4, 256);
-  np.W = sh.W;
+  np.tpr = sh.tpr;
   const bool vec = p->C % 8 == 0 && vec_ok(x, x_ld, p) && vec_ok(r, r_ld, p) && vec_ok(w, 0, p) && vec_ok(h, 0, p) &&
                    (fp8 ? aligned(y, 8) : aligned(y, 16));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -311,33 +313,71 @@ dsa_status_t norm_fwd(const dsa_norm_t* p, const void* x, int64_t x_ld, const vo
   return fp8 ? launch_norm<float, true>(np, sh, vec, s) : launch_norm<float, false>(np, sh, vec, s);
 }
 
-// Blocks of the persistent backward: at most this many per-block partial dw.
-unsigned norm_bwd_blocks(const dsa_norm_t* p, const NormShape& sh) {
-  const int64_t groups = (p->rows + sh.R - 1) / sh.R;
-  const int threads = 32 * sh.W * sh.R, per_sm = threads > 256 ? (threads > 384 ? 1 : 2) : 3;
-  return static_cast<unsigned>(groups < per_sm * kPlanSms ? groups : per_sm * kPlanSms);
+// The backward's launch: block shape, blocks (each with a partial dw), and the stages of the
+// shared-memory ring for `tensors` inputs (0: they do not fit twice, the kernel loads directly).
+// Resident blocks: what 88 registers a thread allow, up to four, and each with two stages or more
+// (both sides of these are measured beside the kernel).
+struct NormBwdShape {
+  NormShape sh;
+  int blocks_per_sm, stages, J;
+  size_t smem;
+  unsigned grid;
+};
+
+NormBwdShape norm_bwd_shape(const dsa_norm_t* p, int tensors, bool vec) {
+  NormBwdShape b;
+  b.sh = norm_shape(p->C, 2, 256);
+  const size_t elem = p->dtype == DSA_BF16 ? 2 : 4, rows = elem * p->C * tensors * b.sh.R;
+  // rows within a warp: as many per thread and iteration as make a stage of about 24 KB
+  b.J = 1;
+  while (b.sh.tpr <= 32 && b.J < 16 && 2 * b.J * rows <= 24 * 1024) b.J *= 2;
+  const size_t stage = b.J * rows;
+  const int threads = b.sh.tpr * b.sh.R;
+  b.stages = 0;
+  b.blocks_per_sm = threads > 336 ? 1 : threads > 224 ? 2 : threads > 168 ? 3 : 4;
+  for (int n = b.blocks_per_sm; n >= 1 && vec && b.stages == 0; --n) {
+    const size_t room = size_t(220) * 1024 / n, need = 2048 + elem * p->C + 2 * stage;
+    if (room < need) continue;
+    const size_t fit = 2 + (room - need) / stage;
+    b.stages = static_cast<int>(fit < dsa::norm::kMaxStages ? fit : dsa::norm::kMaxStages);
+    b.blocks_per_sm = n;
+  }
+  const size_t dw = b.sh.R > 1 ? sizeof(float) * p->C : 0;  // the row slots' sums meet here
+  const size_t ring = b.stages > 0 ? b.stages * stage + elem * p->C : 0;  // and the weight
+  b.smem = ring > dw ? ring : dw;
+  const int64_t G = static_cast<int64_t>(b.sh.R) * b.J, groups = (p->rows + G - 1) / G;
+  b.grid = static_cast<unsigned>(groups < b.blocks_per_sm * kPlanSms ? groups : b.blocks_per_sm * kPlanSms);
+  return b;
+}
+
+template <typename T, int NV, bool kDw, bool kWarpRow>
+dsa_status_t launch_norm_bwd_nv(const dsa::NormBwdParams& np, const NormBwdShape& b, bool vec, cudaStream_t s) {
+  const unsigned threads = b.sh.tpr * b.sh.R;
+  if (b.stages > 0) {
+    auto kernel = dsa::rmsnorm_bwd_kernel<T, NV, true, kDw, true, kWarpRow>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(b.smem)) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    kernel<<<b.grid, threads + 32, b.smem, s>>>(np);
+  } else if (vec) {
+    // (rows within a warp always fit the ring)
+    if constexpr (!kWarpRow)
+      dsa::rmsnorm_bwd_kernel<T, NV, true, kDw, false, false><<<b.grid, threads, b.smem, s>>>(np);
+  } else {
+    dsa::rmsnorm_bwd_kernel<T, NV, false, kDw, false, kWarpRow><<<b.grid, threads, b.smem, s>>>(np);
+  }
+  return launch_status();
 }
 
 template <typename T, bool kDw>
-dsa_status_t launch_norm_bwd(const dsa::NormBwdParams& np, const NormShape& sh, unsigned grid, bool vec,
-                             cudaStream_t s) {
-  const unsigned threads = 32 * sh.W * sh.R;
-  const size_t smem = kDw && sh.R > 1 ? sizeof(float) * np.C : 0;
-#define DSA_NORM_CASE(NV)                                                              \
-  case NV:                                                                             \
-    if (vec)                                                                           \
-      dsa::rmsnorm_bwd_kernel<T, NV, true, kDw><<<grid, threads, smem, s>>>(np);       \
-    else                                                                               \
-      dsa::rmsnorm_bwd_kernel<T, NV, false, kDw><<<grid, threads, smem, s>>>(np);      \
-    break;
-  switch (sh.NV) {
-    DSA_NORM_CASE(1)
-    DSA_NORM_CASE(2)
-    DSA_NORM_CASE(3)
-    DSA_NORM_CASE(4)
+dsa_status_t launch_norm_bwd(const dsa::NormBwdParams& np, const NormBwdShape& b, bool vec, cudaStream_t s) {
+  if (b.sh.tpr <= 32)  // at most two vectors a thread
+    return b.sh.NV == 1 ? launch_norm_bwd_nv<T, 1, kDw, true>(np, b, vec, s) : launch_norm_bwd_nv<T, 2, kDw, true>(np, b, vec, s);
+  switch (b.sh.NV) {
+    case 1: return launch_norm_bwd_nv<T, 1, kDw, false>(np, b, vec, s);
+    case 2: return launch_norm_bwd_nv<T, 2, kDw, false>(np, b, vec, s);
+    case 3: return launch_norm_bwd_nv<T, 3, kDw, false>(np, b, vec, s);
+    default: return launch_norm_bwd_nv<T, 4, kDw, false>(np, b, vec, s);
   }
-#undef DSA_NORM_CASE
-  return launch_status();
 }
 
 }  // namespace
@@ -687,7 +727,9 @@ dsa_status_t dsa_rmsnorm_fp8(const dsa_norm_t* p, const void* x, int64_t x_ld, c
 
 size_t dsa_rmsnorm_bwd_workspace_size(const dsa_norm_t* p) {
   if (check_norm(p) != DSA_OK) return 0;
-  return round_up(sizeof(float) * norm_bwd_blocks(p, norm_shape(p->C, 2, 256)) * static_cast<size_t>(p->C), kAlign);
+  // the most blocks any of its forms launches (four per SM, or one per row group)
+  const int64_t groups = p->rows < 4 * kPlanSms ? p->rows : 4 * kPlanSms;
+  return round_up(sizeof(float) * static_cast<size_t>(groups > 0 ? groups : 1) * p->C, kAlign);
 }
 
 dsa_status_t dsa_rmsnorm_bwd(const dsa_norm_t* p, const void* h, int64_t h_ld, const void* weight, const void* dy,
@@ -702,8 +744,9 @@ dsa_status_t dsa_rmsnorm_bwd(const dsa_norm_t* p, const void* h, int64_t h_ld, c
       !aligned(dweight, elem))
     return DSA_ERR_INVALID_ARG;
   if (p->rows > 0 && (!h || !dy || !dx)) return DSA_ERR_INVALID_ARG;
-  const NormShape sh = norm_shape(p->C, 2, 256);
-  const unsigned grid = norm_bwd_blocks(p, sh);
+  const bool vec = p->C % 8 == 0 && vec_ok(h, h_ld, p) && vec_ok(dy, dy_ld, p) && vec_ok(dh, dh_ld, p) &&
+                   vec_ok(weight, 0, p) && vec_ok(dx, 0, p);
+  const NormBwdShape b = norm_bwd_shape(p, dh != nullptr ? 3 : 2, vec);
   if (dweight != nullptr && p->rows > 0 &&
       (workspace == nullptr || ws_bytes < dsa_rmsnorm_bwd_workspace_size(p) || !aligned(workspace, kAlign)))
     return DSA_ERR_WORKSPACE;
@@ -722,25 +765,23 @@ dsa_status_t dsa_rmsnorm_bwd(const dsa_norm_t* p, const void* h, int64_t h_ld, c
     np.dy_ld = dy_ld;
     np.dh_ld = dh_ld;
     np.C = p->C;
-    np.W = sh.W;
+    np.tpr = b.sh.tpr;
+    np.J = b.J;
+    np.stages = b.stages;
     np.eps = p->eps;
-    const bool vec = p->C % 8 == 0 && vec_ok(h, h_ld, p) && vec_ok(dy, dy_ld, p) && vec_ok(dh, dh_ld, p) &&
-                     vec_ok(weight, 0, p) && vec_ok(dx, 0, p);
     if (p->dtype == DSA_BF16)
-      st = dweight ? launch_norm_bwd<__nv_bfloat16, true>(np, sh, grid, vec, s)
-                   : launch_norm_bwd<__nv_bfloat16, false>(np, sh, grid, vec, s);
+      st = dweight ? launch_norm_bwd<__nv_bfloat16, true>(np, b, vec, s) : launch_norm_bwd<__nv_bfloat16, false>(np, b, vec, s);
     else
-      st = dweight ? launch_norm_bwd<float, true>(np, sh, grid, vec, s)
-                   : launch_norm_bwd<float, false>(np, sh, grid, vec, s);
+      st = dweight ? launch_norm_bwd<float, true>(np, b, vec, s) : launch_norm_bwd<float, false>(np, b, vec, s);
     if (st != DSA_OK) return st;
   }
   if (dweight == nullptr) return DSA_OK;
   const unsigned blocks = static_cast<unsigned>((p->C + 31) / 32);
   if (p->dtype == DSA_BF16)
-    dsa::rmsnorm_dw_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(part, static_cast<int>(grid), p->C,
+    dsa::rmsnorm_dw_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(part, static_cast<int>(b.grid), p->C,
                                                                  static_cast<__nv_bfloat16*>(dweight));
   else
-    dsa::rmsnorm_dw_kernel<float><<<blocks, 256, 0, s>>>(part, static_cast<int>(grid), p->C,
+    dsa::rmsnorm_dw_kernel<float><<<blocks, 256, 0, s>>>(part, static_cast<int>(b.grid), p->C,
                                                          static_cast<float*>(dweight));
   return launch_status();
 }

@@ -10,16 +10,18 @@
 // the unrounded sum x + r, which is also what h rounds.
 //
 // Bound by memory: a row is read once, kept in registers (kVec = 8 consecutive channels per
-// thread and vector, NV vectors per thread, W warps per row) while its sums are taken, and
-// written from there.  C channels are ceil(C / 8) vectors; vector i * 32 W + t belongs to
-// thread t of the row, so a warp's loads are contiguous and a group of 128 channels is 16
-// consecutive lanes.  Rows whose address, length or stride is not a multiple of 16 bytes go
+// thread and vector, NV vectors per thread, tpr threads per row: whole warps, or 16 lanes up to
+// 128 channels) while its sums are taken, and written from there.  C channels are ceil(C / 8)
+// vectors; vector i * tpr + t belongs to thread t of the row, so a warp's loads are contiguous and
+// a group of 128 channels is 16 consecutive lanes.  Rows whose address, length or stride is not a multiple of 16 bytes go
 // through the same kernel with element-wise loads (kAligned = false).
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <stdint.h>
+
+#include "sm100.cuh"
 
 namespace dsa {
 namespace norm {
@@ -28,7 +30,9 @@ constexpr int kVec = 8;        // channels per vector
 constexpr int kMaxNV = 4;      // vectors per thread
 constexpr int kMaxWarps = 16;  // warps per row: C <= 16 * 32 * 4 * 8 = 16384
 constexpr int kMaxC = kMaxWarps * 32 * kMaxNV * kVec;
+constexpr int kMaxRows = 8;    // rows of several warps per block
 constexpr int kGroup = 128;    // channels per 8-bit scale
+constexpr int kMaxStages = 4;  // of the backward's ring
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the reciprocal of a scale stays finite
 
@@ -121,6 +125,17 @@ __device__ __forceinline__ void store8(float* row, int c, int C, const float (&v
   }
 }
 
+// The weight's channels, or ones.
+template <bool kAligned, typename T>
+__device__ __forceinline__ void load_weight(const T* w, int c, int C, float (&v)[8]) {
+  if (w != nullptr) {
+    load8<kAligned>(w, c, C, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 1.f;
+  }
+}
+
 // Eight values as e4m3 (round to nearest even, saturating; NaN stays NaN).
 template <bool kAligned>
 __device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int C, const float (&v)[8]) {
@@ -147,22 +162,30 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-__device__ __forceinline__ float warp_sum(float s) {
+// Sum over the lanes of a row within a warp (16 or 32).
+__device__ __forceinline__ float lane_sum(float s, int tpr) {
+  if (tpr > 16) s += __shfl_xor_sync(0xffffffffu, s, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
-// Sum over the W warps of a row; every thread of the block calls it.  `slot` holds one float
-// per warp of the block and is free again after the next __syncthreads.
-__device__ __forceinline__ float row_sum(float s, int W, float* slot) {
-  s = warp_sum(s);
-  if (W == 1) return s;
-  const int warp = threadIdx.x >> 5, first = warp / W * W;
-  if ((threadIdx.x & 31) == 0) slot[warp] = s;
-  __syncthreads();
+// One sum per warp of a row: rows of kMaxWarps floats, those that no warp writes zero.
+using Slots = float[kMaxRows][kMaxWarps];
+
+__device__ __forceinline__ void clear_slots(Slots& s) {
+  for (int i = threadIdx.x; i < kMaxRows * kMaxWarps; i += blockDim.x) (&s[0][0])[i] = 0.f;
+}
+
+// The sum over a row's warps, in order (four at a time; a loop over the warps took longer than
+// the rest of the reduction).
+__device__ __forceinline__ float slot_sum(const float (&s)[kMaxWarps]) {
   float t = 0.f;
-  for (int i = 0; i < W; ++i) t += slot[first + i];
+#pragma unroll
+  for (int i = 0; i < kMaxWarps / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(s)[i];
+    t += (v.x + v.y) + (v.z + v.w);
+  }
   return t;
 }
 }  // namespace norm
@@ -175,21 +198,25 @@ struct NormParams {
   void* h;         // [rows, C] x + r (with a residual)
   float* scales;   // 8 bits: [rows, ceil(C / 128)]
   int64_t rows, x_ld, r_ld;  // row strides of x and r in elements; y and h are contiguous
-  int C, W;        // W warps per row
+  int C, tpr;      // tpr threads per row
   float eps;
 };
 
-// A block takes blockDim / (32 W) rows.
+// A block takes blockDim / tpr rows.
 template <typename T, int NV, bool kAligned, bool kFp8>
 __global__ void __launch_bounds__(512) rmsnorm_kernel(NormParams p) {
   using namespace norm;
-  __shared__ float slot[kMaxWarps];
-  const int tpr = 32 * p.W, t = threadIdx.x % tpr;
+  __shared__ __align__(16) Slots slot;
+  const int tpr = p.tpr, t = threadIdx.x % tpr;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const bool live = row < p.rows;
   const int64_t row0 = live ? row : 0;
   const T* x = static_cast<const T*>(p.x) + row0 * p.x_ld;
   const T* r = p.r != nullptr ? static_cast<const T*>(p.r) + row0 * p.r_ld : nullptr;
+  if (tpr > 32) {
+    clear_slots(slot);
+    __syncthreads();
+  }
   // every load of the row before its first store: h may be the residual's or x's own buffer, so
   // the compiler keeps loads behind stores
   Raw8<T> xr[NV], rr[NV];
@@ -224,8 +251,13 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(NormParams p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
   }
-  ss = row_sum(ss, p.W, slot);
-  const float rho = 1.f / sqrtf(ss / static_cast<float>(p.C) + p.eps);
+  ss = lane_sum(ss, tpr);
+  if (tpr > 32) {
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x / tpr][t >> 5] = ss;
+    __syncthreads();
+    ss = slot_sum(slot[threadIdx.x / tpr]);
+  }
+  const float rho = rsqrtf(ss / static_cast<float>(p.C) + p.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = kVec * (i * tpr + t);
@@ -272,116 +304,200 @@ struct NormBwdParams {
   void* dx;         // [rows, C]
   float* dw_part;   // [gridDim.x, C] sums over the block's rows, or null
   int64_t rows, h_ld, dy_ld, dh_ld;
-  int C, W;
+  int C, tpr;
+  int J;            // rows per thread and iteration (1 unless a row is within a warp)
+  int stages;       // ring form: stages of the shared-memory ring
   float eps;
 };
 
-// Persistent: block b takes row groups b, b + gridDim.x, ...; each thread keeps the sums of
+// Persistent: block b takes row groups (J rows for each of its R row slots) b, b + gridDim.x, ...;
+// each thread keeps the sums of
 // its channels' dw over the rows it sees in registers, so dw needs no atomics: the block's row
 // slots add theirs in order at the end, and rmsnorm_dw_kernel adds the blocks' in order.
-template <typename T, int NV, bool kAligned, bool kDw>
-__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(NormBwdParams p) {
+//
+// kRing (aligned rows, of which the ring holds two groups or more): one more warp brings the
+// block's rows through a ring of bulk copies into shared memory, so the next row groups are in
+// flight while one is worked on; the rows are read from there twice, for the sums and for the
+// outputs, so nothing of a row stays in registers and two blocks of 352 threads share an SM.
+// (35840 x 5120 bf16 with dh: 299 us with loads at the head of each iteration, 355 us prefetching
+// into registers, 262 to 301 us from a ring that the working warps fill themselves.)  Without the
+// ring the second reading comes from L1 or L2.
+// kWarpRow: a row is within a warp (tpr <= 32), J rows per thread and iteration; else J = 1.
+// (The launch bounds stand for 88 and 120 registers.)
+template <typename T, int NV, bool kAligned, bool kDw, bool kRing, bool kWarpRow>
+__global__ void __launch_bounds__(NV <= 2 ? 736 : 544) rmsnorm_bwd_kernel(NormBwdParams p) {
   using namespace norm;
-  __shared__ float slot[2][2][kMaxWarps];  // [iteration parity][sum][warp]
-  extern __shared__ float dw_smem[];       // kDw and several rows per block: [C]
-  const int tpr = 32 * p.W, t = threadIdx.x % tpr, R = blockDim.x / tpr, rs = threadIdx.x / tpr;
+  __shared__ __align__(16) Slots slot[2][2];  // [iteration parity][sum]
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ int abort;
+  // ring: [C] T of the weight, [stages][h, dy, dh][J R rows][C] T; kDw with several rows per block:
+  // [C] floats at the end
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const int workers = kRing ? blockDim.x - 32 : blockDim.x;
+  const int tpr = p.tpr, R = workers / tpr;
   const T* w = static_cast<const T*>(p.w);
+  const int G = kWarpRow ? R * p.J : R;  // rows of a group
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  const int n_tens = p.dh != nullptr ? 3 : 2;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.C) * sizeof(T);
+  uint8_t* ring = norm_smem + (w != nullptr ? row_bytes : 0u);
+  if constexpr (!kWarpRow) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) clear_slots(slot[i >> 1][i & 1]);
+    __syncthreads();
+  }
+  if constexpr (kRing) {
+    if (w != nullptr) {
+      for (uint32_t i = threadIdx.x; i < row_bytes / 16; i += blockDim.x)
+        reinterpret_cast<uint4*>(norm_smem)[i] = reinterpret_cast<const uint4*>(w)[i];
+      w = reinterpret_cast<const T*>(norm_smem);
+    }
+    if (threadIdx.x == 0) {
+      abort = 0;
+      for (int i = 0; i < p.stages; ++i) {
+        mbar_init(full + i, 1);
+        mbar_init(empty + i, workers / 32);
+      }
+      fence_mbar_init();
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) >= workers) {
+      // the loading warp: per tensor one copy where its rows follow one another in memory, else
+      // one per row
+      const int lane = threadIdx.x & 31;
+      int st = 0, phase = 1;
+      for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * G; r0 < p.rows; r0 += step) {
+        const int n = static_cast<int>(min(static_cast<int64_t>(G), p.rows - r0));
+        if (!__all_sync(0xffffffffu, mbar_wait(empty + st, phase, &abort, 231))) break;
+        if (lane == 0) mbar_arrive_expect_tx(full + st, n * n_tens * row_bytes);
+        __syncwarp();
+        for (int k = 0; k < n_tens; ++k) {
+          const T* src = static_cast<const T*>(k == 0 ? p.h : k == 1 ? p.dy : p.dh);
+          const int64_t ld = k == 0 ? p.h_ld : k == 1 ? p.dy_ld : p.dh_ld;
+          uint8_t* dst = ring + static_cast<size_t>(st * n_tens + k) * G * row_bytes;
+          if (ld == p.C) {
+            if (lane == 0) bulk_load(dst, src + r0 * ld, n * row_bytes, full + st);
+          } else {
+            for (int r = lane; r < n; r += 32) bulk_load(dst + r * row_bytes, src + (r0 + r) * ld, row_bytes, full + st);
+          }
+        }
+        if (++st == p.stages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  }
   float acc[kDw ? NV : 1][8];
 #pragma unroll
   for (int i = 0; i < (kDw ? NV : 1); ++i) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
   }
-  int par = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * R; r0 < p.rows; r0 += static_cast<int64_t>(gridDim.x) * R, par ^= 1) {
-    const int64_t row = r0 + rs;
-    const bool live = row < p.rows;
-    const int64_t row0 = live ? row : 0;
-    const T* h = static_cast<const T*>(p.h) + row0 * p.h_ld;
-    const T* dy = static_cast<const T*>(p.dy) + row0 * p.dy_ld;
-    const T* dh = p.dh != nullptr ? static_cast<const T*>(p.dh) + row0 * p.dh_ld : nullptr;
-    Raw8<T> hr[NV], gr[NV], dr[NV];  // h, dy, dh
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = kVec * (i * tpr + t);
-      zero_raw(hr[i]);
-      zero_raw(gr[i]);
-      zero_raw(dr[i]);
-      if (live && c < p.C) {
-        load_raw<kAligned>(h, c, p.C, hr[i]);
-        load_raw<kAligned>(dy, c, p.C, gr[i]);
-        if (dh != nullptr) load_raw<kAligned>(dh, c, p.C, dr[i]);
-      }
-    }
-    float ss = 0.f, gh = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = kVec * (i * tpr + t);
-      float wv[8];
-      if (w != nullptr && c < p.C) {
-        load8<kAligned>(w, c, p.C, wv);
+  const int t = threadIdx.x % tpr, rs = threadIdx.x / tpr;
+  const float inv_c = 1.f / static_cast<float>(p.C);
+  // a failed wait (in the status word) writes nothing more, but takes part in every barrier
+  bool ok = static_cast<int>(threadIdx.x) < workers;
+  int par = 0, st = 0, phase = 0;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * G; r0 < p.rows && static_cast<int>(threadIdx.x) < workers; r0 += step) {
+    if constexpr (kRing) ok = mbar_wait(full + st, phase, &abort, 230) && ok;
+    for (int j = 0; j < (kWarpRow ? p.J : 1); ++j) {
+      const int64_t row = r0 + j * R + rs;
+      const bool live = row < p.rows;
+      const int64_t row0 = live ? row : 0;
+      const T *h, *dy, *dh;
+      if constexpr (kRing) {
+        const int tens = G * p.C;
+        h = reinterpret_cast<const T*>(ring) + st * n_tens * tens + (j * R + rs) * p.C;
+        dy = h + tens;
+        dh = n_tens == 3 ? dy + tens : nullptr;
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wv[e] = 1.f;
+        h = static_cast<const T*>(p.h) + row0 * p.h_ld;
+        dy = static_cast<const T*>(p.dy) + row0 * p.dy_ld;
+        dh = p.dh != nullptr ? static_cast<const T*>(p.dh) + row0 * p.dh_ld : nullptr;
       }
-      float hv[8], gv[8];
-      expand(hr[i], hv);
-      expand(gr[i], gv);
+      float ss2[2] = {0.f, 0.f}, gh2[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ss = fmaf(hv[e], hv[e], ss);
-        gh = fmaf(gv[e] * wv[e], hv[e], gh);
+      for (int i = 0; i < NV; ++i) {
+        const int c = kVec * (i * tpr + t);
+        if (!live || c >= p.C) continue;
+        float wv[8], hv[8], gv[8];
+        load8<kAligned>(h, c, p.C, hv);
+        load8<kAligned>(dy, c, p.C, gv);
+        load_weight<kAligned>(w, c, p.C, wv);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float g0, g1;
+          ffma2(ss2[0], ss2[1], hv[e], hv[e + 1], hv[e], hv[e + 1], ss2[0], ss2[1]);
+          ffma2(g0, g1, gv[e], gv[e + 1], wv[e], wv[e + 1], 0.f, 0.f);
+          ffma2(gh2[0], gh2[1], g0, g1, hv[e], hv[e + 1], gh2[0], gh2[1]);
+        }
+      }
+      float ss = lane_sum(ss2[0] + ss2[1], tpr), gh = lane_sum(gh2[0] + gh2[1], tpr);
+      if constexpr (!kWarpRow) {
+        // the slots alternate, so one barrier per row suffices: a warp that writes slot[par] again
+        // has passed the other parity's barrier, which every reader of slot[par] reached after
+        // reading
+        if ((threadIdx.x & 31) == 0) {
+          slot[par][0][rs][t >> 5] = ss;
+          slot[par][1][rs][t >> 5] = gh;
+        }
+        named_bar_sync(1, workers);
+        ss = slot_sum(slot[par][0][rs]);
+        gh = slot_sum(slot[par][1][rs]);
+        par ^= 1;
+      }
+      const float rho = rsqrtf(ss * inv_c + p.eps);
+      const float k = rho * rho * rho * (gh * inv_c);
+      if (!live || !ok) continue;  // no barrier follows for this row
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = kVec * (i * tpr + t);
+        if (c >= p.C) continue;
+        float wv[8], hv[8], gv[8], o[8];
+        load_weight<kAligned>(w, c, p.C, wv);
+        load8<kAligned>(h, c, p.C, hv);
+        load8<kAligned>(dy, c, p.C, gv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+        if (dh != nullptr) load8<kAligned>(dh, c, p.C, o);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          float g0, g1;
+          ffma2(g0, g1, gv[e], gv[e + 1], wv[e], wv[e + 1], 0.f, 0.f);
+          ffma2(g0, g1, g0, g1, rho, rho, o[e], o[e + 1]);
+          ffma2(o[e], o[e + 1], hv[e], hv[e + 1], -k, -k, g0, g1);
+          if constexpr (kDw) {
+            ffma2(g0, g1, hv[e], hv[e + 1], rho, rho, 0.f, 0.f);
+            ffma2(acc[i][e], acc[i][e + 1], gv[e], gv[e + 1], g0, g1, acc[i][e], acc[i][e + 1]);
+          }
+        }
+        store8<kAligned>(static_cast<T*>(p.dx) + row * p.C, c, p.C, o);
       }
     }
-    ss = warp_sum(ss);
-    gh = warp_sum(gh);
-    if (p.W > 1) {
-      // the slots alternate, so one barrier per iteration suffices: a warp that writes
-      // slot[par] again has passed the other parity's barrier, which every reader of
-      // slot[par] reached after reading
-      const int warp = threadIdx.x >> 5, first = warp / p.W * p.W;
-      if ((threadIdx.x & 31) == 0) {
-        slot[par][0][warp] = ss;
-        slot[par][1][warp] = gh;
-      }
-      __syncthreads();
-      ss = gh = 0.f;
-      for (int i = 0; i < p.W; ++i) {
-        ss += slot[par][0][first + i];
-        gh += slot[par][1][first + i];
+    if constexpr (kRing) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(empty + st);
+      if (++st == p.stages) {
+        st = 0;
+        phase ^= 1;
       }
     }
-    const float inv_c = 1.f / static_cast<float>(p.C);
-    const float rho = 1.f / sqrtf(ss * inv_c + p.eps);
-    const float k = rho * rho * rho * (gh * inv_c);
-    if (!live) continue;  // no barrier follows in this iteration
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = kVec * (i * tpr + t);
-      if (c >= p.C) continue;
-      float wv[8], hv[8], gv[8], o[8];
-      if (w != nullptr) {
-        load8<kAligned>(w, c, p.C, wv);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wv[e] = 1.f;
+  }
+  if constexpr (kRing) {
+    __syncthreads();
+    if (abort) {  // copies already issued land before the block leaves
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 100000ull) {
       }
-      expand(hr[i], hv);
-      expand(gr[i], gv);
-      expand(dr[i], o);  // zeros without dh
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[e] += rho * (gv[e] * wv[e]) - k * hv[e];
-        if constexpr (kDw) acc[i][e] = fmaf(gv[e], hv[e] * rho, acc[i][e]);
-      }
-      store8<kAligned>(static_cast<T*>(p.dx) + row * p.C, c, p.C, o);
     }
   }
   if constexpr (kDw) {
     float* part = p.dw_part + static_cast<int64_t>(blockIdx.x) * p.C;
+    float* dw_smem = reinterpret_cast<float*>(norm_smem);  // (the ring's copies have all been read)
     for (int s = 0; s < R; ++s) {  // the row slots' sums in order
       __syncthreads();
-      if (rs != s) continue;
+      if (rs != s) continue;  // (the loading warp: rs = R)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = kVec * (i * tpr + t);
