@@ -158,13 +158,13 @@ dsa_status_t persistent_grid(K kernel, uint32_t smem, int regs, int64_t units, u
   return DSA_OK;
 }
 
-// The pair form: as many clusters of two as stay resident, looked up once per device.
-dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                               const CUtensorMap& to, const dsa::CrossFwdParams& fp, cudaStream_t s) {
+// A persistent kernel over CTA pairs: as many clusters of two as stay resident (looked up once per
+// device), no more than units.
+template <auto kKernel, typename... Args>
+dsa_status_t launch_pairs(uint32_t smem, int threads, int regs, int64_t units, cudaStream_t s, const Args&... args) {
   static std::atomic<int> cache[kPairMaxDevices] = {};
-  auto kernel = dsa::cross_fwd_kernel<true>;
   unsigned grid = 0;
-  dsa_status_t st = persistent_grid(kernel, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, INT32_MAX, &grid);
+  dsa_status_t st = persistent_grid(kKernel, smem, regs, INT32_MAX, &grid);
   if (st != DSA_OK) return st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -173,8 +173,8 @@ dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, con
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(grid / 2 * 2, 1, 1);
-  cfg.blockDim = dim3(dsa::crossf::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = dsa::crossf::kSmemBytes;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -183,14 +183,14 @@ dsa_status_t launch_cross_pair(const CUtensorMap& tq, const CUtensorMap& tk, con
   const bool cached = dev >= 0 && dev < kPairMaxDevices;
   if (cached) n = cache[dev].load(std::memory_order_relaxed);
   if (n <= 0) {
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       return DSA_ERR_CUDA;
     }
     if (cached) cache[dev].store(n, std::memory_order_relaxed);
   }
-  cfg.gridDim.x = 2u * static_cast<unsigned>(fp.n_units < n ? fp.n_units : n);
-  if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, to, fp) != cudaSuccess) {
+  cfg.gridDim.x = 2u * static_cast<unsigned>(units < n ? units : n);
+  if (cudaLaunchKernelEx(&cfg, kKernel, args...) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }
@@ -427,6 +427,7 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   fp.n_split = p->Lk > 0 ? c.split_q : 0;
   fp.n_units = static_cast<int>(c.units * c.split_q);
   fp.scale_log2 = p->scale * 1.4426950408889634f;
+  fp.unit_cost = 1;
   if (p->Lk > 0) {
     CUtensorMap tq, tk, tv;
     int mq[3], mk[3], mv[3];
@@ -446,10 +447,14 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     if (c.pair) {
       fp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
       fp.n_units = p->B * p->kv_heads * fp.tiles;
+      // measured on a 512 + 203-key pair: units of four and of two chunks take times of 9 : 5.7
+      // (with a cost of 1 the CTAs of the short entry ran 212 us, those of the long one 186)
+      fp.unit_cost = 3;
       CUtensorMap to;
       int mo[3];
       if (!make_view_map(&to, out, p->B, p->heads, c.group, p->Lq, 32, 1, mo)) return DSA_ERR_CUDA;
-      return launch_cross_pair(tq, tk, tv, to, fp, s);
+      return launch_pairs<dsa::cross_fwd_kernel<true>>(dsa::crossf::kSmemBytes, dsa::crossf::kThreads,
+                                                       dsa::crossf::kRegsAtLaunch, fp.n_units, s, tq, tk, tv, to, fp);
     }
     unsigned grid = 0;
     st = persistent_grid(dsa::cross_fwd_kernel<false>, dsa::crossf::kSmemBytes, dsa::crossf::kRegsAtLaunch, fp.n_units,
@@ -507,6 +512,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   shape.tiles = c.tiles;
   shape.n_split = c.split_q;
   shape.n_units = static_cast<int>(c.units * c.split_q);
+  shape.unit_cost = 1;  // (the dQ pass: the same pair's CTAs end within 3% of each other)
 
   dsa::CrossKvParams kp;
   std::memset(&kp, 0, sizeof(kp));
@@ -596,10 +602,20 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   dp.kb = mk[2];
   dp.vh = mv[1];
   dp.vb = mv[2];
+  if (c.pair) {
+    CUtensorMap tk64, tv64;
+    if (!make_view_map(&tk64, k, p->B, p->kv_heads, 0, p->Lk, 64, 1, mk) ||
+        !make_view_map(&tv64, v, p->B, p->kv_heads, 0, p->Lk, 64, 1, mv))
+      return DSA_ERR_CUDA;
+    dp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
+    dp.n_units = p->B * p->kv_heads * dp.tiles;
+    return launch_pairs<dsa::cross_dq_kernel<true>>(dsa::crossdq::kSmemBytes, dsa::crossdq::kThreads,
+                                                    dsa::bdq::kRegsAtLaunch, dp.n_units, s, tq, tdo, tk64, tk, tv64, tdq, dp);
+  }
   unsigned grid = 0;
-  st = persistent_grid(dsa::cross_dq_kernel, dsa::crossdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
+  st = persistent_grid(dsa::cross_dq_kernel<false>, dsa::crossdq::kSmemBytes, dsa::bdq::kRegsAtLaunch, dp.n_units, &grid);
   if (st != DSA_OK) return st;
-  dsa::cross_dq_kernel<<<grid, dsa::crossdq::kThreads, dsa::crossdq::kSmemBytes, s>>>(tq, tdo, tk, tv, tdq, dp);
+  dsa::cross_dq_kernel<false><<<grid, dsa::crossdq::kThreads, dsa::crossdq::kSmemBytes, s>>>(tq, tdo, tk, tk, tv, tdq, dp);
   st = launch_status();
   if (st != DSA_OK || c.split_q == 1) return st;
   cq.n_part = c.split_q;

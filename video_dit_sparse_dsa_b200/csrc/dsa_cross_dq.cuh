@@ -11,20 +11,25 @@
 //     copied into TMEM by the elementwise warps (a row per thread) when this unit's last dS is
 //     written, while its last dQ product runs;
 //   * a unit's dQ is read out and written after that copy, while the next unit's first scores are
-//     computed, through Q's half of the staging buffer and TMA stores (rows packed from several
-//     heads, and fp32 parts, are stored directly);
-//   * K of up to 384 and V of up to 256 keys stay in shared memory for all consecutive units of
-//     their kv head; a CTA's units are a contiguous range of equal cost, as in the forward, whose
+//     computed, through shared memory and TMA stores (rows packed from several heads, and fp32
+//     parts, are stored directly);
+//   * K and V of short key sequences stay in shared memory for all consecutive units of their kv
+//     head; a CTA's (pair's) units are a contiguous range of equal cost, as in the forward, whose
 //     units these are.
+// More than 128 rows per head run on CTA pairs, as in the forward (kPair): every product is one M
+// = 256 tcgen05.mma.cta_group::2 over 256 rows.  A CTA holds half of every operand, and K twice:
+// its half of a step's keys for the scores and its half of the channels for the dQ product, each
+// with a ring of its own and released by its own product.  On one CTA the K chunk of a step is held
+// from its scores, a step ahead, until its dQ product, and three 32 KB entries, all that fits, left
+// the next scores waiting for their load (3150 clocks per step; 480p pair 308 us).
 //
-// Persistent and warp-specialised, one CTA per SM, 384 threads:
-//   warp 8      TMA producer of K (128-key chunks, 3 entries: read by the scores of its step,
-//               issued a step early, and by its dQ product)
-//   warp 10     TMA producer of V (2 entries) and of Q and dO
-//   warp 11     takes each K chunk as it lands, zeroes the rows past the last key that the dQ
-//               product will read (against dS = 0, but 0 * NaN is NaN) and hands it over
-//   warp 9      MMA issuer, per step t: S(t + 1) once the elementwise warps hold S(t) in
-//               registers; dQ += dS(t) K(t) once dS(t) is written; then dP(t + 1)
+// Persistent and warp-specialised, 384 threads:
+//   warp 8      TMA producer of K
+//   warp 10     TMA producer of V and of Q and dO
+//   warp 11     takes each K chunk of the dQ product as it lands, zeroes the rows past the last key
+//               that the product will read (against dS = 0, but 0 * NaN is NaN) and hands it over
+//   warp 9      MMA issuer (pair: the even CTA's), per step t: S(t + 1) once the elementwise warps
+//               hold S(t) in registers; dQ += dS(t) K(t) once dS(t) is written; then dP(t + 1)
 //   warps 0-7   elementwise, two threads per row: thread h takes keys [64h, 64h + 64) of a step
 // TMEM (512 columns): Q [0, 64) and dO [64, 128) as packed bf16 pairs, scores [128, 256), dP (then
 // dS) [256, 384), dQ [384, 512).
@@ -52,14 +57,23 @@ struct CrossDqParams : CrossShape {
 namespace crossdq {
 constexpr int kThreads = bdq::kThreads;
 constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kHandWarp = 11;
-constexpr int kK = 3, kV = 2;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
-constexpr uint32_t kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kK * kTile;
-constexpr uint32_t kOffBar = kOffV + kV * kTile;
-constexpr uint32_t kSmemUsed = kOffBar + 256;
+// Shared memory: 224 KB of tiles and the barriers.  Q and dO staging (32 KB each); single: K 3 and
+// V 2 chunks of 32 KB, dQ leaves through Q's staging; pair: K 3 entries of 64 keys (scores) and 3 of
+// 64 channels (dQ product), V 2 of 64 keys, 16 KB each, and 32 KB for dQ.
+template <bool kPair>
+struct Mem {
+  static constexpr int kK = 3, kV = 2;  // chunks
+  static constexpr uint32_t kEntry = kPair ? kHalf : kTile;
+  static constexpr uint32_t kOffQ = 0, kOffDO = kTile, kOffK = 2 * kTile, kOffV = kOffK + kK * kEntry;
+  static constexpr uint32_t kOffK2 = kPair ? kOffV + kV * kEntry : kOffK;  // K of the dQ product
+  static constexpr uint32_t kOffOut = kPair ? kOffK2 + kK * kEntry : kOffQ;
+  static_assert((kPair ? kOffOut + kTile : kOffV + kV * kEntry) == 7 * kTile, "both forms use 224 KB");
+};
+constexpr uint32_t kOffBar = 7 * kTile;
+constexpr uint32_t kSmemUsed = kOffBar + 320;
 constexpr uint32_t kSmemBytes = 227 * 1024;
 static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
-using Cur = crossf::Cursor<128>;
 // column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
 constexpr uint32_t kPolyMask = 0x22u;
 
@@ -80,13 +94,49 @@ __device__ __forceinline__ void copy_row(uint32_t tile, int row, uint32_t t_dst)
     tmem_st32(t_dst + 32 * half, w);
   }
 }
+
+// D = A B^T over 128 channels: A (Q or dO) from TMEM, B a K-major tile of the step's 128 keys (pair:
+// 64 of them in either CTA).
+template <bool kPair>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc) {
+  fwd::opaque(b_desc);
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const uint32_t o = (kk >> 2) * (kPair ? kHalf / 2 : kHalf) + (kk & 3) * 32;
+    if constexpr (kPair)
+      mma_ts_pair_warp(d_tmem, a_tmem + 8 * kk, fwd::desc_add(b_desc, o), idesc_bf16_f32(256, 128, 0, 0), kk > 0);
+    else
+      mma_ts_warp(d_tmem, a_tmem + 8 * kk, fwd::desc_add(b_desc, o), bdq::kIdescS, kk > 0);
+  }
+}
+
+// dQ (+)= dS K over 16 keys (dS of keys [16kk, 16kk + 16) at the columns that their thread wrote).
+template <bool kPair>
+__device__ __forceinline__ void issue_dq(uint32_t tmem, int kk, uint64_t k_desc, bool accumulate) {
+  const uint32_t ds = tmem + bdq::kColDP + 64 * (kk >> 2) + 8 * (kk & 3);
+  if constexpr (kPair)
+    mma_ts_pair_warp(tmem + bdq::kColDQ, ds, fwd::desc_add(k_desc, kk * 2048), idesc_bf16_f32(256, 128, 0, 1), accumulate);
+  else
+    mma_ts_warp(tmem + bdq::kColDQ, ds, fwd::desc_add(k_desc, kk * 2048), bdq::kIdescDQ, accumulate);
+}
 }  // namespace crossdq
 
+// kPair: launched as clusters of two; tmK and tmV have boxes of 64 keys, tmK2 of 128.  Single: all of
+// 128, tmK2 is not used.
+template <bool kPair>
 __global__ void __launch_bounds__(crossdq::kThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
-                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmDQ, CrossDqParams p) {
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmK2,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDQ,
+                    CrossDqParams p) {
   using namespace crossdq;
+  using crossf::arrive;
+  using crossf::commit;
+  using crossf::lead_bar;
+  using crossf::wait_lead;
+  using M = Mem<kPair>;
+  using Cur = crossf::Cursor<kPair ? 256 : 128>;
+  constexpr int kK = M::kK, kV = M::kV, kCtas = kPair ? 2 : 1;
   using bdq::kColDO;
   using bdq::kColDP;
   using bdq::kColDQ;
@@ -105,38 +155,45 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
   const uint32_t sbase = raw + pad;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* qd_full = bars;              // Q and dO of a unit have landed in the staging buffer
-  uint64_t* q_free = bars + 1;           // Q's half may be loaded again (8)
+  uint64_t* q_free = bars + 1;           // Q's half may be loaded again (pair: 4, else 8)
   uint64_t* do_free = bars + 2;          // dO's half (4)
-  uint64_t* k_land = bars + 3;           // [kK]
-  uint64_t* k_full = k_land + kK;        // [kK] handed over
+  uint64_t* q_copied = bars + 3;         // single: the unit's Q has been read from there (4)
+  uint64_t* k_land = bars + 4;           // [kK] K of the dQ product has landed in this CTA
+  uint64_t* k2_full = k_land + kK;       // [kK] handed over (by each CTA)
+  uint64_t* k2_empty = k2_full + kK;     // [kK]
+  uint64_t* k_full = k2_empty + kK;      // [kK] pair: K of the scores
   uint64_t* k_empty = k_full + kK;       // [kK]
   uint64_t* v_full = k_empty + kK;       // [kV]
   uint64_t* v_empty = v_full + kV;       // [kV]
   uint64_t* s_full = v_empty + kV;       // S of a step ready
-  uint64_t* s_read = s_full + 1;         // loaded (8)
+  uint64_t* s_read = s_full + 1;         // loaded (8 per CTA)
   uint64_t* dp_full = s_full + 2;        // dP of a step ready
-  uint64_t* ds_full = s_full + 3;        // dS written (8)
+  uint64_t* ds_full = s_full + 3;        // dS written (8 per CTA)
   uint64_t* dq_done = s_full + 4;        // every dQ product of a unit done
-  uint64_t* dq_free = s_full + 5;        // dQ read out (8)
-  uint64_t* qa_full = s_full + 6;        // the unit's Q and dO are in TMEM (8)
-  uint64_t* q_copied = s_full + 7;       // its Q has been read from the staging buffer (4)
-  uint64_t* drain = s_full + 8;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 9);
-  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 9) + 1;
-  int* range = reinterpret_cast<int*>(s_full + 10);  // [2]
-  static_assert(3 + 3 * kK + 2 * kV + 11 <= 256 / 8, "barriers must fit their 256 bytes");
+  uint64_t* dq_free = s_full + 5;        // dQ read out (8 per CTA)
+  uint64_t* qa_full = s_full + 6;        // the unit's Q and dO are in TMEM (8 per CTA)
+  uint64_t* drain = s_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
+  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 8) + 1;
+  int* range = reinterpret_cast<int*>(s_full + 9);  // [2]
+  static_assert(4 + 5 * kK + 2 * kV + 10 <= 320 / 8, "barriers must fit their 320 bytes");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool lead = rank == 0;
   if (tid == 0) {
     tma_prefetch_map(&tmQ);
     tma_prefetch_map(&tmDO);
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
     mbar_init(qd_full, 1);
-    mbar_init(q_free, 8);
+    mbar_init(q_free, kPair ? 4 : 8);
     mbar_init(do_free, 4);
+    mbar_init(q_copied, 4);
     for (int s = 0; s < kK; ++s) {
       mbar_init(k_land + s, 1);
+      mbar_init(k2_full + s, kCtas);
+      mbar_init(k2_empty + s, 1);
       mbar_init(k_full + s, 1);
       mbar_init(k_empty + s, 1);
     }
@@ -145,27 +202,32 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       mbar_init(v_empty + s, 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_read, 8);
+    mbar_init(s_read, 8 * kCtas);
     mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8);
+    mbar_init(ds_full, 8 * kCtas);
     mbar_init(dq_done, 1);
-    mbar_init(dq_free, 8);
-    mbar_init(qa_full, 8);
-    mbar_init(q_copied, 4);
+    mbar_init(dq_free, 8 * kCtas);
+    mbar_init(qa_full, 8 * kCtas);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
     int b, e;
-    crossf::unit_range(p, blockIdx.x, gridDim.x, b, e);
+    crossf::unit_range(p, blockIdx.x / kCtas, gridDim.x / kCtas, b, e);
     range[0] = b;
     range[1] = e;
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, bdq::kTmemCols);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(tmem_slot, bdq::kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, bdq::kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // both CTAs' barriers are ready before either arrives on the other's
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int begin = range[0], end = range[1];
@@ -175,21 +237,44 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     if (warp == kKWarp) {
       // ------------------------------------------------------------------ TMA producer of K
       if (lane == 0) {
-        Cur c;
+        Cur c, d;  // the scores' K of the next step, the dQ product's K of this one
         c.start(p, begin, end);
-        int ld = 0;
+        c.settle(p);
+        d = c;
+        int ld = 0, ld2 = 0;
         bool ok = true;
-        for (c.settle(p); ok && c.valid(); c.next_unit(p)) {
-          if (c.reuse(kK)) continue;
-          for (int j = 0; j < c.n; ++j, ++ld) {
+        // this CTA's half of the keys of c's step for the scores (pair)
+        auto load_scores = [&]() {
+          if (!c.reuse(kK)) {
             const int st = ld % kK;
-            ok = mbar_wait(k_empty + st, ((ld / kK) & 1) ^ 1, abort, 171);
-            if (!ok) break;
-            uint8_t* dst = smem + kOffK + st * kTile;
-            mbar_arrive_expect_tx(k_land + st, kTile);
-            tma_load_4d(dst, &tmK, k_land + st, 0, 128 * (c.c0 + j), c.x.kvh * p.kh, c.x.b * p.kb);
-            tma_load_4d(dst + kHalf, &tmK, k_land + st, 64, 128 * (c.c0 + j), c.x.kvh * p.kh, c.x.b * p.kb);
+            ok = mbar_wait(k_empty + st, ((ld / kK) & 1) ^ 1, abort, 170);
+            if (!ok) return;
+            ++ld;
+            if (lead) mbar_arrive_expect_tx(k_full + st, 2 * M::kEntry);
+            const uint32_t bar = lead_bar<kPair>(k_full + st);
+            uint8_t* dst = smem + M::kOffK + st * M::kEntry;
+            const int row = 128 * (c.c0 + c.t) + 64 * rank;
+            tma_load_4d_pair(dst, &tmK, bar, 0, row, c.x.kvh * p.kh, c.x.b * p.kb);
+            tma_load_4d_pair(dst + kHalf / 2, &tmK, bar, 64, row, c.x.kvh * p.kh, c.x.b * p.kb);
           }
+          c.next_chunk(p);
+        };
+        if (kPair && c.valid()) load_scores();
+        while (ok && d.valid()) {
+          if (kPair && c.valid()) load_scores();
+          if (ok && !d.reuse(kK)) {
+            const int st = ld2 % kK;
+            ok = mbar_wait(k2_empty + st, ((ld2 / kK) & 1) ^ 1, abort, 171);
+            if (!ok) break;
+            ++ld2;
+            uint8_t* dst = smem + M::kOffK2 + st * M::kEntry;
+            mbar_arrive_expect_tx(k_land + st, M::kEntry);
+            const CUtensorMap* map = kPair ? &tmK2 : &tmK;
+            tma_load_4d(dst, map, k_land + st, 64 * rank, 128 * (d.c0 + d.t), d.x.kvh * p.kh, d.x.b * p.kb);
+            if constexpr (!kPair)
+              tma_load_4d(dst + kHalf, map, k_land + st, 64, 128 * (d.c0 + d.t), d.x.kvh * p.kh, d.x.b * p.kb);
+          }
+          d.next_chunk(p);
         }
       }
     } else if (warp == kHandWarp) {
@@ -207,12 +292,18 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
           const int keys = c.keys(j);
           if (keys & 15) {
             const int pad_rows = 16 - (keys & 15);
-            const uint32_t k0 = sbase + kOffK + st * kTile + (lane >> 3 & 1) * kHalf + (lane & 7) * 16;
-            for (int rr = lane >> 4; rr < pad_rows; rr += 2) st_shared_v4(k0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
+            const uint32_t k0 = sbase + M::kOffK2 + st * M::kEntry + (lane & 7) * 16 + (kPair ? 0u : (lane >> 3 & 1) * kHalf);
+            for (int rr = lane >> (kPair ? 3 : 4); rr < pad_rows; rr += kPair ? 4 : 2)
+              st_shared_v4(k0 + (keys + rr) * 128, 0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(k_full + st);
+          if (lane == 0) {
+            if constexpr (kPair)
+              mbar_arrive_release_cluster(lead_bar<kPair>(k2_full + st));
+            else
+              mbar_arrive(k2_full + st);
+          }
         }
       }
     } else if (warp == kVWarp) {
@@ -225,31 +316,39 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
         for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
           ok = mbar_wait(do_free, (un & 1) ^ 1, abort, 173);
           if (!ok) break;
-          const int g = c.x.g, row = c.x.row;
+          const int g = c.x.g, row = c.x.row + 128 * rank;
           mbar_arrive_expect_tx(qd_full, 2 * p.q_bytes);
-          tma_load_5d(smem + kOffDO, &tmDO, qd_full, 0, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
-          tma_load_5d(smem + kOffDO + kHalf, &tmDO, qd_full, 64, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
+          tma_load_5d(smem + M::kOffDO, &tmDO, qd_full, 0, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
+          tma_load_5d(smem + M::kOffDO + kHalf, &tmDO, qd_full, 64, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
           ok = mbar_wait(q_free, (un & 1) ^ 1, abort, 174);
           if (!ok) break;
-          tma_load_5d(smem + kOffQ, &tmQ, qd_full, 0, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
-          tma_load_5d(smem + kOffQ + kHalf, &tmQ, qd_full, 64, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          tma_load_5d(smem + M::kOffQ, &tmQ, qd_full, 0, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
+          tma_load_5d(smem + M::kOffQ + kHalf, &tmQ, qd_full, 64, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
           if (c.reuse(kV)) continue;
           for (int j = 0; j < c.n; ++j, ++ld) {
             const int st = ld % kV;
             ok = mbar_wait(v_empty + st, ((ld / kV) & 1) ^ 1, abort, 175);
             if (!ok) break;
-            uint8_t* dst = smem + kOffV + st * kTile;
-            mbar_arrive_expect_tx(v_full + st, kTile);
-            tma_load_4d(dst, &tmV, v_full + st, 0, 128 * (c.c0 + j), c.x.kvh * p.vh, c.x.b * p.vb);
-            tma_load_4d(dst + kHalf, &tmV, v_full + st, 64, 128 * (c.c0 + j), c.x.kvh * p.vh, c.x.b * p.vb);
+            uint8_t* dst = smem + M::kOffV + st * M::kEntry;
+            const int at = 128 * (c.c0 + j) + (kPair ? 64 * rank : 0);
+            if (lead) mbar_arrive_expect_tx(v_full + st, kCtas * M::kEntry);
+            if constexpr (kPair) {
+              const uint32_t bar = lead_bar<kPair>(v_full + st);
+              tma_load_4d_pair(dst, &tmV, bar, 0, at, c.x.kvh * p.vh, c.x.b * p.vb);
+              tma_load_4d_pair(dst + kHalf / 2, &tmV, bar, 64, at, c.x.kvh * p.vh, c.x.b * p.vb);
+            } else {
+              tma_load_4d(dst, &tmV, v_full + st, 0, at, c.x.kvh * p.vh, c.x.b * p.vb);
+              tma_load_4d(dst + kHalf, &tmV, v_full + st, 64, at, c.x.kvh * p.vh, c.x.b * p.vb);
+            }
           }
         }
       }
-    } else {
+    } else if (lead) {
       // ------------------------------------------------------------------ MMA issuer (whole warp)
-      const uint64_t dKk = smem_desc_sw128(sbase + kOffK, 16, 1024);     // K-major
-      const uint64_t dKm = smem_desc_sw128(sbase + kOffK, kHalf, 1024);  // MN-major
-      const uint64_t dVk = smem_desc_sw128(sbase + kOffV, 16, 1024);
+      const uint64_t dKk = smem_desc_sw128(sbase + M::kOffK, 16, 1024);      // K-major
+      const uint64_t dKm = smem_desc_sw128(sbase + M::kOffK2, kHalf, 1024);  // MN-major
+      const uint64_t dVk = smem_desc_sw128(sbase + M::kOffV, 16, 1024);
+      uint64_t* ks_full = kPair ? k_full : k2_full;  // K of the scores
       Cur c;
       c.start(p, begin, end);
       int ks = 0, vs = 0, un = 0, G = 0;  // ring positions of the unit's first chunk; units, steps before
@@ -257,52 +356,61 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
         const bool k_reuse = c.reuse(kK), k_keep = c.keep(p, kK), v_reuse = c.reuse(kV), v_keep = c.keep(p, kV);
         const int n = c.n;
-        ok = warp_wait(qa_full, un & 1, abort, 180);
-        if (!ok) break;
         auto issue_s = [&](int t) -> bool {  // once S of the step before has been loaded
           const int st = (ks + t) % kK;
-          if (!k_reuse && !warp_wait(k_full + st, ((ks + t) / kK) & 1, abort, 181)) return false;
-          if (G + t > 0 && !warp_wait(s_read, (G + t - 1) & 1, abort, 182)) return false;
+          if (!k_reuse && !wait_lead<kPair>(ks_full + st, ((ks + t) / kK) & 1, abort, 181)) return false;
+          if (G + t > 0 && !wait_lead<kPair>(s_read, (G + t - 1) & 1, abort, 182)) return false;
           tc_fence_after();
-          bdq::issue_qk(tmem + kColS, tmem + kColQ, desc_add(dKk, st * kTile));
-          mma_commit_warp(s_full);
+          issue_qk<kPair>(tmem + kColS, tmem + kColQ, desc_add(dKk, st * M::kEntry));
+          commit<kPair>(s_full);
+          if (kPair && !k_keep) commit<kPair>(k_empty + st);
           return true;
         };
-        auto issue_dp = [&](int t) -> bool {  // after the dQ product that read dS(t - 1) from its columns
+        // dP (after the dQ product that read dS(t - 1) from its columns), V being in
+        auto wait_v = [&](int t) -> bool {
+          return v_reuse || wait_lead<kPair>(v_full + (vs + t) % kV, ((vs + t) / kV) & 1, abort, 183);
+        };
+        auto issue_dp = [&](int t) {
           const int st = (vs + t) % kV;
-          if (!v_reuse && !warp_wait(v_full + st, ((vs + t) / kV) & 1, abort, 183)) return false;
-          tc_fence_after();
-          bdq::issue_qk(tmem + kColDP, tmem + kColDO, desc_add(dVk, st * kTile));
-          mma_commit_warp(dp_full);
-          if (!v_keep) mma_commit_warp(v_empty + st);
-          return true;
+          issue_qk<kPair>(tmem + kColDP, tmem + kColDO, desc_add(dVk, st * M::kEntry));
+          commit<kPair>(dp_full);
+          if (!v_keep) commit<kPair>(v_empty + st);
         };
-        ok = issue_s(0) && issue_dp(0);
+        ok = wait_v(0) && wait_lead<kPair>(qa_full, un & 1, abort, 180) && issue_s(0);
+        if (ok) issue_dp(0);
         for (int t = 0; t < n && ok; ++t) {
           if (t + 1 < n) ok = issue_s(t + 1);
+          // everything but dS is waited for before dS: from its arrival the elementwise warps wait
+          // for dP(t + 1)
           const int st = (ks + t) % kK, n16 = (c.keys(t) + 15) >> 4;
-          if (ok && t == 0) ok = warp_wait(dq_free, (un & 1) ^ 1, abort, 185);
-          if (ok) ok = warp_wait(ds_full, (G + t) & 1, abort, 184);
+          if (ok && kPair && !k_reuse) ok = wait_lead<kPair>(k2_full + st, ((ks + t) / kK) & 1, abort, 186);
+          if (ok && t + 1 < n) ok = wait_v(t + 1);
+          if (ok && t == 0) ok = wait_lead<kPair>(dq_free, (un & 1) ^ 1, abort, 185);
+          uint64_t k = desc_add(dKm, st * M::kEntry);
+          fwd::opaque(k);
+          if (ok) ok = wait_lead<kPair>(ds_full, (G + t) & 1, abort, 184);
           if (!ok) break;
           tc_fence_after();
           if (n16 == 8) {
-            bdq::issue_dq(tmem + kColDQ, tmem + kColDP, desc_add(dKm, st * kTile), t > 0);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) issue_dq<kPair>(tmem, kk, k, t > 0 || kk > 0);
           } else {  // the last chunk: only the sixteens that hold keys
 #pragma unroll 1
-            for (int kk = 0; kk < n16; ++kk)
-              mma_ts_warp(tmem + kColDQ, tmem + kColDP + 64 * (kk >> 2) + 8 * (kk & 3),
-                          desc_add(dKm, st * kTile + kk * 2048), bdq::kIdescDQ, t > 0 || kk > 0);
+            for (int kk = 0; kk < n16; ++kk) issue_dq<kPair>(tmem, kk, k, t > 0 || kk > 0);
           }
-          if (!k_keep) mma_commit_warp(k_empty + st);
-          if (t + 1 < n) ok = issue_dp(t + 1);
+          if (t + 1 < n) issue_dp(t + 1);
+          if (!k_keep) commit<kPair>(k2_empty + st);
         }
         if (!ok) break;
-        mma_commit_warp(dq_done);
+        commit<kPair>(dq_done);
         G += n;
         if (!k_keep) ks += n;
         if (!v_keep) vs += n;
       }
-      mma_commit_warp(drain);
+      if constexpr (kPair)
+        mma_commit_pair_warp(drain, 1);
+      else
+        mma_commit_warp(drain);
       fwdp::drain_wait(drain, 0);
     }
   } else {
@@ -311,7 +419,7 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     const int h = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float kLog2e = 1.4426950408889634f;
-    const bool staged = p.n_split == 1 && p.pk == 1;  // dQ through the staging buffer
+    const bool staged = kPair || (p.n_split == 1 && p.pk == 1);  // dQ through shared memory
     int G = 0, un = 0;
     bool ok = true, stored = false;  // stored: this lane has a TMA store that may still read the buffer
     crossf::Unit px = {};            // the unit whose dQ is still in TMEM
@@ -321,13 +429,15 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       tc_fence_after();
       const uint32_t tD = tmem + kColDQ + 64 * h + lane_off;
       if (staged) {
-        const uint32_t off = kOffQ + h * kHalf + quarter * 4096;
+        const uint32_t off = M::kOffOut + h * kHalf + quarter * 4096;
+        if (kPair && lane == 0) tma_store_wait_read();  // the unit before has left the buffer
+        __syncwarp();
         crossf::stage_o(tD, p.scale, sbase + off);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(dq_free);
+          arrive<kPair>(lead_bar<kPair>(dq_free));
           const int r0 = px.row + 32 * quarter;
           if (r0 < p.Lq) {
             tma_store_5d(&tmDQ, smem + off, 64 * h, r0, px.g, px.kvh, px.b);
@@ -335,7 +445,7 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
           }
         }
       } else {
-        const crossf::Row y = crossf::unit_row(p, px, r);
+        const crossf::Row y = crossf::unit_row(p, px, r);  // (single)
         if (p.n_split > 1) {
           const int64_t rows = static_cast<int64_t>(p.B) * p.heads * p.Lq;
           const int64_t row = (static_cast<int64_t>(px.b) * p.heads + y.head) * p.Lq + y.q;
@@ -354,7 +464,9 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     Cur c;
     c.start(p, begin, end);
     for (; ok && c.valid(); c.advance(p)) {
-      const crossf::Row y = crossf::unit_row(p, c.x, r);
+      crossf::Unit x = c.x;  // (row: this CTA's first)
+      x.row += 128 * rank;
+      const crossf::Row y = crossf::unit_row(p, x, r);
       const int64_t bh = static_cast<int64_t>(c.x.b) * p.heads + y.head;
       if (c.n == 0) {  // no keys: no gradient
         if (y.ok) {
@@ -377,22 +489,22 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       // have completed: this warp has seen its last scores and dP
       ok = warp_wait(qd_full, un & 1, abort, 191);
       if (!ok) break;
-      copy_row(sbase + (h ? kOffDO : kOffQ), r, tmem + (h ? kColDO : kColQ) + lane_off);
+      copy_row(sbase + (h ? M::kOffDO : M::kOffQ), r, tmem + (h ? kColDO : kColQ) + lane_off);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(qa_full);
-        mbar_arrive(h ? do_free : q_copied);
+        arrive<kPair>(lead_bar<kPair>(qa_full));
+        mbar_arrive(h ? do_free : kPair ? q_free : q_copied);
       }
       if (un > 0) {
-        // (these rows of dQ go where the other warp's Q was)
-        if (h) ok = warp_wait(q_copied, un & 1, abort, 194);
+        // (single: these rows of dQ go where the other warp's Q was)
+        if (!kPair && h) ok = warp_wait(q_copied, un & 1, abort, 194);
         if (ok) ok = write_out(un - 1);
         if (!ok) break;
-        stored = staged;
+        stored = !kPair && staged;
       }
-      if (!stored && lane == 0) mbar_arrive(q_free);
+      if (!kPair && !stored && lane == 0) mbar_arrive(q_free);
       for (c.t = 0; c.t < c.n; ++c.t, ++G) {
         const int nv = c.keys(c.t) - 64 * h;  // keys of this thread's 64 columns
         ok = warp_wait(s_full, G & 1, abort, 192);
@@ -411,7 +523,7 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
           tmem_ld64_wait(tmem + kColS + 64 * h + lane_off, s);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(s_read);
+          if (lane == 0) arrive<kPair>(lead_bar<kPair>(s_read));
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float x0, x1;
@@ -449,9 +561,9 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(ds_full);
+        if (lane == 0) arrive<kPair>(lead_bar<kPair>(ds_full));
       }
-      px = c.x;
+      px = x;
       ++un;
     }
     if (ok && un > 0) write_out(un - 1);
@@ -467,9 +579,13 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     }
   }
   __syncthreads();
+  if constexpr (kPair) cluster_sync();  // neither CTA leaves while the other may still reach into it
   if (warp == kMmaWarp) {
     __syncwarp();
-    tmem_dealloc(tmem, bdq::kTmemCols);
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, bdq::kTmemCols);
+    else
+      tmem_dealloc(tmem, bdq::kTmemCols);
   }
 }
 

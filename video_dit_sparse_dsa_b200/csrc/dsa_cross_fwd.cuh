@@ -64,6 +64,7 @@ struct CrossShape {
   int tiles;              // units per kv head and part
   int n_split;            // parts of the keys
   int n_units;            // B * kv_heads * n_split * tiles
+  int unit_cost;          // a unit's fixed cost in half chunks
 };
 
 struct CrossFwdParams : CrossShape {
@@ -116,10 +117,10 @@ __device__ __forceinline__ int chunks_per_part(const CrossShape& p, int chunks) 
   return p.n_split > 1 ? (per + 1) & ~1 : per;
 }
 
-// The CTA's units [begin, end): the sequence is cut at equal cost, a unit costing its chunks and
-// a constant (about half a chunk's) for its own start and end.
+// The CTA's units [begin, end): the sequence is cut at equal cost, a unit costing its chunks and a
+// constant for its own start and end, in half chunks: unit_cost (chosen by each kernel's launch).
 __device__ __forceinline__ int64_t unit_cost(const CrossShape& p, int b) {
-  return 2 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + 1;
+  return 2 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + p.unit_cost;
 }
 
 __device__ __forceinline__ void unit_range(const CrossShape& p, int cta, int n_cta, int& begin, int& end) {
@@ -228,6 +229,13 @@ struct Cursor {
   __device__ __forceinline__ void next_unit(const CrossShape& p) {
     advance(p);
     settle(p);
+  }
+  // The next chunk (a user that counts t in chunks).
+  __device__ __forceinline__ void next_chunk(const CrossShape& p) {
+    if (t + 1 >= n)
+      next_unit(p);
+    else
+      ++t;
   }
   __device__ __forceinline__ void next_step(const CrossShape& p) {
     if (last())
@@ -814,13 +822,19 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         continue;
       }
       float m_used = -INFINITY, l = 0.f;
+      // a warp without query rows (few rows, the last tile of a head) does no softmax: what its
+      // rows of P and O hold reaches no other row (one token over 115201 + 70007 keys: 119 us
+      // with all warps' exponentials in the way)
+      const bool act = p.pk > 1 ? 32 * (warp & 3) < p.pk * p.Lq : c.x.row + 128 * rank + 32 * (warp & 3) < p.Lq;
       for (c.t = 0; 2 * c.t < c.n; ++c.t, ++G) {
         const int e = G & 1;
         if (ok) ok = warp_wait(s_full + e, (G >> 1) & 1, abort, 160);  // (committed to this CTA too)
         if (ok) tc_fence_after();
-        float alpha;
-        bool need;
-        if (c.in_step() == 2)
+        float alpha = 1.f;
+        bool need = false;
+        if (!act) {
+          if (ok && lane == 0) arrive<kPair>(lead_bar<kPair>(s_read + e));
+        } else if (c.in_step() == 2)
           need = softmax_step<128, kPair>(ok, tmem + fwd::col_s(e) + 128 * i + lane_off, tmem + fwd::col_p(e) + 64 * i + lane_off,
                                    lead_bar<kPair>(s_read + e), p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
                                    c.keys(2 * c.t + i));
@@ -843,7 +857,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           if (lane == 0) arrive<kPair>(lead_bar<kPair>(p_full + e));
         }
       }
-      const float l_all = l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, l);
+      const float l_all = act ? l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, l) : 1.f;
       px = c.x;
       px.row += 128 * rank;
       p_inv = 1.f / l_all;
