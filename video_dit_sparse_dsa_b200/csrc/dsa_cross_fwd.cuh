@@ -34,7 +34,7 @@
 //            unit's first, as soon as the softmax warps hold those of step G in registers, then
 //            O += P(G) V(G)
 //   warps 0-7  softmax of the CTA's own 128 rows: warpgroup i takes the step's chunk i (a single
-//            chunk: its columns [64 i, 64 i + 64)), a thread per query row; the two threads of a
+//            chunk: half of its sixteens of columns), a thread per query row; the two threads of a
 //            row agree on the row max through shared memory.
 // The pipeline does not drain between units: a unit's output is read out of TMEM, divided and
 // written during the next unit's first step, after that step's P is stored and before it is
@@ -305,79 +305,135 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem, uint32_t tP, uint64_t v,
     mma_ts_warp(tmem + kColO, tP, v, idesc_bf16_f32(128, 128, 0, 1), accumulate);
 }
 
-// One step's softmax for this thread's NC score columns at tS: agrees on the row max with the
-// partner thread, writes P as packed bf16 at tP, updates the reference max and the row sum, and
-// returns whether the reference moved (alpha: the factor that the old O and l take).  Columns
-// from nvalid on hold no key.  With !ok (an earlier wait failed) the thread only takes part in
-// the exchange.
-template <int NC, bool kPair>
-__device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, uint32_t loaded, float scale_log2,
-                                             float& m_used, float& l, float& alpha, float* xbuf, int& xe, int i, int r,
-                                             int bar_id, int nvalid) {
-  uint32_t s[NC];
-  if constexpr (NC == 128)
-    tmem_ld128_wait(tS, s);
-  else
-    tmem_ld64_wait(tS, s);
-  if (nvalid < NC) {
+// 2^x of 16 score columns (scaled, less the reference max) as packed bf16, added to the row sums.
+__device__ __forceinline__ void exp_16(const uint32_t* s, float scale_log2, float neg_m, float (&sa)[4], float (&sb)[4],
+                                       uint32_t (&pk)[8]) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+  for (int e = 0; e < 8; ++e) {
+    float x0, x1, p0, p1;
+    ffma2(x0, x1, __uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), scale_log2, scale_log2, neg_m, neg_m);
+    if ((kPolyMask >> e) & 1u) {
+      exp2_quartic2(x0, x1, p0, p1);
+    } else {
+      p0 = ex2_approx(x0);
+      p1 = ex2_approx(x1);
+    }
+    fadd2(sa[e & 3], sb[e & 3], sa[e & 3], sb[e & 3], p0, p1);
+    pk[e] = pack_bf16x2(p0, p1);
+  }
+}
+
+// A row's running softmax: the reference max, the row sum against it, and the factor that the old
+// O and l take where the reference moved in the last step.
+struct RowState {
+  float m_used, l, alpha;
+  // Agrees with the partner thread on the row max, mx being this thread's; true: it moved.
+  __device__ __forceinline__ bool update(bool ok, float mx, float scale_log2, float* xbuf, int& xe, int i, int r, int bar_id) {
+    mx = fmaxf(mx, fwd::pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
+    alpha = 1.f;
+    if (!ok) return false;
+    const float m_new = fmaxf(m_used, mx * scale_log2);
+    const bool need = m_new > m_used + kRescaleThreshold;
+    if (need) {
+      alpha = ex2_approx(m_used - m_new);
+      m_used = m_new;
+    }
+    l *= alpha;
+    return need;
+  }
+};
+
+// The scores are in registers: their columns may be overwritten.
+template <bool kPair>
+__device__ __forceinline__ void scores_loaded(bool ok, uint32_t loaded) {
+  if (!ok) return;
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive<kPair>(loaded);
+}
+
+// One step's softmax for this thread's 128 score columns at tS, of which the first nvalid hold
+// keys: writes P as packed bf16 at tP; true: the reference max moved.  With !ok (an earlier wait
+// failed) the thread only takes part in the exchange.
+template <bool kPair>
+__device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, uint32_t loaded, float scale_log2,
+                                             RowState& st, float* xbuf, int& xe, int i, int r, int bar_id, int nvalid) {
+  uint32_t s[128];
+  tmem_ld128_wait(tS, s);
+  if (nvalid < 128) {
+#pragma unroll
+    for (int c = 0; c < 128; ++c)
       if (c >= nvalid) s[c] = 0xff800000u;
   }
-  if (ok) {
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) arrive<kPair>(loaded);
-  }
+  scores_loaded<kPair>(ok, loaded);
   float mxs[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    mxs[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[NC - 8 + e]));
+    mxs[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[120 + e]));
 #pragma unroll
-    for (int c = 8 + e; c < NC - 8; c += 16)
+    for (int c = 8 + e; c < 120; c += 16)
       mxs[e] = max3f(mxs[e], __uint_as_float(s[c]), __uint_as_float(s[c + 8]));
   }
-  float mx = max3f(max3f(mxs[0], mxs[1], mxs[2]), max3f(mxs[3], mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]));
-  mx = fmaxf(mx, fwd::pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
-  alpha = 1.f;
+  const float mx = max3f(max3f(mxs[0], mxs[1], mxs[2]), max3f(mxs[3], mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]));
+  const bool need = st.update(ok, mx, scale_log2, xbuf, xe, i, r, bar_id);
   if (!ok) return false;
-  const float m_new = fmaxf(m_used, mx * scale_log2);
-  const bool need = m_new > m_used + kRescaleThreshold;
-  if (need) {
-    alpha = ex2_approx(m_used - m_new);
-    m_used = m_new;
-  }
-  l *= alpha;
-  const float neg_m = -m_used;
   float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int g = 0; g < NC / 16; ++g) {
+  for (int g = 0; g < 8; ++g) {
     uint32_t pk[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float x0, x1, p0, p1;
-      ffma2(x0, x1, __uint_as_float(s[16 * g + 2 * e]), __uint_as_float(s[16 * g + 2 * e + 1]), scale_log2, scale_log2,
-            neg_m, neg_m);
-      if ((kPolyMask >> e) & 1u) {
-        exp2_quartic2(x0, x1, p0, p1);
-      } else {
-        p0 = ex2_approx(x0);
-        p1 = ex2_approx(x1);
-      }
-      fadd2(sa[e & 3], sb[e & 3], sa[e & 3], sb[e & 3], p0, p1);
-      pk[e] = pack_bf16x2(p0, p1);
-    }
+    exp_16(s + 16 * g, scale_log2, -st.m_used, sa, sb, pk);
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[8 * g + e] = pk[e];
   }
-  l += ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
+  st.l += ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
 #pragma unroll
-  for (int h = 0; h < NC / 64; ++h) {
+  for (int h = 0; h < 2; ++h) {
     uint32_t w[32];
 #pragma unroll
     for (int e = 0; e < 32; ++e) w[e] = s[32 * h + e];
     tmem_st32(tP + 32 * h, w);
   }
+  return need;
+}
+
+// The same over at most 64 columns, in sixteens: only those below n16 are worked on and written
+// (a step's softmax costs by its keys; against one that masks a step's rest: a pair of
+// prompts of 512 and 203 keys 205 -> 197 us, 77 keys 65.9 -> 64.8 us).
+template <bool kPair>
+__device__ __forceinline__ bool softmax_few(bool ok, uint32_t tS, uint32_t tP, uint32_t loaded, float scale_log2,
+                                            RowState& st, float* xbuf, int& xe, int i, int r, int bar_id, int n16,
+                                            int nvalid) {
+  uint32_t s[64];
+  tmem_ld64_wait(tS, s);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (g >= n16) continue;
+    if (16 * g + 16 > nvalid) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (16 * g + e >= nvalid) s[16 * g + e] = 0xff800000u;
+    }
+    float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
+#pragma unroll
+    for (int e = 2; e < 16; e += 4) {
+      a = max3f(a, __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + e + 1]));
+      if (e + 2 < 16) b = max3f(b, __uint_as_float(s[16 * g + e + 2]), __uint_as_float(s[16 * g + e + 3]));
+    }
+    mx = max3f(mx, a, b);
+  }
+  scores_loaded<kPair>(ok, loaded);
+  const bool need = st.update(ok, mx, scale_log2, xbuf, xe, i, r, bar_id);
+  if (!ok) return false;
+  float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if (g >= n16) continue;
+    uint32_t pk[8];
+    exp_16(s + 16 * g, scale_log2, -st.m_used, sa, sb, pk);
+    tmem_st8(tP + 8 * g, pk);
+  }
+  st.l += ((sa[0] + sb[0]) + (sa[1] + sb[1])) + ((sa[2] + sb[2]) + (sa[3] + sb[3]));
   return need;
 }
 
@@ -767,7 +823,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       if (!ok) return;
       tc_fence_after();
       const Row y = unit_row(p, px, r);
-      const int64_t row = (static_cast<int64_t>(px.b) * p.heads + (y.ok ? y.head : 0)) * p.Lq + (y.ok ? y.q : 0);
+      const int row = y.ok ? (px.b * p.heads + y.head) * p.Lq + y.q : 0;  // (rows in all fit 31 bits)
       if constexpr (kPair) {
         // through shared memory and a TMA store of the warp's 32 rows x 64 channels, 4 KB each
         const uint32_t off = M::kOffOut + warp * 4096;
@@ -821,7 +877,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         }
         continue;
       }
-      float m_used = -INFINITY, l = 0.f;
+      RowState st = {-INFINITY, 0.f, 1.f};
       // a warp without query rows (few rows, the last tile of a head) does no softmax: what its
       // rows of P and O hold reaches no other row (one token over 115201 + 70007 keys: 119 us
       // with all warps' exponentials in the way)
@@ -830,24 +886,27 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         const int e = G & 1;
         if (ok) ok = warp_wait(s_full + e, (G >> 1) & 1, abort, 160);  // (committed to this CTA too)
         if (ok) tc_fence_after();
-        float alpha = 1.f;
         bool need = false;
+        const uint32_t tS = tmem + fwd::col_s(e) + lane_off, tP = tmem + fwd::col_p(e) + lane_off;
+        const uint32_t loaded = lead_bar<kPair>(s_read + e);
+        const bool two = c.in_step() == 2;
+        const int keys = c.keys(2 * c.t + (two ? i : 0));  // of this warpgroup's chunk
         if (!act) {
-          if (ok && lane == 0) arrive<kPair>(lead_bar<kPair>(s_read + e));
-        } else if (c.in_step() == 2)
-          need = softmax_step<128, kPair>(ok, tmem + fwd::col_s(e) + 128 * i + lane_off, tmem + fwd::col_p(e) + 64 * i + lane_off,
-                                   lead_bar<kPair>(s_read + e), p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
-                                   c.keys(2 * c.t + i));
-        else
-          need = softmax_step<64, kPair>(ok, tmem + fwd::col_s(e) + 64 * i + lane_off, tmem + fwd::col_p(e) + 32 * i + lane_off,
-                                  lead_bar<kPair>(s_read + e), p.scale_log2, m_used, l, alpha, xbuf, xe, i, r, bar_id,
-                                  min(max(c.keys(2 * c.t) - 64 * i, 0), 64));
+          if (ok && lane == 0) arrive<kPair>(loaded);
+        } else if (two && keys > 64) {
+          need = softmax_step<kPair>(ok, tS + 128 * i, tP + 64 * i, loaded, p.scale_log2, st, xbuf, xe, i, r, bar_id, keys);
+        } else {
+          // a single chunk: this warpgroup's half of its sixteens; the second chunk, up to 64 keys
+          const int n16 = two ? (keys + 15) >> 4 : (keys + 31) >> 5, first = two ? 0 : 16 * n16 * i;
+          need = softmax_few<kPair>(ok, tS + (two ? 128 * i : first), tP + (two ? 64 * i : first / 2), loaded, p.scale_log2,
+                                    st, xbuf, xe, i, r, bar_id, n16, keys - first);
+        }
         if (ok && c.t == 0 && pending) write_out();
         if (ok && c.t > 0 && __any_sync(0xffffffffu, need)) {
           ok = warp_wait(o_done, (G - 1) & 1, abort, 161);
           if (ok) {
             tc_fence_after();
-            fwd::rescale_o(tO, 2, alpha);
+            fwd::rescale_o(tO, 2, st.alpha);
           }
         }
         if (ok) {
@@ -857,11 +916,11 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           if (lane == 0) arrive<kPair>(lead_bar<kPair>(p_full + e));
         }
       }
-      const float l_all = act ? l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, l) : 1.f;
+      const float l_all = act ? st.l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, st.l) : 1.f;
       px = c.x;
       px.row += 128 * rank;
       p_inv = 1.f / l_all;
-      p_lse = (m_used + __log2f(l_all)) * 0.69314718055994531f;
+      p_lse = (st.m_used + __log2f(l_all)) * 0.69314718055994531f;
       pending = true;
     }
     if (ok && pending) write_out();
