@@ -77,43 +77,24 @@ static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
 // column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
 constexpr uint32_t kPolyMask = 0x22u;
 
-// A lane's row (32 q + lane, 256 bytes in two swizzled 64-channel halves at `tile`) into TMEM as
-// packed bf16 pairs.
-__device__ __forceinline__ void copy_row(uint32_t tile, int row, uint32_t t_dst) {
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t w[32];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint32_t at = tile + half * kHalf + row * 128 + ((c ^ (row & 7)) << 4);
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
-                   : "r"(at)
-                   : "memory");
-    }
-    tmem_st32(t_dst + 32 * half, w);
-  }
+// Regions of 128 TMEM columns rotate: S of step G at region(G), dP (then dS) at the one after it.
+__device__ __forceinline__ int next_region(int r) { return r == 0 ? 2 : r - 1; }  // S of the next step
+__device__ __forceinline__ uint32_t col_s(int r) { return 128 * r; }
+__device__ __forceinline__ uint32_t col_dp(int r) { return 128 * (r == 2 ? 0 : r + 1); }
+
+// D = A B^T over 128 channels: A (Q or dO, K-major) and B (a K-major tile of the step's 128 keys;
+// pair: 64 of them in either CTA) from shared memory.
+template <bool kPair>
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc) {
+  mma_ss_128<kPair, kHalf, kPair ? kHalf / 2 : kHalf>(d_tmem, a_desc, b_desc,
+                                                      kPair ? idesc_bf16_f32(256, 128, 0, 0) : bdq::kIdescS, 0);
 }
 
-// D = A B^T over 128 channels: A (Q or dO) from TMEM, B a K-major tile of the step's 128 keys (pair:
-// 64 of them in either CTA).
+// dQ (+)= dS K over 16 keys (dS of keys [16kk, 16kk + 16) at the columns of its region t_ds that
+// their thread wrote).
 template <bool kPair>
-__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc) {
-  fwd::opaque(b_desc);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t o = (kk >> 2) * (kPair ? kHalf / 2 : kHalf) + (kk & 3) * 32;
-    if constexpr (kPair)
-      mma_ts_pair_warp(d_tmem, a_tmem + 8 * kk, fwd::desc_add(b_desc, o), idesc_bf16_f32(256, 128, 0, 0), kk > 0);
-    else
-      mma_ts_warp(d_tmem, a_tmem + 8 * kk, fwd::desc_add(b_desc, o), bdq::kIdescS, kk > 0);
-  }
-}
-
-// dQ (+)= dS K over 16 keys (dS of keys [16kk, 16kk + 16) at the columns that their thread wrote).
-template <bool kPair>
-__device__ __forceinline__ void issue_dq(uint32_t tmem, int kk, uint64_t k_desc, bool accumulate) {
-  const uint32_t ds = tmem + bdq::kColDP + 64 * (kk >> 2) + 8 * (kk & 3);
+__device__ __forceinline__ void issue_dq(uint32_t tmem, uint32_t t_ds, int kk, uint64_t k_desc, bool accumulate) {
+  const uint32_t ds = t_ds + 64 * (kk >> 2) + 8 * (kk & 3);
   if constexpr (kPair)
     mma_ts_pair_warp(tmem + bdq::kColDQ, ds, fwd::desc_add(k_desc, kk * 2048), idesc_bf16_f32(256, 128, 0, 1), accumulate);
   else
@@ -137,11 +118,7 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
   using M = Mem<kPair>;
   using Cur = crossf::Cursor<kPair ? 256 : 128>;
   constexpr int kK = M::kK, kV = M::kV, kCtas = kPair ? 2 : 1;
-  using bdq::kColDO;
-  using bdq::kColDP;
   using bdq::kColDQ;
-  using bdq::kColQ;
-  using bdq::kColS;
   using fwd::desc_add;
   using fwd::warp_wait;
   extern __shared__ uint8_t smem_raw[];
@@ -154,10 +131,10 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = raw + pad;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* qd_full = bars;              // Q and dO of a unit have landed in the staging buffer
-  uint64_t* q_free = bars + 1;           // Q's half may be loaded again (pair: 4, else 8)
-  uint64_t* do_free = bars + 2;          // dO's half (4)
-  uint64_t* q_copied = bars + 3;         // single: the unit's Q has been read from there (4)
+  uint64_t* q_full = bars;               // Q of a unit has landed
+  uint64_t* q_empty = bars + 1;
+  uint64_t* do_full = bars + 2;          // dO
+  uint64_t* do_empty = bars + 3;
   uint64_t* k_land = bars + 4;           // [kK] K of the dQ product has landed in this CTA
   uint64_t* k2_full = k_land + kK;       // [kK] handed over (by each CTA)
   uint64_t* k2_empty = k2_full + kK;     // [kK]
@@ -165,18 +142,16 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
   uint64_t* k_empty = k_full + kK;       // [kK]
   uint64_t* v_full = k_empty + kK;       // [kV]
   uint64_t* v_empty = v_full + kV;       // [kV]
-  uint64_t* s_full = v_empty + kV;       // S of a step ready
-  uint64_t* s_read = s_full + 1;         // loaded (8 per CTA)
-  uint64_t* dp_full = s_full + 2;        // dP of a step ready
-  uint64_t* ds_full = s_full + 3;        // dS written (8 per CTA)
-  uint64_t* dq_done = s_full + 4;        // every dQ product of a unit done
-  uint64_t* dq_free = s_full + 5;        // dQ read out (8 per CTA)
-  uint64_t* qa_full = s_full + 6;        // the unit's Q and dO are in TMEM (8 per CTA)
-  uint64_t* drain = s_full + 7;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
-  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 8) + 1;
-  int* range = reinterpret_cast<int*>(s_full + 9);  // [2]
-  static_assert(4 + 5 * kK + 2 * kV + 10 <= 320 / 8, "barriers must fit their 320 bytes");
+  uint64_t* s_full = v_empty + kV;       // [2] S of a step (by its parity) ready
+  uint64_t* s_read = s_full + 2;         // [2] loaded (8 per CTA)
+  uint64_t* dp_full = s_full + 4;        // [2] dP of a step ready
+  uint64_t* ds_full = s_full + 6;        // [2] dS written (8 per CTA); a unit's first: also the previous dQ read
+  uint64_t* dq_done = s_full + 8;        // every dQ product of a unit done
+  uint64_t* drain = s_full + 9;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 10);
+  volatile int* abort = reinterpret_cast<volatile int*>(s_full + 10) + 1;
+  int* range = reinterpret_cast<int*>(s_full + 11);  // [2]
+  static_assert(4 + 5 * kK + 2 * kV + 12 <= 320 / 8, "barriers must fit their 320 bytes");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
@@ -186,10 +161,10 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     tma_prefetch_map(&tmDO);
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
-    mbar_init(qd_full, 1);
-    mbar_init(q_free, kPair ? 4 : 8);
-    mbar_init(do_free, 4);
-    mbar_init(q_copied, 4);
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(do_full, 1);
+    mbar_init(do_empty, 1);
     for (int s = 0; s < kK; ++s) {
       mbar_init(k_land + s, 1);
       mbar_init(k2_full + s, kCtas);
@@ -201,13 +176,13 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       mbar_init(v_full + s, 1);
       mbar_init(v_empty + s, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_read, 8 * kCtas);
-    mbar_init(dp_full, 1);
-    mbar_init(ds_full, 8 * kCtas);
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(s_full + e, 1);
+      mbar_init(s_read + e, 8 * kCtas);
+      mbar_init(dp_full + e, 1);
+      mbar_init(ds_full + e, 8 * kCtas);
+    }
     mbar_init(dq_done, 1);
-    mbar_init(dq_free, 8 * kCtas);
-    mbar_init(qa_full, 8 * kCtas);
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
@@ -314,16 +289,24 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
         int ld = 0, un = 0;
         bool ok = true;
         for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
-          ok = mbar_wait(do_free, (un & 1) ^ 1, abort, 173);
+          const int row = c.x.row + 128 * rank;
+          auto load = [&](uint64_t* full, uint64_t* empty, uint32_t off, const CUtensorMap* map, int g, int kvh, int b,
+                          int site) -> bool {
+            if (!mbar_wait(empty, (un & 1) ^ 1, abort, site)) return false;
+            if (lead) mbar_arrive_expect_tx(full, kCtas * p.q_bytes);
+            if constexpr (kPair) {
+              const uint32_t bar = lead_bar<kPair>(full);
+              tma_load_5d_pair(smem + off, map, bar, 0, row, g, kvh, b);
+              tma_load_5d_pair(smem + off + kHalf, map, bar, 64, row, g, kvh, b);
+            } else {
+              tma_load_5d(smem + off, map, full, 0, row, g, kvh, b);
+              tma_load_5d(smem + off + kHalf, map, full, 64, row, g, kvh, b);
+            }
+            return true;
+          };
+          ok = load(q_full, q_empty, M::kOffQ, &tmQ, c.x.g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb, 173) &&
+               load(do_full, do_empty, M::kOffDO, &tmDO, c.x.g * p.dg, c.x.kvh * p.dk, c.x.b * p.db, 174);
           if (!ok) break;
-          const int g = c.x.g, row = c.x.row + 128 * rank;
-          mbar_arrive_expect_tx(qd_full, 2 * p.q_bytes);
-          tma_load_5d(smem + M::kOffDO, &tmDO, qd_full, 0, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
-          tma_load_5d(smem + M::kOffDO + kHalf, &tmDO, qd_full, 64, row, g * p.dg, c.x.kvh * p.dk, c.x.b * p.db);
-          ok = mbar_wait(q_free, (un & 1) ^ 1, abort, 174);
-          if (!ok) break;
-          tma_load_5d(smem + M::kOffQ, &tmQ, qd_full, 0, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
-          tma_load_5d(smem + M::kOffQ + kHalf, &tmQ, qd_full, 64, row, g * p.qg, c.x.kvh * p.qk, c.x.b * p.qb);
           if (c.reuse(kV)) continue;
           for (int j = 0; j < c.n; ++j, ++ld) {
             const int st = ld % kV;
@@ -348,64 +331,76 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
       const uint64_t dKk = smem_desc_sw128(sbase + M::kOffK, 16, 1024);      // K-major
       const uint64_t dKm = smem_desc_sw128(sbase + M::kOffK2, kHalf, 1024);  // MN-major
       const uint64_t dVk = smem_desc_sw128(sbase + M::kOffV, 16, 1024);
+      const uint64_t dQk = smem_desc_sw128(sbase + M::kOffQ, 16, 1024), dDOk = smem_desc_sw128(sbase + M::kOffDO, 16, 1024);
       uint64_t* ks_full = kPair ? k_full : k2_full;  // K of the scores
-      Cur c;
-      c.start(p, begin, end);
-      int ks = 0, vs = 0, un = 0, G = 0;  // ring positions of the unit's first chunk; units, steps before
-      bool ok = true;
-      for (c.settle(p); ok && c.valid(); c.next_unit(p), ++un) {
-        const bool k_reuse = c.reuse(kK), k_keep = c.keep(p, kK), v_reuse = c.reuse(kV), v_keep = c.keep(p, kV);
-        const int n = c.n;
-        auto issue_s = [&](int t) -> bool {  // once S of the step before has been loaded
-          const int st = (ks + t) % kK;
-          if (!k_reuse && !wait_lead<kPair>(ks_full + st, ((ks + t) / kK) & 1, abort, 181)) return false;
-          if (G + t > 0 && !wait_lead<kPair>(s_read, (G + t - 1) & 1, abort, 182)) return false;
-          tc_fence_after();
-          issue_qk<kPair>(tmem + kColS, tmem + kColQ, desc_add(dKk, st * M::kEntry));
-          commit<kPair>(s_full);
-          if (kPair && !k_keep) commit<kPair>(k_empty + st);
-          return true;
-        };
-        // dP (after the dQ product that read dS(t - 1) from its columns), V being in
-        auto wait_v = [&](int t) -> bool {
-          return v_reuse || wait_lead<kPair>(v_full + (vs + t) % kV, ((vs + t) / kV) & 1, abort, 183);
-        };
-        auto issue_dp = [&](int t) {
-          const int st = (vs + t) % kV;
-          issue_qk<kPair>(tmem + kColDP, tmem + kColDO, desc_add(dVk, st * M::kEntry));
-          commit<kPair>(dp_full);
-          if (!v_keep) commit<kPair>(v_empty + st);
-        };
-        ok = wait_v(0) && wait_lead<kPair>(qa_full, un & 1, abort, 180) && issue_s(0);
-        if (ok) issue_dp(0);
-        for (int t = 0; t < n && ok; ++t) {
-          if (t + 1 < n) ok = issue_s(t + 1);
-          // everything but dS is waited for before dS: from its arrival the elementwise warps wait
-          // for dP(t + 1)
-          const int st = (ks + t) % kK, n16 = (c.keys(t) + 15) >> 4;
-          if (ok && kPair && !k_reuse) ok = wait_lead<kPair>(k2_full + st, ((ks + t) / kK) & 1, abort, 186);
-          if (ok && t + 1 < n) ok = wait_v(t + 1);
-          if (ok && t == 0) ok = wait_lead<kPair>(dq_free, (un & 1) ^ 1, abort, 185);
-          uint64_t k = desc_add(dKm, st * M::kEntry);
-          fwd::opaque(k);
-          if (ok) ok = wait_lead<kPair>(ds_full, (G + t) & 1, abort, 184);
-          if (!ok) break;
-          tc_fence_after();
-          if (n16 == 8) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) issue_dq<kPair>(tmem, kk, k, t > 0 || kk > 0);
-          } else {  // the last chunk: only the sixteens that hold keys
-#pragma unroll 1
-            for (int kk = 0; kk < n16; ++kk) issue_dq<kPair>(tmem, kk, k, t > 0 || kk > 0);
-          }
-          if (t + 1 < n) issue_dp(t + 1);
-          if (!k_keep) commit<kPair>(k2_empty + st);
+      Cur sc, dc;                  // the steps whose S and dP, and whose dQ product come next
+      int ks = 0, vs = 0, kd = 0;  // ring positions of their units' first chunks
+      int qn = 0;                  // units before sc's
+      int rs = 0;                  // region of S of the step whose dQ product comes next
+      sc.start(p, begin, end);
+      sc.settle(p);
+      // S of sc's step, the G-th, into the region that dS(G - 2) held (its product was issued)
+      auto issue_s = [&](int G, int region) -> bool {
+        const int pos = ks + sc.t, st = pos % kK;
+        const bool reuse = sc.reuse(kK), keep = sc.keep(p, kK);
+        if (sc.t == 0 && !wait_lead<kPair>(q_full, qn & 1, abort, 180)) return false;
+        if (!reuse && !wait_lead<kPair>(ks_full + st, (pos / kK) & 1, abort, 181)) return false;
+        tc_fence_after();
+        issue_qk<kPair>(tmem + col_s(region), dQk, desc_add(dKk, st * M::kEntry));
+        commit<kPair>(s_full + (G & 1));
+        if (kPair && !keep) commit<kPair>(k_empty + st);
+        if (sc.t + 1 == sc.n) commit<kPair>(q_empty);
+        return true;
+      };
+      // dP of the same step, into the region of S(G - 1), which has been loaded
+      auto issue_dp = [&](int G, int region) -> bool {
+        const int pos = vs + sc.t, st = pos % kV;
+        const bool reuse = sc.reuse(kV), keep = sc.keep(p, kV);
+        if (sc.t == 0 && !wait_lead<kPair>(do_full, qn & 1, abort, 182)) return false;
+        if (!reuse && !wait_lead<kPair>(v_full + st, (pos / kV) & 1, abort, 183)) return false;
+        if (G > 0 && !wait_lead<kPair>(s_read + ((G - 1) & 1), ((G - 1) >> 1) & 1, abort, 184)) return false;
+        tc_fence_after();
+        issue_qk<kPair>(tmem + col_dp(region), dDOk, desc_add(dVk, st * M::kEntry));
+        commit<kPair>(dp_full + (G & 1));
+        if (!keep) commit<kPair>(v_empty + st);
+        if (sc.t + 1 == sc.n) {
+          commit<kPair>(do_empty);
+          ++qn;
+          if (!sc.keep(p, kK)) ks += sc.n;
+          if (!keep) vs += sc.n;
         }
+        return true;
+      };
+      bool ok = true;
+      if (sc.valid()) ok = issue_s(0, rs) && issue_dp(0, rs);
+      dc = sc;
+      if (sc.valid()) sc.next_chunk(p);
+      for (int G = 0; ok && dc.valid(); ++G) {
+        const int rn = next_region(rs);
+        if (sc.valid()) ok = issue_s(G + 1, rn) && issue_dp(G + 1, rn);
+        const int pos = kd + dc.t, st = pos % kK, n16 = (dc.keys(dc.t) + 15) >> 4;
+        const bool keep = dc.keep(p, kK);
+        if (ok && kPair && !dc.reuse(kK)) ok = wait_lead<kPair>(k2_full + st, (pos / kK) & 1, abort, 185);
+        uint64_t k = desc_add(dKm, st * M::kEntry);
+        fwd::opaque(k);
+        const uint32_t t_ds = tmem + col_dp(rs);
+        if (ok) ok = wait_lead<kPair>(ds_full + (G & 1), (G >> 1) & 1, abort, 186);
         if (!ok) break;
-        commit<kPair>(dq_done);
-        G += n;
-        if (!k_keep) ks += n;
-        if (!v_keep) vs += n;
+        tc_fence_after();
+        if (n16 == 8) {
+          mma_ts_128<kPair, 64>(tmem + kColDQ, t_ds, k, kPair ? idesc_bf16_f32(256, 128, 0, 1) : bdq::kIdescDQ, dc.t > 0);
+        } else {  // the last chunk: only the sixteens that hold keys
+#pragma unroll 1
+          for (int kk = 0; kk < n16; ++kk) issue_dq<kPair>(tmem, t_ds, kk, k, dc.t > 0 || kk > 0);
+        }
+        if (!keep) commit<kPair>(k2_empty + st);
+        if (dc.t + 1 == dc.n) {
+          commit<kPair>(dq_done);
+          if (!keep) kd += dc.n;
+        }
+        dc = sc;
+        if (sc.valid()) sc.next_chunk(p);
+        rs = rn;
       }
       if constexpr (kPair)
         mma_commit_pair_warp(drain, 1);
@@ -419,25 +414,22 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     const int h = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float kLog2e = 1.4426950408889634f;
-    const bool staged = kPair || (p.n_split == 1 && p.pk == 1);  // dQ through shared memory
-    int G = 0, un = 0;
-    bool ok = true, stored = false;  // stored: this lane has a TMA store that may still read the buffer
-    crossf::Unit px = {};            // the unit whose dQ is still in TMEM
+    int G = 0, un = 0, rs = 0;
+    bool ok = true;
+    crossf::Unit px = {};  // the unit whose dQ is still in TMEM
     // dQ = scale * accumulator, channels [64h, 64h + 64) of this thread's row of unit px
     auto write_out = [&](int unit) -> bool {
       if (!warp_wait(dq_done, unit & 1, abort, 190)) return false;
       tc_fence_after();
       const uint32_t tD = tmem + kColDQ + 64 * h + lane_off;
-      if (staged) {
+      if constexpr (kPair) {
         const uint32_t off = M::kOffOut + h * kHalf + quarter * 4096;
-        if (kPair && lane == 0) tma_store_wait_read();  // the unit before has left the buffer
+        if (lane == 0) tma_store_wait_read();  // the unit before has left the buffer
         __syncwarp();
         crossf::stage_o(tD, p.scale, sbase + off);
         fence_proxy_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          arrive<kPair>(lead_bar<kPair>(dq_free));
           const int r0 = px.row + 32 * quarter;
           if (r0 < p.Lq) {
             tma_store_5d(&tmDQ, smem + off, 64 * h, r0, px.g, px.kvh, px.b);
@@ -455,75 +447,62 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
           const int64_t at = y.ok ? px.b * p.dq_s[0] + y.head * p.dq_s[1] + y.q * p.dq_s[2] : 0;
           fwd::store_o(tD, 2, p.scale, reinterpret_cast<uint4*>(p.dq + at) + 8 * h, y.ok);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dq_free);
       }
       return true;
     };
-    Cur c;
-    c.start(p, begin, end);
-    for (; ok && c.valid(); c.advance(p)) {
-      crossf::Unit x = c.x;  // (row: this CTA's first)
+    // the row statistics of a unit, loaded while the unit before is worked on
+    float n_lse = 0.f, n_dd = 0.f;
+    auto load_stats = [&](const Cur& u) {
+      crossf::Unit x = u.x;
       x.row += 128 * rank;
       const crossf::Row y = crossf::unit_row(p, x, r);
-      const int64_t bh = static_cast<int64_t>(c.x.b) * p.heads + y.head;
+      const int64_t at = (static_cast<int64_t>(x.b) * p.heads + y.head) * p.Lq + y.q;
+      n_lse = y.ok ? p.lse[at] : 0.f;
+      n_dd = y.ok ? p.delta[at] : 0.f;
+    };
+    Cur c, nx;
+    c.start(p, begin, end);
+    if (c.valid()) load_stats(c);
+    for (; ok && c.valid(); c = nx) {
+      crossf::Unit x = c.x;  // (row: this CTA's first)
+      x.row += 128 * rank;
+      const float neg_lse2 = -n_lse * kLog2e, dd = n_dd;
+      nx = c;
+      nx.advance(p);
+      if (nx.valid()) load_stats(nx);
       if (c.n == 0) {  // no keys: no gradient
+        const crossf::Row y = crossf::unit_row(p, x, r);
         if (y.ok) {
           if (p.n_split > 1) {
+            const int64_t bh = static_cast<int64_t>(x.b) * p.heads + y.head;
             float4* dst = reinterpret_cast<float4*>(
-                p.dq_part + (c.x.part * static_cast<int64_t>(p.B) * p.heads * p.Lq + bh * p.Lq + y.q) * 128) + 16 * h;
+                p.dq_part + (x.part * static_cast<int64_t>(p.B) * p.heads * p.Lq + bh * p.Lq + y.q) * 128) + 16 * h;
 #pragma unroll
             for (int e = 0; e < 16; ++e) dst[e] = make_float4(0.f, 0.f, 0.f, 0.f);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(p.dq + c.x.b * p.dq_s[0] + y.head * p.dq_s[1] + y.q * p.dq_s[2]) + 8 * h;
+            uint4* dst = reinterpret_cast<uint4*>(p.dq + x.b * p.dq_s[0] + y.head * p.dq_s[1] + y.q * p.dq_s[2]) + 8 * h;
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         continue;
       }
-      const int64_t lrow = bh * p.Lq + y.q;
-      const float neg_lse2 = y.ok ? -p.lse[lrow] * kLog2e : 0.f, dd = y.ok ? p.delta[lrow] : 0.f;
-      // Q (h = 0) or dO (h = 1) of the row into TMEM; the previous unit's products that read them
-      // have completed: this warp has seen its last scores and dP
-      ok = warp_wait(qd_full, un & 1, abort, 191);
-      if (!ok) break;
-      copy_row(sbase + (h ? M::kOffDO : M::kOffQ), r, tmem + (h ? kColDO : kColQ) + lane_off);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        arrive<kPair>(lead_bar<kPair>(qa_full));
-        mbar_arrive(h ? do_free : kPair ? q_free : q_copied);
-      }
-      if (un > 0) {
-        // (single: these rows of dQ go where the other warp's Q was)
-        if (!kPair && h) ok = warp_wait(q_copied, un & 1, abort, 194);
-        if (ok) ok = write_out(un - 1);
-        if (!ok) break;
-        stored = !kPair && staged;
-      }
-      if (!kPair && !stored && lane == 0) mbar_arrive(q_free);
-      for (c.t = 0; c.t < c.n; ++c.t, ++G) {
+      // a warp without query rows works on nothing: its rows of dS and dQ reach no other row
+      const bool act = p.pk > 1 ? 32 * quarter < p.pk * p.Lq : x.row + 32 * quarter < p.Lq;
+      for (c.t = 0; c.t < c.n; ++c.t, ++G, rs = next_region(rs)) {
+        const int e2 = G & 1;
         const int nv = c.keys(c.t) - 64 * h;  // keys of this thread's 64 columns
-        ok = warp_wait(s_full, G & 1, abort, 192);
+        const bool work = act && nv > 0;
+        ok = warp_wait(s_full + e2, (G >> 1) & 1, abort, 192);
         if (!ok) break;
         tc_fence_after();
-        if (stored) {  // dQ of the previous unit has left the buffer by now: Q may be loaded
-          if (lane == 0) {
-            tma_store_wait_read();
-            mbar_arrive(q_free);
-          }
-          stored = false;
-        }
         float pf[64];
-        {
+        if (work) {
           uint32_t s[64];
-          tmem_ld64_wait(tmem + kColS + 64 * h + lane_off, s);
+          tmem_ld64_wait(tmem + col_s(rs) + 64 * h + lane_off, s);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive<kPair>(lead_bar<kPair>(s_read));
+          if (lane == 0) arrive<kPair>(lead_bar<kPair>(s_read + e2));
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float x0, x1;
@@ -536,32 +515,41 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
               pf[e + 1] = ex2_approx(x1);
             }
           }
+        } else if (lane == 0) {
+          arrive<kPair>(lead_bar<kPair>(s_read + e2));
         }
-        ok = warp_wait(dp_full, G & 1, abort, 193);
+        ok = warp_wait(dp_full + e2, (G >> 1) & 1, abort, 193);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dp[64];
-        tmem_ld64_wait(tmem + kColDP + 64 * h + lane_off, dp);
-        uint32_t w[32];
+        if (work) {
+          const uint32_t tDP = tmem + col_dp(rs) + 64 * h + lane_off;
+          uint32_t dp[64];
+          tmem_ld64_wait(tDP, dp);
+          uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float a0, a1, d0, d1;
-          fadd2(a0, a1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), -dd, -dd);
-          ffma2(d0, d1, a0, a1, pf[e], pf[e + 1], 0.f, 0.f);
-          w[e >> 1] = pack_bf16x2(d0, d1);
-        }
-        if (nv < 64) {  // no key in these columns: their P and dP may be anything, dS is zero
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (2 * e >= nv) w[e] = 0u;
-            else if (2 * e + 1 >= nv) w[e] &= 0xffffu;
+          for (int e = 0; e < 64; e += 2) {
+            float a0, a1, d0, d1;
+            fadd2(a0, a1, __uint_as_float(dp[e]), __uint_as_float(dp[e + 1]), -dd, -dd);
+            ffma2(d0, d1, a0, a1, pf[e], pf[e + 1], 0.f, 0.f);
+            w[e >> 1] = pack_bf16x2(d0, d1);
           }
+          if (nv < 64) {  // no key in these columns: their P and dP may be anything, dS is zero
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (2 * e >= nv) w[e] = 0u;
+              else if (2 * e + 1 >= nv) w[e] &= 0xffffu;
+            }
+          }
+          tmem_st32(tDP, w);
+          tmem_wait_st();
         }
-        tmem_st32(tmem + kColDP + 64 * h + lane_off, w);
-        tmem_wait_st();
+        if (c.t == 0 && un > 0) {  // this step's dQ product overwrites the previous unit's dQ
+          ok = write_out(un - 1);
+          if (!ok) break;
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive<kPair>(lead_bar<kPair>(ds_full));
+        if (lane == 0) arrive<kPair>(lead_bar<kPair>(ds_full + e2));
       }
       px = x;
       ++un;

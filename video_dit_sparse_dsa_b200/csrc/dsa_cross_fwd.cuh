@@ -727,19 +727,10 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           const int pos = ks + (kPair ? sc.t : 2 * sc.t + b), st = pos % M::kK;
           if (!reuse && !wait_lead<kPair>(k_full + st, (pos / M::kK) & 1, abort, 151)) return false;
           tc_fence_after();
-          uint64_t q = desc_add(dQ, qs * kTile), k = desc_add(dK, st * kTile);
-          fwd::opaque(q);
-          fwd::opaque(k);
           const uint32_t idesc = kPair ? idesc_bf16_f32(256, nb == 2 ? 256 : 2 * sc.half_columns(), 0, 0)
                                        : idesc_bf16_f32(128, (sc.keys(2 * sc.t + b) + 15) & ~15, 0, 0);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-            if constexpr (kPair)
-              mma_ss_pair_warp(tmem + fwd::col_s(e), desc_add(q, o), desc_add(k, o), idesc, kk > 0);
-            else
-              mma_ss_warp(tmem + fwd::col_s(e) + 128 * b, desc_add(q, o), desc_add(k, o), idesc, kk > 0);
-          }
+          mma_ss_128<kPair, kHalf, kHalf>(tmem + fwd::col_s(e) + 128 * b, desc_add(dQ, qs * kTile), desc_add(dK, st * kTile),
+                                          idesc, 0);
           if (!keep) commit<kPair>(k_empty + st);
         }
         commit<kPair>(s_full + e);
@@ -774,8 +765,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
           const bool first = pc.t == 0 && b == 0;
           const uint32_t tP = tmem + fwd::col_p(e) + 64 * b;
           if (kk_n == 8) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk) issue_pv<kPair>(tmem, tP + 8 * kk, desc_add(v, kk * 2048), !first || kk > 0);
+            mma_ts_128<kPair, 32>(tmem + kColO, tP, v, idesc_bf16_f32(kPair ? 256 : 128, 128, 0, 1), !first);
           } else {  // the last chunk: only the sixteens that hold keys
 #pragma unroll 1
             for (int kk = 0; kk < kk_n; ++kk) issue_pv<kPair>(tmem, tP + 8 * kk, desc_add(v, kk * 2048), !first || kk > 0);

@@ -131,23 +131,13 @@ struct QChunk {
 
 // D (+)= A B^T over 128 channels, both K-major tiles of two 64-channel halves.
 __device__ __forceinline__ void issue_scores(uint32_t d_tmem, uint64_t a, uint64_t b) {
-  fwd::opaque(a);
-  fwd::opaque(b);
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) {
-    const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-    mma_ss_warp(d_tmem, fwd::desc_add(a, o), fwd::desc_add(b, o), kIdescS, kk > 0);
-  }
+  mma_ss_128<false, kHalf, kHalf>(d_tmem, a, b, kIdescS, 0);
 }
 
 // D (+)= A B over 64 queries: A (P^T at +0, dS^T at +16 of each thread's 32 columns) from TMEM, B
 // an MN-major tile of queries x channels.
 __device__ __forceinline__ void issue_grad(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, bool accumulate) {
-  fwd::opaque(b);
-#pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
-    mma_ts_warp(d_tmem, a_tmem + 32 * (kk >> 1) + 8 * (kk & 1), fwd::desc_add(b, kk * 2048), kIdescAcc,
-                accumulate || kk > 0);
+  mma_ts_64<32>(d_tmem, a_tmem, b, kIdescAcc, accumulate);
 }
 }  // namespace crosskv
 

@@ -514,6 +514,75 @@ __device__ __forceinline__ void mma_commit_pair_warp(uint64_t* bar, uint16_t cta
       : "memory");
 }
 
+// A whole accumulation of 16-wide steps in one statement: one election and one branch for all of its
+// products, where a product per statement (the forms above) issues one per 100 to 118 clocks,
+// whatever its 64 clocks of work at N = 128.  Called by every lane of a converged warp (a pair's: of
+// the even CTA); `accumulate` is the first step's, the others add.
+#define DSA_MMA_OPEN(regs)            \
+  "{\n\t.reg .pred p, e;\n\t" regs    \
+  "elect.sync _|e, 0xffffffff;\n\t"   \
+  "setp.ne.b32 p, %4, 0;\n\t"         \
+  "@!e bra DONE;\n\t"
+#define DSA_MMA_SS(cg, oa, ob)                     \
+  "add.s64 a, %1, " oa ";\n\tadd.s64 b, %2, " ob ";\n\t" \
+  "tcgen05.mma.cta_group::" cg ".kind::f16 [%0], a, b, %3, p;\n\t"
+#define DSA_MMA_TS(cg, oa, ob)                     \
+  "add.s32 a, %1, " oa ";\n\tadd.s64 b, %2, " ob ";\n\t" \
+  "tcgen05.mma.cta_group::" cg ".kind::f16 [%0], [a], b, %3, p;\n\t"
+#define DSA_MMA_ADD "setp.eq.b32 p, 0, 0;\n\t"
+#define DSA_MMA_DONE "DONE:\n\t}"
+
+// D (+)= A B^T over 128 channels: both K-major in shared memory in 64-channel halves of kHalfA and
+// kHalfB bytes.
+#define DSA_MMA_SS8(cg)                                                                        \
+  DSA_MMA_OPEN(".reg .b64 a, b;\n\t")                                                          \
+  DSA_MMA_SS(cg, "0", "0") DSA_MMA_ADD DSA_MMA_SS(cg, "2", "2") DSA_MMA_SS(cg, "4", "4")       \
+  DSA_MMA_SS(cg, "6", "6") DSA_MMA_SS(cg, "%5", "%6") DSA_MMA_SS(cg, "%5 + 2", "%6 + 2")       \
+  DSA_MMA_SS(cg, "%5 + 4", "%6 + 4") DSA_MMA_SS(cg, "%5 + 6", "%6 + 6") DSA_MMA_DONE
+template <bool kPair, int kHalfA, int kHalfB>
+__device__ __forceinline__ void mma_ss_128(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(DSA_MMA_SS8("2")::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHalfA >> 4),
+                 "n"(kHalfB >> 4));
+  else
+    asm volatile(DSA_MMA_SS8("1")::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHalfA >> 4),
+                 "n"(kHalfB >> 4));
+}
+
+// D (+)= A B over 128 (or 64) rows of B: A in TMEM as packed bf16 pairs, 8 columns per 16 rows, its
+// second half kHalfA columns after the first; B MN-major, 2048 bytes per 16 rows.
+#define DSA_MMA_TS8(cg)                                                                              \
+  DSA_MMA_OPEN(".reg .b32 a;\n\t.reg .b64 b;\n\t")                                                   \
+  DSA_MMA_TS(cg, "0", "0") DSA_MMA_ADD DSA_MMA_TS(cg, "8", "128") DSA_MMA_TS(cg, "16", "256")        \
+  DSA_MMA_TS(cg, "24", "384") DSA_MMA_TS(cg, "%5", "512") DSA_MMA_TS(cg, "%5 + 8", "640")            \
+  DSA_MMA_TS(cg, "%5 + 16", "768") DSA_MMA_TS(cg, "%5 + 24", "896") DSA_MMA_DONE
+#define DSA_MMA_TS4(cg)                                                                              \
+  DSA_MMA_OPEN(".reg .b32 a;\n\t.reg .b64 b;\n\t")                                                   \
+  DSA_MMA_TS(cg, "0", "0") DSA_MMA_ADD DSA_MMA_TS(cg, "8", "128") DSA_MMA_TS(cg, "%5", "256")        \
+  DSA_MMA_TS(cg, "%5 + 8", "384") DSA_MMA_DONE
+template <bool kPair, int kHalfA>
+__device__ __forceinline__ void mma_ts_128(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(DSA_MMA_TS8("2")::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHalfA));
+  else
+    asm volatile(DSA_MMA_TS8("1")::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHalfA));
+}
+template <int kHalfA>
+__device__ __forceinline__ void mma_ts_64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(DSA_MMA_TS4("1")::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(kHalfA));
+}
+#undef DSA_MMA_OPEN
+#undef DSA_MMA_SS
+#undef DSA_MMA_TS
+#undef DSA_MMA_ADD
+#undef DSA_MMA_DONE
+#undef DSA_MMA_SS8
+#undef DSA_MMA_TS8
+#undef DSA_MMA_TS4
+
 // ---------------------------------------------------------------- math
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
