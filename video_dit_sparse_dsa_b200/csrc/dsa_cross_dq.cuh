@@ -2,37 +2,41 @@
 // batch entry
 //   P_nm = exp(scale q_n.k_m - LSE_n),  dS_nm = P_nm (dO_n.v_m - D_n),  dQ_n = scale sum_m dS_nm k_m.
 //
-// As bwd_dq_kernel (the window backward's dQ pass) it recomputes S = Q K^T and dP = dO V^T on the
-// tensor cores 128 keys at a time, forms dS in registers and accumulates dQ += dS K in TMEM, with
-// Q and dO as TMEM operands.  What differs is the unit: a window holds thousands of keys, a
-// prompt one to four steps' worth, so here the time goes where units meet (that kernel took 9700
-// clocks per step on a 203 + 512-key pair of prompts, 1540 of them products):
-//   * Q and dO of the next unit are loaded by TMA during this one into a 64 KB staging buffer, and
-//     copied into TMEM by the elementwise warps (a row per thread) when this unit's last dS is
-//     written, while its last dQ product runs;
-//   * a unit's dQ is read out and written after that copy, while the next unit's first scores are
-//     computed, through shared memory and TMA stores (rows packed from several heads, and fp32
-//     parts, are stored directly);
+// Per 128 keys the tensor cores form S = Q K^T and dP = dO V^T again, the elementwise warps dS, and
+// dQ += dS K accumulates in TMEM: 1536 clocks of products, 768 of exponentials (a quarter of them
+// run on the FMA pipe).  A window holds thousands of keys, a prompt one to four steps' worth, so what
+// counts here is that nothing drains between units:
+//   * three regions of TMEM columns rotate: S of step G + 1 goes where dS of step G - 1 was, dP of
+//     step G + 1 where S of step G was, so both are ready when the elementwise warps end step G
+//     (with Q and dO as TMEM operands there was room for one of each, and dP waited for dS);
+//   * a unit's dQ is read out in the next unit's first step, after its dS is written and before it is
+//     handed over (that step's product overwrites dQ), and leaves through shared memory and TMA
+//     stores;
+//   * the row statistics of a unit are loaded during the unit before;
 //   * K and V of short key sequences stay in shared memory for all consecutive units of their kv
 //     head; a CTA's (pair's) units are a contiguous range of equal cost, as in the forward, whose
 //     units these are.
 // More than 128 rows per head run on CTA pairs, as in the forward (kPair): every product is one M
 // = 256 tcgen05.mma.cta_group::2 over 256 rows.  A CTA holds half of every operand, and K twice:
 // its half of a step's keys for the scores and its half of the channels for the dQ product, each
-// with a ring of its own and released by its own product.  On one CTA the K chunk of a step is held
-// from its scores, a step ahead, until its dQ product, and three 32 KB entries, all that fits, left
-// the next scores waiting for their load (3150 clocks per step; 480p pair 308 us).
+// with a ring of its own and released by its own product.  (24 heads x 35840 rows over 512 and 203
+// keys, whole backward: 645 us, and 695 with this pass on single CTAs.)
+//
+// What bounds it: 302 us there, 3300 clocks per step.  A step takes in 48 KB of K and V per CTA
+// and, over four steps, 96 KB of Q, dO and dQ, 36 bytes per clock and SM or 9 TB/s over the chip,
+// and the MMA warp goes through seven waits of 200 clocks, which follow one another.  Measured and
+// not kept: rings of two entries with two Q tiles (430 us); one wait per step for all loads, behind
+// a warp that collects them (336); dQ stored from registers, four V entries in its place (350).
 //
 // Persistent and warp-specialised, 384 threads:
 //   warp 8      TMA producer of K
 //   warp 10     TMA producer of V and of Q and dO
 //   warp 11     takes each K chunk of the dQ product as it lands, zeroes the rows past the last key
 //               that the product will read (against dS = 0, but 0 * NaN is NaN) and hands it over
-//   warp 9      MMA issuer (pair: the even CTA's), per step t: S(t + 1) once the elementwise warps
-//               hold S(t) in registers; dQ += dS(t) K(t) once dS(t) is written; then dP(t + 1)
+//   warp 9      MMA issuer (pair: the even CTA's), per step G: S(G + 1); dP(G + 1) once the
+//               elementwise warps hold S(G) in registers; dQ += dS(G) K(G) once dS(G) is written
 //   warps 0-7   elementwise, two threads per row: thread h takes keys [64h, 64h + 64) of a step
-// TMEM (512 columns): Q [0, 64) and dO [64, 128) as packed bf16 pairs, scores [128, 256), dP (then
-// dS) [256, 384), dQ [384, 512).
+// TMEM (512 columns): three regions of 128 [0, 384), dQ [384, 512).
 #pragma once
 
 #include <stdint.h>
@@ -58,9 +62,9 @@ namespace crossdq {
 constexpr int kThreads = bdq::kThreads;
 constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kHandWarp = 11;
 constexpr uint32_t kTile = 128 * 128 * 2, kHalf = kTile / 2;
-// Shared memory: 224 KB of tiles and the barriers.  Q and dO staging (32 KB each); single: K 3 and
-// V 2 chunks of 32 KB, dQ leaves through Q's staging; pair: K 3 entries of 64 keys (scores) and 3 of
-// 64 channels (dQ product), V 2 of 64 keys, 16 KB each, and 32 KB for dQ.
+// Shared memory: 224 KB of tiles and the barriers.  Q and dO (32 KB each); single: K 3 and V 2
+// chunks of 32 KB; pair: K 3 entries of 64 keys (scores) and 3 of 64 channels (dQ product), V 2 of
+// 64 keys, 16 KB each, and 32 KB through which dQ leaves.
 template <bool kPair>
 struct Mem {
   static constexpr int kK = 3, kV = 2;  // chunks
