@@ -273,7 +273,7 @@ dsa_status_t dsa_lstsq_solve(int32_t m, int32_t p, int32_t batch, const float* M
  * The operators around the sliding attention in a video transformer block: cross attention to
  * an encoder's states, rotary positions over (time, height, width), and the root-mean-square
  * norm.  Ownership, streams, capture and errors as above; every one is deterministic (the same
- * bits from run to run). */
+ * bits from run to run).  An output overlaps no input unless its function says so. */
 
 /* A view of a [B, heads, rows, d] tensor: the channels of a row are contiguous, the other
  * dimensions have strides in elements, so both head-major tensors and the token-major rows of
@@ -304,7 +304,7 @@ size_t dsa_cross_workspace_size(const dsa_cross_t* p, int32_t kind);
 /* Forward: writes out (a view like q's, strides of its own) and lse (fp32 [B, heads, Lq]).
  * Views: 16-byte aligned data, strides multiples of 8 elements and at least 128; the batch and
  * head strides of an input may be 0 (broadcast).  workspace: 256-byte aligned.  P is rounded to
- * bf16 before the value product (relative error 2^-9); scores, softmax statistics and sums are
+ * bf16 before the value product (relative error 2^-8); scores, softmax statistics and sums are
  * fp32.  With few query rows the keys are cut into parts whose fp32 partial results are joined
  * by a second launch. */
 dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_view_t* k, const dsa_view_t* v,

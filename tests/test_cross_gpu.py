@@ -178,6 +178,18 @@ def test_broadcast_inputs():
     ok()
 
 
+@pytest.mark.parametrize("Lq,Lk", [(7, 200), (1, 1300), (64, 77)])
+@pytest.mark.parametrize("which", ["q", "dout", "both"])
+def test_broadcast_heads_of_a_shared_kv_head(Lq, Lk, which):
+    """Few rows, whose heads are packed into one tile unless they are one head by a stride of 0."""
+    q, k, v, do = draw(18, 2, 6, 2, Lq, Lk)
+    if which != "dout":
+        q = q[:, 2:3].expand(2, 6, Lq, 128)
+    if which != "q":
+        do = do[:, 1:2].expand(2, 6, Lq, 128)
+    check(q, k, v, do, (Lk, Lk // 2), what=which)
+
+
 def test_outputs_through_strides_leave_neighbours():
     B, h, Lq, Lk = 2, 3, 150, 200
     q, k, v, do = draw(11, B, h, h, Lq, Lk)

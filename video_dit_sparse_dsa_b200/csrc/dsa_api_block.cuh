@@ -73,7 +73,9 @@ struct CrossPlan {
   int64_t kv_units;       // 128-key units of kv heads (dK, dV), at most; `tiles` query chunks each
 };
 
-dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
+// pack: a kv head's heads may share a unit.  (Not packing takes more units, so at most as many
+// parts of the keys and as much workspace.)
+dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c, bool pack = true) {
   if (p == nullptr) return DSA_ERR_INVALID_ARG;
   if (p->B <= 0 || p->heads <= 0 || p->kv_heads <= 0 || p->heads % p->kv_heads != 0 || p->Lq < 0 || p->Lk < 0)
     return DSA_ERR_INVALID_ARG;
@@ -81,7 +83,7 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
   if (p->dtype != DSA_F32 && p->dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
   if (p->dtype != DSA_BF16 || p->d != 128) return DSA_ERR_UNSUPPORTED;
   c->group = p->heads / p->kv_heads;
-  c->pk = c->group > 1 && p->Lq > 0 && p->Lq <= 64 ? (c->group < 128 / p->Lq ? c->group : 128 / p->Lq) : 1;
+  c->pk = pack && c->group > 1 && p->Lq > 0 && p->Lq <= 64 ? (c->group < 128 / p->Lq ? c->group : 128 / p->Lq) : 1;
   const int64_t tiles = c->pk > 1 ? (c->group + c->pk - 1) / c->pk
                                   : static_cast<int64_t>(c->group) * ((static_cast<int64_t>(p->Lq) + 127) / 128);
   const int64_t slices = static_cast<int64_t>(p->B) * p->kv_heads;
@@ -109,6 +111,10 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c) {
   if (c->kv_units > INT32_MAX) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
+
+// Several heads of a unit come in one TMA box, which cannot repeat a head: a view whose heads are
+// one (stride 0) is not packed.
+bool heads_broadcast(const dsa_view_t* v, const CrossPlan& c) { return c.pk > 1 && v->stride[1] == 0; }
 
 struct CrossWorkspace {
   float *part_o, *part_lse;                       // forward, split_q > 1
@@ -402,6 +408,7 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     return DSA_ERR_INVALID_ARG;
   if (p->Lk > 0 && (!view_ok(k, p->B, p->kv_heads, p->Lk, false) || !view_ok(v, p->B, p->kv_heads, p->Lk, false)))
     return DSA_ERR_INVALID_ARG;
+  if (heads_broadcast(q, c)) cross_plan(p, &c, false);
   const CrossWorkspace ws = cross_workspace(p, c, DSA_WS_FWD, workspace);
   if (ws.bytes > 0 && (workspace == nullptr || ws_bytes < ws.bytes || !aligned(workspace, kAlign)))
     return DSA_ERR_WORKSPACE;
@@ -483,6 +490,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
                     !view_ok(dk, p->B, p->kv_heads, p->Lk, true) || !view_ok(dv, p->B, p->kv_heads, p->Lk, true)))
     return DSA_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(kv_len, 4)) return DSA_ERR_INVALID_ARG;
+  if (heads_broadcast(q, c) || heads_broadcast(dout, c)) cross_plan(p, &c, false);
   const CrossWorkspace ws = cross_workspace(p, c, DSA_WS_BWD, workspace);
   if (ws.bytes > 0 && (workspace == nullptr || ws_bytes < ws.bytes || !aligned(workspace, kAlign)))
     return DSA_ERR_WORKSPACE;

@@ -190,10 +190,14 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
+  }
+  if (warp == 0) {
     int b, e;
     crossf::unit_range(p, blockIdx.x / kCtas, gridDim.x / kCtas, b, e);
-    range[0] = b;
-    range[1] = e;
+    if (lane == 0) {
+      range[0] = b;
+      range[1] = e;
+    }
   }
   if (warp == kMmaWarp) {
     if constexpr (kPair) {

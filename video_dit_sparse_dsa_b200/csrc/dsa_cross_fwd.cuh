@@ -123,25 +123,35 @@ __device__ __forceinline__ int64_t unit_cost(const CrossShape& p, int b) {
   return 2 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + p.unit_cost;
 }
 
+// Called by a whole warp: a lane takes a batch entry of 32.
 __device__ __forceinline__ void unit_range(const CrossShape& p, int cta, int n_cta, int& begin, int& end) {
+  const int lane = threadIdx.x & 31;
   const int64_t per_b = static_cast<int64_t>(p.kv_heads) * p.n_split * p.tiles;
   int64_t total = 0;
-  for (int b = 0; b < p.B; ++b) total += per_b * unit_cost(p, b);
+  for (int b = lane; b < p.B; b += 32) total += per_b * unit_cost(p, b);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
   const int64_t x0 = total * cta / n_cta, x1 = total * (cta + 1) / n_cta;
-  int64_t acc = 0;
   begin = end = p.n_units;
-  bool b0 = false, b1 = false;
-  for (int b = 0; b < p.B; ++b) {
-    const int64_t c = unit_cost(p, b), next = acc + per_b * c;
-    if (!b0 && x0 < next) {
-      begin = static_cast<int>(b * per_b + (x0 - acc + c - 1) / c);
-      b0 = true;
+  int64_t acc = 0;
+  for (int first = 0; first < p.B; first += 32) {
+    const int b = first + lane;
+    const int64_t c = b < p.B ? unit_cost(p, b) : 0;
+    int64_t next = per_b * c;  // (inclusive sums)
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t below = __shfl_up_sync(0xffffffffu, next, d);
+      if (lane >= d) next += below;
     }
-    if (!b1 && x1 < next) {
-      end = static_cast<int>(b * per_b + (x1 - acc + c - 1) / c);
-      b1 = true;
-    }
-    acc = next;
+    next += acc;
+    const int64_t at = next - per_b * c;
+    const unsigned m0 = __ballot_sync(0xffffffffu, at <= x0 && x0 < next);
+    const unsigned m1 = __ballot_sync(0xffffffffu, at <= x1 && x1 < next);
+    const int u0 = at <= x0 && x0 < next ? static_cast<int>(b * per_b + (x0 - at + c - 1) / c) : 0;
+    const int u1 = at <= x1 && x1 < next ? static_cast<int>(b * per_b + (x1 - at + c - 1) / c) : 0;
+    if (m0) begin = __shfl_sync(0xffffffffu, u0, __ffs(m0) - 1);
+    if (m1) end = __shfl_sync(0xffffffffu, u1, __ffs(m1) - 1);
+    acc = __shfl_sync(0xffffffffu, next, 31);
   }
 }
 
@@ -568,10 +578,14 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
     mbar_init(drain, 1);
     *abort = 0;
     fence_mbar_init();
+  }
+  if (warp == 0) {
     int b, e;
     unit_range(p, blockIdx.x / kCtas, gridDim.x / kCtas, b, e);
-    range[0] = b;
-    range[1] = e;
+    if (lane == 0) {
+      range[0] = b;
+      range[1] = e;
+    }
   }
   if (warp == kMmaWarp) {
     if constexpr (kPair) {
