@@ -52,6 +52,18 @@ def check(q, k, v, do, lens, scale=None, backward=True, what=""):
     return out, lse
 
 
+# more batch entries than a warp has lanes, most of them without keys, units cut between CTAs
+def many_lens(B, Lk):
+    return tuple((Lk, 0, 0, 1, 0, Lk // 2, 0, 130)[b % 8] if b not in (0, B - 1) else 0 for b in range(B))
+
+
+@pytest.mark.parametrize("B,h,hk,Lq,Lk", [(70, 2, 1, 3, 200), (45, 1, 1, 300, 260), (200, 1, 1, 1, 140)])
+def test_many_batch_entries(B, h, hk, Lq, Lk):
+    q, k, v, do = draw(19, B, h, hk, Lq, Lk)
+    check(q, k, v, do, many_lens(B, Lk))
+    check(q, k, v, do, (0,) * B)
+
+
 # (B, heads, kv_heads, Lq, Lk, lens): one key and one row, chunk and step borders of the keys
 # (16, 64, 128, 256), lengths of zero, shared kv heads, several tiles per CTA
 CASES = [

@@ -108,7 +108,7 @@ dsa_status_t cross_plan(const dsa_cross_t* p, CrossPlan* c, bool pack = true) {
   // more than one 128-row tile per head, and not in parts: a cluster of two CTAs per 256 rows
   c->pair = c->split_q == 1 && p->Lq > 128;
   c->kv_units = slices * c->chunks;
-  if (c->kv_units > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (c->kv_units > INT32_MAX - kPlanSms) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
@@ -536,9 +536,8 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   kp.dv_part = ws.dv_part;
   kp.scale = p->scale;
   kp.scale_log2 = p->scale * 1.4426950408889634f;
-  const dim3 kv_grid(static_cast<unsigned>(c.kv_units), 2, 8);
   if (p->Lq == 0) {  // no queries: dk = dv = 0
-    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(kp, 1);
+    dsa::cross_kv_combine<<<dim3(static_cast<unsigned>(c.kv_units), 2, 8), 256, 0, s>>>(kp, 0);
     return launch_status();
   }
 
@@ -585,7 +584,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     dsa::cross_kv_kernel<<<grid, dsa::crosskv::kThreads, dsa::crosskv::kSmemBytes, s>>>(tq, tdo, tk, tv, kp);
     st = launch_status();
     if (st != DSA_OK) return st;
-    dsa::cross_kv_combine<<<kv_grid, 256, 0, s>>>(kp, static_cast<int>(grid));
+    dsa::cross_kv_combine<<<dim3(static_cast<unsigned>(c.kv_units) + grid, 2, 8), 256, 0, s>>>(kp, static_cast<int>(grid));
     st = launch_status();
     if (st != DSA_OK) return st;
   }

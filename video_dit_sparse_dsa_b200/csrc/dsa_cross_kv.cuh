@@ -66,46 +66,74 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0), kIdescAcc = idesc_b
 
 __device__ __forceinline__ int kv_chunks(const CrossKvParams& p, int b) { return (crossf::kv_length(p, b) + 127) / 128; }
 
-// Units in all, and those of the batch entries before b (whole warp).
-__device__ __forceinline__ void count_units(const CrossKvParams& p, int b, int64_t& all, int64_t& before) {
-  all = before = 0;
-  for (int i = threadIdx.x & 31; i < p.B; i += 32) {
-    const int64_t n = static_cast<int64_t>(kv_chunks(p, i)) * p.kv_heads;
-    all += n;
-    if (i < b) before += n;
-  }
+// Units in all (whole warp).
+__device__ __forceinline__ int64_t count_units(const CrossKvParams& p) {
+  int64_t all = 0;
+  for (int i = threadIdx.x & 31; i < p.B; i += 32) all += static_cast<int64_t>(kv_chunks(p, i)) * p.kv_heads;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+  for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  return all;
 }
 
-// The k-th piece of the CTA's range [lo, hi) of the chunk sequence: its unit (kv head, batch
-// entry, 128-key chunk kt), first query chunk and number of chunks (0: past the range).
-struct Piece {
-  int b, kvh, kt, c0, n;
+// A unit: 128-key chunk kt of kv head kvh of batch entry b.
+struct KvUnit {
+  int b, kvh, kt;
 };
 
-__device__ __forceinline__ Piece piece(const CrossKvParams& p, int64_t lo, int64_t hi, int k) {
-  Piece x;
-  const int64_t v = lo / p.per_unit + k, start = k == 0 ? lo : v * p.per_unit;
-  x.b = x.kvh = x.kt = 0;
-  x.c0 = static_cast<int>(start - v * p.per_unit);
-  x.n = start < hi ? static_cast<int>(min((v + 1) * p.per_unit, hi) - start) : 0;
-  int64_t rem = v;
-  for (; x.n > 0 && x.b < p.B; ++x.b) {
-    const int c = kv_chunks(p, x.b);
-    const int64_t n = static_cast<int64_t>(c) * p.kv_heads;
-    if (rem < n) {
-      x.kvh = static_cast<int>(rem / c);
-      x.kt = static_cast<int>(rem % c);
+// The v-th unit (whole warp, v below their number; a lane takes a batch entry of 32).
+__device__ __forceinline__ KvUnit find_unit(const CrossKvParams& p, int64_t v) {
+  const int lane = threadIdx.x & 31;
+  KvUnit x = {0, 0, 0};
+  int64_t before = 0;
+  for (int first = 0; first < p.B; first += 32) {
+    const int c = first + lane < p.B ? kv_chunks(p, first + lane) : 0;
+    const int64_t own = static_cast<int64_t>(c) * p.kv_heads;
+    int64_t end = own;  // (inclusive sums)
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t below = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += below;
+    }
+    end += before;
+    const unsigned m = __ballot_sync(0xffffffffu, v < end);
+    if (m) {
+      const int at = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, c, at);
+      const int64_t rem = v - __shfl_sync(0xffffffffu, end - own, at);
+      x.b = first + at;
+      x.kvh = static_cast<int>(rem / n);
+      x.kt = static_cast<int>(rem % n);
       break;
     }
-    rem -= n;
+    before = __shfl_sync(0xffffffffu, end, 31);
   }
   return x;
 }
+
+// Walks the pieces of a CTA's range of the chunk sequence: unit, first query chunk, number of
+// chunks (0: past the range).
+struct Pieces : KvUnit {
+  int chunks;  // key chunks of the batch entry
+  int c0, n;
+  int64_t left;
+  __device__ __forceinline__ Pieces(const CrossKvParams& p, const KvUnit& first, int64_t lo, int64_t hi) : KvUnit(first) {
+    chunks = kv_chunks(p, b);
+    c0 = static_cast<int>(lo % max(p.per_unit, 1));
+    left = hi - lo;
+    n = static_cast<int>(min(static_cast<int64_t>(p.per_unit - c0), left));
+  }
+  __device__ __forceinline__ void next(const CrossKvParams& p) {
+    left -= n;
+    c0 = 0;
+    n = static_cast<int>(min(static_cast<int64_t>(p.per_unit), left));
+    if (n == 0 || ++kt < chunks) return;
+    kt = 0;
+    if (++kvh < p.kv_heads) return;
+    kvh = 0;
+    do {
+      chunks = kv_chunks(p, ++b);  // (units are left: an entry with keys follows)
+    } while (chunks == 0);
+  }
+};
 
 // A query chunk of a kv head: rows from `row` of head g of the group (pk > 1: pk heads from g).
 struct QChunk {
@@ -174,7 +202,9 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
   uint64_t* drain = s_full + 7;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
   volatile int* abort = reinterpret_cast<volatile int*>(s_full + 8) + 1;
-  static_assert(2 + 2 * kQ + 4 * kDo + 9 <= 256 / 8, "barriers must fit their 256 bytes");
+  int64_t* range = reinterpret_cast<int64_t*>(s_full + 9);        // [2] of the chunk sequence
+  KvUnit* first_unit = reinterpret_cast<KvUnit*>(s_full + 11);    // the one that it begins in
+  static_assert(2 + 2 * kQ + 4 * kDo + 13 <= 256 / 8, "barriers must fit their 256 bytes");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -205,6 +235,16 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
     *abort = 0;
     fence_mbar_init();
   }
+  if (warp == 0) {
+    const int64_t all = count_units(p) * p.per_unit;
+    const int64_t b = all * blockIdx.x / gridDim.x, e = all * (blockIdx.x + 1) / gridDim.x;
+    const KvUnit x = find_unit(p, b / max(p.per_unit, 1));
+    if (lane == 0) {
+      range[0] = b;
+      range[1] = e;
+      *first_unit = x;
+    }
+  }
   if (p.pk > 1) {
     // chunks of packed heads leave the rows from pk * Lq on unwritten, and the gradient products
     // read them against P = dS = 0: zeros, once
@@ -219,14 +259,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int64_t lo, hi;
-  {
-    int64_t all, before;
-    count_units(p, 0, all, before);
-    all *= p.per_unit;
-    lo = all * blockIdx.x / gridDim.x;
-    hi = all * (blockIdx.x + 1) / gridDim.x;
-  }
+  const int64_t lo = range[0], hi = range[1];
+  const KvUnit u0 = *first_unit;
 
   if (warp >= 8) {
     setmaxnreg_dec<kRegsAux>();
@@ -235,9 +269,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
       if (lane == 0) {
         int ld = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-          const Piece x = piece(p, lo, hi, k);
-          if (x.n == 0) break;
+        Pieces x(p, u0, lo, hi);
+        for (int k = 0; ok && x.n > 0; ++k, x.next(p)) {
           ok = mbar_wait(kv_free, (k & 1) ^ 1, abort, 200);
           if (!ok) break;
           mbar_arrive_expect_tx(kv_full, 2 * kTile);
@@ -263,9 +296,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
       if (lane == 0) {
         int ld = 0;
         bool ok = true;
-        for (int k = 0; ok; ++k) {
-          const Piece x = piece(p, lo, hi, k);
-          if (x.n == 0) break;
+        Pieces x(p, u0, lo, hi);
+        for (int k = 0; ok && x.n > 0; ++k, x.next(p)) {
           QChunk q;
           q.start(p, x.c0);
           for (int c = 0; c < x.n; ++c, ++ld, q.next(p)) {
@@ -283,9 +315,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
       // ------------------------------------------------------------------ -LSE log2 e and -D (whole warp)
       int ld = 0;
       bool ok = true;
-      for (int k = 0; ok; ++k) {
-        const Piece x = piece(p, lo, hi, k);
-        if (x.n == 0) break;
+      Pieces x(p, u0, lo, hi);
+      for (int k = 0; ok && x.n > 0; ++k, x.next(p)) {
         QChunk q;
         q.start(p, x.c0);
         for (int c = 0; c < x.n; ++c, ++ld, q.next(p)) {
@@ -325,9 +356,9 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
         mma_commit_warp(s_full);
         return true;
       };
-      for (int k = 0; ok; ++k) {
-        const int n = piece(p, lo, hi, k).n;
-        if (n == 0) break;
+      Pieces x(p, u0, lo, hi);
+      for (int k = 0; ok && x.n > 0; ++k, x.next(p)) {
+        const int n = x.n;
         ok = warp_wait(kv_full, k & 1, abort, 212) && issue_s(C);
         for (int c = 0; c < n && ok; ++c, ++C) {
           const int st = C % kDo;
@@ -342,12 +373,12 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
             mma_commit_warp(kv_free);
           if (ok && c == 0) ok = warp_wait(dkv_free, (k & 1) ^ 1, abort, 214);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (ok) ok = warp_wait(p_full + x, C & 1, abort, 215);
+          for (int i = 0; i < 2; ++i) {
+            if (ok) ok = warp_wait(p_full + i, C & 1, abort, 215);
             if (!ok) break;
             tc_fence_after();
-            issue_grad(tmem + kColDV, tmem + kColDP + 64 * x, desc_add(dOm, st * kTile + x * 8192), c > 0 || x > 0);
-            issue_grad(tmem + kColDK, tmem + kColDP + 64 * x + 16, desc_add(dQm, C % kQ * kTile + x * 8192), c > 0 || x > 0);
+            issue_grad(tmem + kColDV, tmem + kColDP + 64 * i, desc_add(dOm, st * kTile + i * 8192), c > 0 || i > 0);
+            issue_grad(tmem + kColDK, tmem + kColDP + 64 * i + 16, desc_add(dQm, C % kQ * kTile + i * 8192), c > 0 || i > 0);
           }
           if (!ok) break;
           mma_commit_warp(q_empty + C % kQ);
@@ -366,9 +397,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int C = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const Piece x = piece(p, lo, hi, k);
-      if (x.n == 0) break;
+    Pieces x(p, u0, lo, hi);
+    for (int k = 0; ok && x.n > 0; ++k, x.next(p)) {
       const int len = crossf::kv_length(p, x.b);
       const bool k_ok = 128 * x.kt + m < len, tail = 128 * x.kt + 128 > len;
       for (int c = 0; c < x.n; ++c, ++C) {
@@ -503,35 +533,46 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
   }
 }
 
-// dK and dV of the units that were cut between CTAs: scale * (for dK) the sum of the pieces' fp32
-// sums, in CTA order, as bf16; and zeros for the padding's rows that no unit covers.  A block takes
-// 16 rows (blockIdx.z) of one 128-key chunk of one kv head (blockIdx.x) of dk or dv (blockIdx.y);
-// n_cta: the key-major pass' grid.
+// What the key-major pass leaves: dK and dV of the units that were cut between its n_cta CTAs,
+// scale * (for dK) the sum of the pieces' fp32 sums, in CTA order, as bf16; and zeros for the
+// padding's rows that no unit covers (without queries: for every row).  A block takes 16 rows
+// (blockIdx.z) of dk or dv (blockIdx.y), of the unit that the end of CTA blockIdx.x's range cuts if
+// its first piece is there, or (blockIdx.x >= n_cta) of a 128-key chunk of a kv head.
 __global__ void __launch_bounds__(256) cross_kv_combine(CrossKvParams p, int n_cta) {
-  const int chunks = (p.Lk + 127) / 128, kt = blockIdx.x % chunks, bh = blockIdx.x / chunks, b = bh / p.kv_heads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, len = crossf::kv_length(p, b), kv_c = (len + 127) / 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = 16 * blockIdx.z + warp;  // this warp's rows: r and r + 8
   const bool is_dk = blockIdx.y == 0;
   const int64_t* s = is_dk ? p.dk_s : p.dv_s;
-  __nv_bfloat16* out = (is_dk ? p.dk : p.dv) + b * s[0] + (bh % p.kv_heads) * s[1];
-  int64_t all, before;
-  crosskv::count_units(p, b, all, before);
-  all *= p.per_unit;
-  int i0 = 0, i1 = -1;  // the CTAs that hold pieces of this unit
-  int64_t start = 0;
-  if (kt < kv_c && p.per_unit > 0) {
-    start = (before + static_cast<int64_t>(bh % p.kv_heads) * kv_c + kt) * p.per_unit;
-    i0 = static_cast<int>(((start + 1) * n_cta - 1) / all);
-    i1 = static_cast<int>(((start + p.per_unit) * n_cta - 1) / all);
+  __nv_bfloat16* out = is_dk ? p.dk : p.dv;
+  if (blockIdx.x >= static_cast<unsigned>(n_cta)) {
+    const int chunks = (p.Lk + 127) / 128, x = blockIdx.x - n_cta, kt = x % chunks, bh = x / chunks, b = bh / p.kv_heads;
+    // (a whole unit's CTA, or the other blocks, write its chunk: the padding in it too)
+    const int from = p.per_unit > 0 ? 128 * crosskv::kv_chunks(p, b) : 0;
+    out += b * s[0] + (bh % p.kv_heads) * s[1];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int l = 128 * kt + r + 8 * j;
+      if (l >= from && l < p.Lk) reinterpret_cast<uint2*>(out + l * s[2])[lane] = make_uint2(0u, 0u);
+    }
+    return;
   }
+  if (p.per_unit == 0) return;
+  const int64_t all = crosskv::count_units(p) * p.per_unit;
+  auto bound = [&](int i) -> int64_t { return all * i / n_cta; };
+  const int i0 = blockIdx.x;
+  const int64_t lo0 = bound(i0), cut_at = bound(i0 + 1);
+  if (lo0 >= cut_at || cut_at >= all || cut_at % p.per_unit == 0) return;  // no range, or it ends with a unit
+  const int64_t v = cut_at / p.per_unit, start = v * p.per_unit, end = start + p.per_unit;
+  if (lo0 > start) return;  // an earlier CTA holds the first piece
+  const crosskv::KvUnit u = crosskv::find_unit(p, v);
+  const int len = crossf::kv_length(p, u.b), l = 128 * u.kt + r;
+  out += u.b * s[0] + u.kvh * s[1];
   const float f = is_dk ? p.scale : 1.f;
   const float* part = is_dk ? p.dk_part : p.dv_part;
-  const int r = 16 * blockIdx.z + warp, l = 128 * kt + r;  // this warp's rows: l and l + 8
-  const bool cut = i0 != i1;  // (otherwise one CTA's own: its valid rows are written)
   float4 a[2];
   a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-  int64_t lo = i1 >= i0 ? all * i0 / n_cta : 0;
-  for (int i = i0; i <= i1 && cut; ++i) {
-    const int64_t hi = all * (i + 1) / n_cta;
+  int64_t lo = lo0;
+  for (int i = i0; i < n_cta && lo < end; ++i) {
+    const int64_t hi = bound(i + 1);
     if (lo < hi) {  // (a range is empty where there are fewer query chunks than CTAs)
       const float4* src =
           reinterpret_cast<const float4*>(part + (2 * static_cast<int64_t>(i) + (lo < start)) * 16384 + r * 128) + lane;
@@ -550,7 +591,7 @@ __global__ void __launch_bounds__(256) cross_kv_combine(CrossKvParams p, int n_c
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int lj = l + 8 * j;
-    if (lj >= p.Lk || (lj < len && !cut)) continue;
+    if (lj >= p.Lk) continue;
     reinterpret_cast<uint2*>(out + lj * s[2])[lane] =
         make_uint2(pack_bf16x2(a[j].x * f, a[j].y * f), pack_bf16x2(a[j].z * f, a[j].w * f));
   }
