@@ -434,7 +434,7 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   fp.n_split = p->Lk > 0 ? c.split_q : 0;
   fp.n_units = static_cast<int>(c.units * c.split_q);
   fp.scale_log2 = p->scale * 1.4426950408889634f;
-  fp.unit_cost = 1;
+  fp.unit_cost = 4;
   if (p->Lk > 0) {
     CUtensorMap tq, tk, tv;
     int mq[3], mk[3], mv[3];
@@ -456,7 +456,7 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
       fp.n_units = p->B * p->kv_heads * fp.tiles;
       // measured on a 512 + 203-key pair: units of four and of two chunks take times of 9 : 5.7
       // (with a cost of 1 the CTAs of the short entry ran 212 us, those of the long one 186)
-      fp.unit_cost = 3;
+      fp.unit_cost = 12;
       CUtensorMap to;
       int mo[3];
       if (!make_view_map(&to, out, p->B, p->heads, c.group, p->Lq, 32, 1, mo)) return DSA_ERR_CUDA;
@@ -520,7 +520,7 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
   shape.tiles = c.tiles;
   shape.n_split = c.split_q;
   shape.n_units = static_cast<int>(c.units * c.split_q);
-  shape.unit_cost = 1;  // (the dQ pass: the same pair's CTAs end within 3% of each other)
+  shape.unit_cost = 4;
 
   dsa::CrossKvParams kp;
   std::memset(&kp, 0, sizeof(kp));
@@ -616,6 +616,9 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
       return DSA_ERR_CUDA;
     dp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
     dp.n_units = p->B * p->kv_heads * dp.tiles;
+    // measured on the same pair of lengths: units of four and of two chunks take times of 14.2 : 7.0
+    // (with a cost of 4 the CTAs of the long entry ran 510 thousand clocks, those of the short one 441)
+    dp.unit_cost = 1;
     return launch_pairs<dsa::cross_dq_kernel<true>>(dsa::crossdq::kSmemBytes, dsa::crossdq::kThreads,
                                                     dsa::bdq::kRegsAtLaunch, dp.n_units, s, tq, tdo, tk64, tk, tv64, tdq, dp);
   }

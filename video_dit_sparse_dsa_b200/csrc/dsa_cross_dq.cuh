@@ -22,10 +22,11 @@
 // with a ring of its own and released by its own product.  (24 heads x 35840 rows over 512 and 203
 // keys, whole backward: 645 us, and 695 with this pass on single CTAs.)
 //
-// What bounds it: 302 us there, 3300 clocks per step.  A step takes in 48 KB of K and V per CTA
-// and, over four steps, 96 KB of Q, dO and dQ, 36 bytes per clock and SM or 9 TB/s over the chip,
-// and the MMA warp goes through seven waits of 200 clocks, which follow one another.  Measured and
-// not kept: rings of two entries with two Q tiles (430 us); one wait per step for all loads, behind
+// What bounds it: 302 us there, 3300 clocks per step.  Latency: the tensor pipe is active 41 to 52%
+// of the time, L2 at 14% of its rate; the MMA warp goes through seven waits of 200 clocks a step,
+// which follow one another, a unit's start and its dQ take 3000 to 3500 clocks of the elementwise
+// warps, and of the stalls of a warp a fifth are for instructions (long unrolled code, run once a
+// step).  Ring depth counts: two entries in place of three cost 40%.  Measured and not kept: rings of two entries with two Q tiles (430 us); one wait per step for all loads, behind
 // a warp that collects them (336); dQ stored from registers, four V entries in its place (350).
 //
 // Persistent and warp-specialised, 384 threads:

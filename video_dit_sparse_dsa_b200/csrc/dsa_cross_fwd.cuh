@@ -70,7 +70,7 @@ struct CrossShape {
   int tiles;              // units per kv head and part
   int n_split;            // parts of the keys
   int n_units;            // B * kv_heads * n_split * tiles
-  int unit_cost;          // a unit's fixed cost in half chunks
+  int unit_cost;          // a unit's fixed cost in eighths of a chunk, at least 1
 };
 
 struct CrossFwdParams : CrossShape {
@@ -124,9 +124,9 @@ __device__ __forceinline__ int chunks_per_part(const CrossShape& p, int chunks) 
 }
 
 // The CTA's units [begin, end): the sequence is cut at equal cost, a unit costing its chunks and a
-// constant for its own start and end, in half chunks: unit_cost (chosen by each kernel's launch).
+// constant for its own start and end, in eighths of a chunk: unit_cost (chosen by each kernel's launch).
 __device__ __forceinline__ int64_t unit_cost(const CrossShape& p, int b) {
-  return 2 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + p.unit_cost;
+  return 8 * static_cast<int64_t>(chunks_per_part(p, (kv_length(p, b) + 127) / 128)) + p.unit_cost;
 }
 
 // Called by a whole warp: a lane takes a batch entry of 32.
