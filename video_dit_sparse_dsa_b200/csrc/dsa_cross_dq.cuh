@@ -20,7 +20,7 @@
 // = 256 tcgen05.mma.cta_group::2 over 256 rows.  A CTA holds half of every operand, and K twice:
 // its half of a step's keys for the scores and its half of the channels for the dQ product, each
 // with a ring of its own and released by its own product.  (24 heads x 35840 rows over 512 and 203
-// keys, whole backward: 645 us, and 695 with this pass on single CTAs.)
+// keys, whole backward: 650 us, and 695 with this pass on single CTAs.)
 //
 // What bounds it: 302 us there, 3300 clocks per step.  Latency: the tensor pipe is active 41 to 52%
 // of the time, L2 at 14% of its rate; the MMA warp goes through seven waits of 200 clocks a step,

@@ -16,7 +16,7 @@
 // elementwise work is handed over in two halves of 64 queries:
 //   tensor pipe   dP(c)      S(c+1)       grads A(c)  grads B(c)   dP(c+1) ...
 //   elementwise   (exp of c) dS A, dS B(c)      exp of c+1 ...
-// 24 heads x 35840 rows over 512 and 203 keys: 273 us, 3700 clocks per chunk.  What bounds it is
+// 24 heads x 35840 rows over 512 and 203 keys: 267 us, 3700 clocks per chunk.  What bounds it is
 // that cycle: dP(c), dS (750 clocks), the four gradient products and dP(c + 1) follow one another,
 // with 1250 clocks of exponentials and some 200 per hand-over beside them; running a quarter or
 // three eighths of the exponentials on the FMA pipe changed nothing.  A second dP buffer would
@@ -71,10 +71,10 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0, 0), kIdescAcc = idesc_b
 
 __device__ __forceinline__ int kv_chunks(const CrossKvParams& p, int b) { return (crossf::kv_length(p, b) + 127) / 128; }
 
-// Units in all (whole warp).
-__device__ __forceinline__ int64_t count_units(const CrossKvParams& p) {
-  int64_t all = 0;
-  for (int i = threadIdx.x & 31; i < p.B; i += 32) all += static_cast<int64_t>(kv_chunks(p, i)) * p.kv_heads;
+// Units in all (whole warp); their number fits 31 bits.
+__device__ __forceinline__ int count_units(const CrossKvParams& p) {
+  int all = 0;
+  for (int i = threadIdx.x & 31; i < p.B; i += 32) all += kv_chunks(p, i) * p.kv_heads;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
   return all;
@@ -86,27 +86,28 @@ struct KvUnit {
 };
 
 // The v-th unit (whole warp, v below their number; a lane takes a batch entry of 32).
-__device__ __forceinline__ KvUnit find_unit(const CrossKvParams& p, int64_t v) {
+__device__ __forceinline__ KvUnit find_unit(const CrossKvParams& p, int v) {
   const int lane = threadIdx.x & 31;
   KvUnit x = {0, 0, 0};
-  int64_t before = 0;
+  int before = 0;
+#pragma unroll 1
   for (int first = 0; first < p.B; first += 32) {
     const int c = first + lane < p.B ? kv_chunks(p, first + lane) : 0;
-    const int64_t own = static_cast<int64_t>(c) * p.kv_heads;
-    int64_t end = own;  // (inclusive sums)
+    const int own = c * p.kv_heads;
+    int end = own;  // (inclusive sums)
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t below = __shfl_up_sync(0xffffffffu, end, d);
+      const int below = __shfl_up_sync(0xffffffffu, end, d);
       if (lane >= d) end += below;
     }
     end += before;
     const unsigned m = __ballot_sync(0xffffffffu, v < end);
     if (m) {
       const int at = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, c, at);
-      const int64_t rem = v - __shfl_sync(0xffffffffu, end - own, at);
+      const int rem = v - __shfl_sync(0xffffffffu, end - own, at);
       x.b = first + at;
-      x.kvh = static_cast<int>(rem / n);
-      x.kt = static_cast<int>(rem % n);
+      x.kvh = rem / n;
+      x.kt = rem - x.kvh * n;
       break;
     }
     before = __shfl_sync(0xffffffffu, end, 31);
@@ -241,9 +242,9 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    const int64_t all = count_units(p) * p.per_unit;
+    const int64_t all = static_cast<int64_t>(count_units(p)) * p.per_unit;
     const int64_t b = all * blockIdx.x / gridDim.x, e = all * (blockIdx.x + 1) / gridDim.x;
-    const KvUnit x = find_unit(p, b / max(p.per_unit, 1));
+    const KvUnit x = find_unit(p, static_cast<int>(b / max(p.per_unit, 1)));
     if (lane == 0) {
       range[0] = b;
       range[1] = e;
@@ -561,13 +562,17 @@ __global__ void __launch_bounds__(256) cross_kv_combine(CrossKvParams p, int n_c
     return;
   }
   if (p.per_unit == 0) return;
-  const int64_t all = crosskv::count_units(p) * p.per_unit;
-  auto bound = [&](int i) -> int64_t { return all * i / n_cta; };
+  const int64_t all = static_cast<int64_t>(crosskv::count_units(p)) * p.per_unit;
+  // all * i / n_cta, with one wide division for all of them
+  const int64_t per = all / n_cta;
+  const int over = static_cast<int>(all - per * n_cta);
+  auto bound = [&](int i) -> int64_t { return per * i + over * i / n_cta; };
   const int i0 = blockIdx.x;
   const int64_t lo0 = bound(i0), cut_at = bound(i0 + 1);
-  if (lo0 >= cut_at || cut_at >= all || cut_at % p.per_unit == 0) return;  // no range, or it ends with a unit
-  const int64_t v = cut_at / p.per_unit, start = v * p.per_unit, end = start + p.per_unit;
-  if (lo0 > start) return;  // an earlier CTA holds the first piece
+  if (lo0 >= cut_at || cut_at >= all) return;  // no range, or the last
+  const int v = static_cast<int>(cut_at / p.per_unit);
+  const int64_t start = static_cast<int64_t>(v) * p.per_unit, end = start + p.per_unit;
+  if (cut_at == start || lo0 > start) return;  // no unit is cut here, or an earlier CTA holds its first piece
   const crosskv::KvUnit u = crosskv::find_unit(p, v);
   const int len = crossf::kv_length(p, u.b), l = 128 * u.kt + r;
   out += u.b * s[0] + u.kvh * s[1];
@@ -576,6 +581,7 @@ __global__ void __launch_bounds__(256) cross_kv_combine(CrossKvParams p, int n_c
   float4 a[2];
   a[0] = a[1] = make_float4(0.f, 0.f, 0.f, 0.f);
   int64_t lo = lo0;
+#pragma unroll 1
   for (int i = i0; i < n_cta && lo < end; ++i) {
     const int64_t hi = bound(i + 1);
     if (lo < hi) {  // (a range is empty where there are fewer query chunks than CTAs)
