@@ -455,7 +455,7 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
       fp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
       fp.n_units = p->B * p->kv_heads * fp.tiles;
       // measured on a 512 + 203-key pair: units of four and of two chunks take times of 9 : 5.7
-      // (with a cost of 1 the CTAs of the short entry ran 212 us, those of the long one 186)
+      // (with a cost of 4 the CTAs of the short entry ran 212 us, those of the long one 186)
       fp.unit_cost = 12;
       CUtensorMap to;
       int mo[3];
