@@ -144,3 +144,45 @@ def test_block_graph_replays_with_new_inputs():
         for n, t in expect.items():
             if n not in ("ck", "cv"):
                 assert torch.equal(s[n], t), n
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^24 elements apart in one buffer of 2.5e9 elements: the last rows lie past 2^31."""
+    L, step = 150, 1 << 24
+    buf = torch.zeros((L - 1) * step + 4096, dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(34)
+    at = iter(range(0, 4096, 128))
+
+    def view(fill=True):
+        t = buf.as_strided((1, 1, L, 128), (128, 128, step, 1), next(at))
+        if fill:
+            t.copy_(torch.randn(1, 1, L, 128, generator=g, device="cuda"))
+        return t
+
+    q, k, v, do = (view() for _ in range(4))
+    out, dq, dk, dv = (view(False) for _ in range(4))
+    _, lse = dsa.forward_cross(q, k, v, out=out)
+    dsa.backward_cross(q, k, v, out, lse, do, dq=dq, dk=dk, dv=dv)
+    ok()
+    ro, rl, tol = ref.cross(q, k, v, None)
+    ref.close(out, ro, tol, "out")
+    ref.close(lse, rl, ref.LSE_TOL, "lse")
+    rg, rt = ref.cross_bwd(q, k, v, out, lse, do, None)
+    for name, a, want, t in zip(("dq", "dk", "dv"), (dq, dk, dv), rg, rt):
+        ref.close(a, want, t, name)
+    grid = (6, 5, 5)
+    table = dsa.rope_table(grid, AXES, device="cuda")
+    y = view(False)
+    as_grid = lambda t: t.as_strided((1, 1, *grid, 128), (128, 128, 25 * step, 5 * step, step, 1), t.storage_offset())  # noqa: E731
+    dsa.rope(as_grid(q), None, table, AXES, q_out=as_grid(y))
+    ok()
+    want, tol = ref.rope(as_grid(q), grid, AXES, table, True, False)
+    ref.close(as_grid(y), want, tol + ref.U[BF] * want.abs(), "rope")
+    x = q[0, 0]
+    y, _ = dsa.rms_norm(x, None, EPS)
+    dx, _ = dsa.rms_norm_backward(x, None, do[0, 0], None, EPS)
+    ok()
+    ry, _ = ref.norm(x, None, None, EPS)
+    ref.close(y, ry, (ref.U[BF] + ref.NORM_ERR) * ry.abs(), "norm")
+    rx, _, tx, _ = ref.norm_bwd(x, None, do[0, 0], None, EPS)
+    ref.close(dx, rx, tx + ref.U[BF] * rx.abs(), "norm dx")
