@@ -289,7 +289,9 @@ typedef struct {
  * to [0, Lk] (kv_len: device int32 [B]; NULL: Lk for every entry):
  *   O_n = sum_{m < len_b} softmax_m(scale <q_n, k_m>) v_m,  LSE_n = ln sum_{m < len_b} exp(scale <q_n, k_m>).
  * Rows len_b and on of k and v are padding: whatever they hold (NaN and infinities included)
- * reaches no result.  len_b = 0 gives O = 0 and LSE = -inf.  Lq = 0 and Lk = 0 are valid. */
+ * reaches no result.  len_b = 0 gives O = 0 and LSE = -inf.  Lq = 0 and Lk = 0 are valid.
+ * Scores of valid keys that are not finite give what the formulas give: -inf the weight 0 (all of a
+ * row: O = NaN, LSE = -inf); +inf O = NaN, LSE = +inf; NaN O = NaN, LSE = NaN (+inf beside a +inf). */
 typedef struct {
   int32_t B, heads, kv_heads, d; /* d = 128 */
   int32_t Lq, Lk;

@@ -262,13 +262,16 @@ struct Cursor {
 };
 
 // 2^x for a pair on the FMA pipe: as exp2_poly2, with a quartic for 2^f (minimax fit on
-// [-0.5, 0.5], relative error 2.6e-6), because the row sums also give the fp32 LSE.
+// [-0.5, 0.5], relative error 2.6e-6), because the row sums also give the fp32 LSE, and a NaN
+// argument kept: the clamp keeps it, and 2^n comes in as a factor (added to the exponent field it
+// would make a number of it).  Times as with exp2_poly2's clamp and addition; a max over the scores
+// that keeps NaN took 1 to 2% more.
 __device__ __forceinline__ void exp2_quartic2(float x0, float x1, float& y0, float& y1) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 0.9999992847442627f, c1 = 0.6931217908859253f, c2 = 0.240247443318367f,
                   c3 = 0.05591785907745361f, c4 = 0.009570101276040077f;
-  x0 = fmaxf(x0, -126.f);
-  x1 = fmaxf(x1, -126.f);
+  x0 = max_nan(x0, -126.f);
+  x1 = max_nan(x1, -126.f);
   float t0, t1, n0, n1, f0, f1, q0, q1;
   fadd2(t0, t1, x0, x1, kRound, kRound);
   fadd2(n0, n1, t0, t1, -kRound, -kRound);
@@ -277,8 +280,8 @@ __device__ __forceinline__ void exp2_quartic2(float x0, float x1, float& y0, flo
   ffma2(q0, q1, q0, q1, f0, f1, c2, c2);
   ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
   ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
-  y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+  constexpr int kOne = 0x3f800000;
+  fmul2(y0, y1, q0, q1, __int_as_float(kOne + (__float_as_int(t0) << 23)), __int_as_float(kOne + (__float_as_int(t1) << 23)));
 }
 
 // An arrival on the MMA warp's barrier: this CTA's, or the even CTA's of the pair (whose address
@@ -341,8 +344,14 @@ __device__ __forceinline__ void exp_16(const uint32_t* s, float scale_log2, floa
 
 // A row's running softmax: the reference max, the row sum against it, and the factor that the old
 // O and l take where the reference moved in the last step.
+//
+// Scores that are not finite: NaN reaches l and O through its exponential; +inf becomes the
+// reference, and against it its own exponential is NaN; -inf has the weight 0 against the lowest
+// finite value, where the reference starts, so a row that ends there has no weight at all.
+constexpr float kLowest = -3.402823466e38f;
 struct RowState {
-  float m_used, l, alpha;
+  static constexpr float kNan = __builtin_nanf("");
+  float m_used = kLowest, l = 0.f, alpha = 1.f;
   // Agrees with the partner thread on the row max, mx being this thread's; true: it moved.
   __device__ __forceinline__ bool update(bool ok, float mx, float scale_log2, float* xbuf, int& xe, int i, int r, int bar_id) {
     mx = fmaxf(mx, fwd::pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
@@ -356,6 +365,12 @@ struct RowState {
     }
     l *= alpha;
     return need;
+  }
+  // 1 / l and LSE of the row, l being the sum of both threads'.
+  __device__ __forceinline__ float inverse(float l_all) const { return m_used == kLowest ? kNan : 1.f / l_all; }
+  __device__ __forceinline__ float lse(float l_all) const {
+    if (m_used == kLowest) return l_all == l_all ? -INFINITY : l_all;  // (every score NaN)
+    return m_used == INFINITY ? INFINITY : (m_used + __log2f(l_all)) * 0.69314718055994531f;
   }
 };
 
@@ -887,7 +902,7 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
         }
         continue;
       }
-      RowState st = {-INFINITY, 0.f, 1.f};
+      RowState st;
       // a warp without query rows (few rows, the last tile of a head) does no softmax: what its
       // rows of P and O hold reaches no other row (one token over 115201 + 70007 keys: 119 us
       // with all warps' exponentials in the way)
@@ -929,8 +944,8 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       const float l_all = act ? st.l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, st.l) : 1.f;
       px = c.x;
       px.row += 128 * rank;
-      p_inv = 1.f / l_all;
-      p_lse = (st.m_used + __log2f(l_all)) * 0.69314718055994531f;
+      p_inv = st.inverse(l_all);
+      p_lse = st.lse(l_all);
       pending = true;
     }
     if (ok && pending) write_out();
@@ -958,8 +973,9 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
 
 // Joins the n_part partial attentions of each row (fp32 O_j over disjoint keys, with LSE_j):
 // L = ln sum_j e^LSE_j, O = sum_j e^(LSE_j - L) O_j, in part order.  A part with LSE = -inf has
-// no keys and its O is not read.  A block takes one row: 8 warps take the parts in turn, a lane
-// four channels, and the warps' sums are added in warp order.
+// no keys, or none of any weight, and its O is not read; if all are so, O is 0 without keys and NaN
+// (0 / 0) with them.  A block takes one row: 8 warps take the parts in turn, a lane four channels,
+// and the warps' sums are added in warp order.
 __global__ void __launch_bounds__(256) cross_merge_kernel(CrossFwdParams p) {
   __shared__ float4 acc[8][32];
   __shared__ float wsum[8], wmax[8];
@@ -976,13 +992,13 @@ __global__ void __launch_bounds__(256) cross_merge_kernel(CrossFwdParams p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float v = __shfl_xor_sync(0xffffffffu, m, o);
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(v));
+    m = max_nan(m, v);
   }
   if (lane == 0) wmax[warp] = m;
   __syncthreads();
   m = wmax[0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(wmax[w]));
+  for (int w = 1; w < 8; ++w) m = max_nan(m, wmax[w]);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   float s = 0.f;
   if (m != -INFINITY) {
@@ -1013,12 +1029,12 @@ __global__ void __launch_bounds__(256) cross_merge_kernel(CrossFwdParams p) {
     a.z += acc[w][lane].z;
     a.w += acc[w][lane].w;
   }
-  const bool none = m == -INFINITY;
-  const float inv = none ? 0.f : 1.f / s;
   const int q = static_cast<int>(row % p.Lq), h = static_cast<int>(row / p.Lq % p.heads), b = static_cast<int>(row / p.Lq / p.heads);
+  const bool none = m == -INFINITY && crossf::kv_length(p, b) == 0;
+  const float inv = none ? 0.f : 1.f / s;
   reinterpret_cast<uint2*>(p.out + b * p.ob + h * p.oh + q * p.ol)[lane] =
       make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-  if (lane == 0) p.lse[row] = none ? -INFINITY : m + __logf(s);
+  if (lane == 0) p.lse[row] = fabsf(m) < INFINITY ? m + __logf(s) : m;
 }
 
 }  // namespace dsa

@@ -158,13 +158,6 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* row, int c, int C, const fl
   }
 }
 
-// max that keeps NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Sum over the lanes of a row within a warp (16 or 32).
 __device__ __forceinline__ float lane_sum(float s, int tpr) {
   if (tpr > 16) s += __shfl_xor_sync(0xffffffffu, s, 16);
