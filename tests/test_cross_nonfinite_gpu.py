@@ -25,16 +25,17 @@ def draw(seed, B, h, hk, Lq, Lk):
     return [torch.randn(B, n, L, 128, generator=g, device=DEV).to(BF) for n, L in ((h, Lq), (hk, Lk), (hk, Lk), (h, Lq))]
 
 
-def check(q, k, v, do=None, what=""):
+def check(q, k, v, do=None, what="", grads=("dq", "dk", "dv")):
     out, lse = dsa.forward_cross(q, k, v)
     ro, rl, tol = ref.cross(q, k, v, None)
     ref.close(lse, rl, ref.LSE_TOL, f"lse {what}")
     ref.close(out, ro, tol, f"out {what}")
     if do is not None:
-        grads = dsa.backward_cross(q, k, v, out, lse, do)
+        got = dsa.backward_cross(q, k, v, out, lse, do)
         rg, rt = ref.cross_bwd(q, k, v, out, lse, do, None)
-        for name, a, b, t in zip(("dq", "dk", "dv"), grads, rg, rt):
-            ref.close(a, b, t, f"{name} {what}")
+        for name, a, b, t in zip(("dq", "dk", "dv"), got, rg, rt):
+            if name in grads:
+                ref.close(a, b, t, f"{name} {what}")
     assert dsa.device_status()[0] == 0
     return out, lse
 
@@ -82,3 +83,30 @@ def test_whole_steps_of_minus_infinity(form):
         lo, hi = ((0, Lk), (0, min(256, Lk - 1)), (Lk // 2, Lk), (1, Lk))[b % 4]
         k[b, :, lo:hi, 9] = -math.inf
     check(q, k, v)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "x".join(str(x) for x in f[:4]))
+def test_dq_one_key(form, bad):
+    """A weight of 0 against an infinite key is NaN: dS of that key is 0, not a small number."""
+    h, hk, Lq, Lk, first = form
+    q, k, v, do = draw(Lk + 3, 16, h, hk, Lq, Lk)
+    for b in range(16):
+        k[b, hk - 1, first + b, 7 * b] = bad
+        if bad == -math.inf:
+            q[b, :, :, 7 * b] = q[b, :, :, 7 * b].abs() + 0.25  # scores of -inf only
+    check(q, k, v, do, what=f"{bad}", grads=("dq",))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "x".join(str(x) for x in f[:4]))
+def test_backward_one_row(form, bad):
+    """A row of dout, or a value, that is not finite."""
+    h, hk, Lq, Lk, first = form
+    q, k, v, do = draw(Lk + 4, 16, h, hk, Lq, Lk)
+    for b in range(16):
+        if b % 2:
+            v[b, hk - 1, first + b, 5 * b] = bad
+        else:
+            do[b, h - 1, (7 * b) % Lq, 5 * b] = bad
+    check(q, k, v, do, what=f"{bad}")

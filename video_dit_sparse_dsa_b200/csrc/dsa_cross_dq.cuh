@@ -3,9 +3,11 @@
 //   P_nm = exp(scale q_n.k_m - LSE_n),  dS_nm = P_nm (dO_n.v_m - D_n),  dQ_n = scale sum_m dS_nm k_m.
 //
 // Per 128 keys the tensor cores form S = Q K^T and dP = dO V^T again, the elementwise warps dS, and
-// dQ += dS K accumulates in TMEM: 1536 clocks of products, 768 of exponentials (a quarter of them
-// run on the FMA pipe).  A window holds thousands of keys, a prompt one to four steps' worth, so what
-// counts here is that nothing drains between units:
+// dQ += dS K accumulates in TMEM: 1536 clocks of products, 1024 of exponentials (all on the MUFU
+// unit: with a quarter of them on the FMA pipe the whole backward took 722 in place of 714 us for the
+// 480p pair below, and a score of -inf got a small weight where 0 is meant).  A window holds
+// thousands of keys, a prompt one to four steps' worth, so what counts here is that nothing drains
+// between units:
 //   * three regions of TMEM columns rotate: S of step G + 1 goes where dS of step G - 1 was, dP of
 //     step G + 1 where S of step G was, so both are ready when the elementwise warps end step G
 //     (with Q and dO as TMEM operands there was room for one of each, and dP waited for dS);
@@ -79,8 +81,6 @@ constexpr uint32_t kOffBar = 7 * kTile;
 constexpr uint32_t kSmemUsed = kOffBar + 320;
 constexpr uint32_t kSmemBytes = 227 * 1024;
 static_assert(kSmemUsed <= kSmemBytes, "shared memory layout too large");
-// column pairs (bit e of the 8 pairs of every 16 columns) whose 2^x runs on the FMA pipe
-constexpr uint32_t kPolyMask = 0x22u;
 
 // Regions of 128 TMEM columns rotate: S of step G at region(G), dP (then dS) at the one after it.
 __device__ __forceinline__ int next_region(int r) { return r == 0 ? 2 : r - 1; }  // S of the next step
@@ -517,12 +517,8 @@ __global__ void __launch_bounds__(crossdq::kThreads, 1)
             float x0, x1;
             ffma2(x0, x1, __uint_as_float(s[e]), __uint_as_float(s[e + 1]), p.scale_log2, p.scale_log2, neg_lse2,
                   neg_lse2);
-            if ((kPolyMask >> (e / 2 & 7)) & 1u) {
-              exp2_poly2(x0, x1, pf[e], pf[e + 1]);
-            } else {
-              pf[e] = ex2_approx(x0);
-              pf[e + 1] = ex2_approx(x1);
-            }
+            pf[e] = ex2_approx(x0);
+            pf[e + 1] = ex2_approx(x1);
           }
         } else if (lane == 0) {
           arrive<kPair>(lead_bar<kPair>(s_read + e2));
