@@ -110,3 +110,16 @@ def test_backward_one_row(form, bad):
         else:
             do[b, h - 1, (7 * b) % Lq, 5 * b] = bad
     check(q, k, v, do, what=f"{bad}")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("form", FORMS, ids=lambda f: "x".join(str(x) for x in f[:4]))
+def test_dk_dv_one_key(form, bad):
+    """A tile's missing rows (zeros, whose score with an infinite key is NaN) add nothing."""
+    h, hk, Lq, Lk, first = form
+    q, k, v, do = draw(Lk + 5, 16, h, hk, Lq, Lk)
+    for b in range(16):
+        k[b, hk - 1, first + b, 7 * b] = bad
+        if bad == -math.inf:
+            q[b, :, :, 7 * b] = q[b, :, :, 7 * b].abs() + 0.25  # scores of -inf only
+    check(q, k, v, do, what=f"{bad}", grads=("dk", "dv"))

@@ -27,8 +27,9 @@
 // Persistent and warp-specialised, one CTA per SM, 384 threads:
 //   warp 8      TMA producer of K and V of a unit, and Q of its chunks (3 entries)
 //   warp 10     TMA producer of dO (2 entries)
-//   warp 11     -LSE log2 e and -D of a chunk's rows into shared memory (2 entries; rows that do
-//               not exist get -inf, so their P and dS are 0)
+//   warp 11     -LSE log2 e and -D of a chunk's rows into shared memory (2 entries), and how many
+//               of its rows exist (the others' P and dS are set to 0: against an infinite key the
+//               score of a row of zeros is NaN)
 //   warp 9      MMA issuer
 //   warps 0-7   elementwise, two threads per key row: thread h takes queries [32h, 32h + 32) of
 //               either half; at the end of a piece warps 0-3 write dV and warps 4-7 dK
@@ -144,6 +145,10 @@ struct Pieces : KvUnit {
 // A query chunk of a kv head: rows from `row` of head g of the group (pk > 1: pk heads from g).
 struct QChunk {
   int g, row;
+  // Rows that exist: the first of the 128.
+  __device__ __forceinline__ int rows(const CrossKvParams& p) const {
+    return p.pk > 1 ? min(p.pk, p.group - g) * p.Lq : min(p.Lq - row, 128);
+  }
   __device__ __forceinline__ void start(const CrossKvParams& p, int c) {
     if (p.pk > 1) {
       g = c * p.pk;
@@ -210,7 +215,8 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
   volatile int* abort = reinterpret_cast<volatile int*>(s_full + 8) + 1;
   int64_t* range = reinterpret_cast<int64_t*>(s_full + 9);        // [2] of the chunk sequence
   KvUnit* first_unit = reinterpret_cast<KvUnit*>(s_full + 11);    // the one that it begins in
-  static_assert(2 + 2 * kQ + 4 * kDo + 13 <= 256 / 8, "barriers must fit their 256 bytes");
+  int* n_rows = reinterpret_cast<int*>(s_full + 13);              // [kDo] rows of a chunk (with -LSE and -D)
+  static_assert(2 + 2 * kQ + 4 * kDo + 13 + (kDo + 1) / 2 <= 256 / 8, "barriers must fit their 256 bytes");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -343,6 +349,7 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
             v[32 * e + lane] = nl[e];
             v[128 + 32 * e + lane] = nd[e];
           }
+          if (lane == 0) n_rows[st] = q.rows(p);
           __syncwarp();
           if (lane == 0) mbar_arrive(vec_full + st);
         }
@@ -414,6 +421,7 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
         if (ok) ok = warp_wait(s_full, C & 1, abort, 221);
         if (!ok) break;
         tc_fence_after();
+        const int nq = n_rows[st];
         float pf[64];  // P^T of queries [32h, 32h + 32) and [64 + 32h, 96 + 32h)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -465,6 +473,15 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
           if (tail && !k_ok) {  // a padding key's P and dP may be anything: both are zero
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = ds[e] = 0u;
+          }
+          if (nq < 128) {  // and a missing row's
+            const int left = nq - 64 * half - 32 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t keep = 2 * e + 1 < left ? 0xffffffffu : 2 * e < left ? 0xffffu : 0u;
+              pk[e] &= keep;
+              ds[e] &= keep;
+            }
           }
           __syncwarp();
           tmem_st16(tD, pk);  // over this thread's own dP columns
