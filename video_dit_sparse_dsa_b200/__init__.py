@@ -20,7 +20,9 @@ encoder's states), ``rope_table`` / ``rope`` (rotary positions over the token gr
 ``rms_norm`` / ``rms_norm_fp8`` / ``rms_norm_backward`` (root-mean-square norm with the
 residual's addition).  These take strided tensors (views of a projection), run on the device
 of their first argument whichever device is current, and on ``stream`` (default: that device's
-current stream).
+current stream).  A call on another stream than the current one is ordered after what is on that
+stream, as its kernels would be: the caller orders it after the work that makes its inputs, and
+what reads its results after it.
 """
 from __future__ import annotations
 
@@ -553,25 +555,29 @@ def _dtype_of(t: torch.Tensor, name: str) -> int:
 
 
 class _On:
-    """Runs a call on a tensor's device and on ``stream`` (default: that device's current
-    stream).  Scratch taken here is tied to that stream, so its memory is not reused while the
-    call's kernels run.  (The raw stream and device lookups: a Stream object and a device guard
-    cost a small call more host time than its kernel takes.)"""
-    __slots__ = ("device", "index", "stream", "guard", "ptr", "other")
+    """Runs a call on a device and on ``stream`` (default: that device's current stream).  What the
+    call allocates comes from that stream's memory: a block of another stream's (the current
+    one's) may still be in use by work queued there, which nothing orders before this call.
+    (The raw stream and device lookups: a Stream object and a device guard cost a small call more
+    host time than its kernel takes.)"""
+    __slots__ = ("device", "index", "guard", "ptr", "side")
 
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
+    def __init__(self, device: torch.device, stream):
+        if device.type != "cuda":
             raise ValueError("tensors must be CUDA tensors")
-        self.device, self.index, self.stream = t.device, t.get_device(), stream
+        self.device, self.index = device, device.index
+        own = torch._C._cuda_getCurrentRawStream(self.index)
+        self.ptr = own if stream is None else _stream(stream)
+        self.side = None  # the call's stream, where it is not the current one
+        if self.ptr != own:
+            self.side = (torch.cuda.ExternalStream(self.ptr, device=device) if self.ptr else
+                         torch.cuda.default_stream(device))
 
     def __enter__(self):
         self.guard = None
         if torch._C._cuda_getDevice() != self.index:
             self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
-        own = torch._C._cuda_getCurrentRawStream(self.index)
-        self.ptr = own if self.stream is None else _stream(self.stream)
-        self.other = self.ptr != own
         return self
 
     def __exit__(self, *exc):
@@ -579,15 +585,26 @@ class _On:
             self.guard.__exit__(*exc)
 
     def scratch(self, n_bytes: int):
-        if n_bytes == 0:
-            return None
-        return self.keep(torch.empty(n_bytes, dtype=torch.uint8, device=self.device))
+        """Memory of the call's own (freed after it on the host, so reused on its stream alone)."""
+        return self._make(torch.empty, n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
 
-    def keep(self, t: torch.Tensor) -> torch.Tensor:
-        """A tensor allocated by the call on the current stream, used on ``stream``."""
-        if self.other:
-            t.record_stream(torch.cuda.ExternalStream(self.ptr, device=self.device) if self.ptr else
-                            torch.cuda.default_stream(self.device))
+    def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        return self._result(torch.empty, shape, dtype=dtype, device=self.device)
+
+    def empty_like(self, t: torch.Tensor) -> torch.Tensor:
+        return self._result(torch.empty_like, t)
+
+    def _make(self, f, *args, **kw) -> torch.Tensor:
+        if self.side is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(self.side):
+            return f(*args, **kw)
+
+    def _result(self, f, *args, **kw) -> torch.Tensor:
+        """A tensor that the caller gets, and may use and drop on its own current stream."""
+        t = self._make(f, *args, **kw)
+        if self.side is not None:
+            t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
 
@@ -637,7 +654,7 @@ def _cross(q, k, v, kv_len, scale) -> Cross:
 def _out_like(t: Optional[torch.Tensor], name: str, ref: torch.Tensor, on: _On) -> torch.Tensor:
     """`t`, or a new tensor of ref's shape and dimension order."""
     if t is None:
-        return on.keep(torch.empty_like(ref))
+        return on.empty_like(ref)
     _like(t, name, ref, ref.shape, ref.dtype)
     return t
 
@@ -655,10 +672,10 @@ def forward_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: Opt
     result; 0 gives out = 0 and lse = -inf).  Returns (out, lse), out in q's dimension order."""
     lib = load_library()
     p = _cross(q, k, v, kv_len, scale)
-    with _On(q, stream) as on:
+    with _On(q.device, stream) as on:
         out = _out_like(out, "out", q, on)
         if lse is None:
-            lse = on.keep(torch.empty(q.shape[:3], dtype=torch.float32, device=q.device))
+            lse = on.empty(q.shape[:3], torch.float32)
         _like(lse, "lse", q, q.shape[:3], torch.float32)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
@@ -680,7 +697,7 @@ def backward_cross(q, k, v, out, lse, dout, kv_len: Optional[torch.Tensor] = Non
     _like(lse, "lse", q, q.shape[:3], torch.float32)
     if not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    with _On(q, stream) as on:
+    with _On(q.device, stream) as on:
         dq, dk, dv = _out_like(dq, "dq", q, on), _out_like(dk, "dk", k, on), _out_like(dv, "dv", v, on)
         ws, n_ws = _ws(ws, cross_workspace_size(p, backward=True), on, q)
         _check(lib.dsa_bwd_cross(p, _rows_view(q, "q"), _rows_view(k, "k"), _rows_view(v, "v"), _rows_view(out, "out"),
@@ -705,9 +722,11 @@ def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0,
     if len(grid) != 3 or len(start) != 3 or len(step) != 3:
         raise ValueError("grid, start and step must have three entries")
     n = sum(int(g) * (a // 2) for g, a in zip(grid, axes))
-    table = torch.empty((max(n, 0), 2), dtype=torch.float32, device=device)
-    with _On(table, stream) as on:
-        on.keep(table)
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _On(device, stream) as on:
+        table = on.empty((max(n, 0), 2), torch.float32)
         i3, d3 = ctypes.c_int32 * 3, ctypes.c_double * 3
         _check(lib.dsa_rope_table(i3(*(int(g) for g in grid)), i3(*axes), d3(*(float(x) for x in start)),
                                   d3(*(float(x) for x in step)), float(theta), table.data_ptr(), on.ptr),
@@ -750,11 +769,11 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: 
     def result(x, y, name):
         _like(x, name, q, q.shape, q.dtype)
         if y is None:
-            return on.keep(torch.empty(x.shape, dtype=x.dtype, device=x.device))
+            return on.empty(x.shape, x.dtype)
         _like(y, name + "_out", q, q.shape, q.dtype)
         return y
 
-    with _On(q, stream) as on:
+    with _On(q.device, stream) as on:
         q_out = result(q, q_out, "q")
         kv = ko = None
         if k is not None:
@@ -797,7 +816,7 @@ def _norm(x: torch.Tensor, weight, eps: float):
 def _contiguous_out(t, name: str, ref: torch.Tensor, on: _On, dtype=None):
     dtype = dtype or ref.dtype
     if t is None:
-        return on.keep(torch.empty(ref.shape, dtype=dtype, device=ref.device))
+        return on.empty(ref.shape, dtype)
     _like(t, name, ref, ref.shape, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -833,7 +852,7 @@ def _rms_norm(x, weight, eps, residual, out, scales, sum_out, dtype8, stream):
         r_ld = _rows(residual, "residual")[2]
     elif sum_out is not None:
         raise ValueError("sum_out without a residual")
-    with _On(x, stream) as on:
+    with _On(x.device, stream) as on:
         y = _contiguous_out(out, "out", x, on, dtype8)
         h = _contiguous_out(sum_out, "sum_out", x, on) if residual is not None else None
         args = (p, x.data_ptr(), x_ld, _addr(residual), r_ld, _addr(weight), y.data_ptr())
@@ -842,7 +861,7 @@ def _rms_norm(x, weight, eps, residual, out, scales, sum_out, dtype8, stream):
         else:
             shape = x.shape[:-1] + ((p.C + 127) // 128,)
             if scales is None:
-                scales = on.keep(torch.empty(shape, dtype=torch.float32, device=x.device))
+                scales = on.empty(shape, torch.float32)
             _like(scales, "scales", x, shape, torch.float32)
             if not scales.is_contiguous():
                 raise ValueError("scales must be contiguous")
@@ -865,7 +884,7 @@ def rms_norm_backward(h: torch.Tensor, weight: Optional[torch.Tensor], dy: torch
         dh_ld = _rows(dh, "dh")[2]
     if weight is None and dweight is not None:
         raise ValueError("dweight without a weight")
-    with _On(h, stream) as on:
+    with _On(h.device, stream) as on:
         dx = _contiguous_out(dx, "dx", h, on)
         if weight is not None:
             dweight = _contiguous_out(dweight, "dweight", weight, on)
