@@ -444,7 +444,9 @@ __global__ void __launch_bounds__(NV <= 2 ? 736 : 544) rmsnorm_bwd_kernel(NormBw
         par ^= 1;
       }
       const float rho = rsqrtf(ss * inv_c + p.eps);
-      const float k = rho * rho * rho * (gh * inv_c);
+      // dx = rho (g - h rho^2 mean(g h)) + dh, rho taken in one factor at a time: rho^3 alone leaves
+      // fp32's range for rows of 1e13 and above or 1e-13 and below, whose gradient does not
+      const float k = rho * (gh * inv_c) * rho;
       if (!live || !ok) continue;  // no barrier follows for this row
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -461,8 +463,8 @@ __global__ void __launch_bounds__(NV <= 2 ? 736 : 544) rmsnorm_bwd_kernel(NormBw
         for (int e = 0; e < 8; e += 2) {
           float g0, g1;
           ffma2(g0, g1, gv[e], gv[e + 1], wv[e], wv[e + 1], 0.f, 0.f);
-          ffma2(g0, g1, g0, g1, rho, rho, o[e], o[e + 1]);
-          ffma2(o[e], o[e + 1], hv[e], hv[e + 1], -k, -k, g0, g1);
+          ffma2(g0, g1, hv[e], hv[e + 1], -k, -k, g0, g1);
+          ffma2(o[e], o[e + 1], g0, g1, rho, rho, o[e], o[e + 1]);
           if constexpr (kDw) {
             ffma2(g0, g1, hv[e], hv[e + 1], rho, rho, 0.f, 0.f);
             ffma2(acc[i][e], acc[i][e + 1], gv[e], gv[e + 1], g0, g1, acc[i][e], acc[i][e + 1]);
