@@ -279,10 +279,18 @@ __global__ void __launch_bounds__(512) rmsnorm_kernel(NormParams p) {
       for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
       // NaN in the group: NaN scale; nothing but zeros: 1
       const float s = m == 0.f ? 1.f : max_nan(m / kE4m3Max, kMinScale);
-      const float inv = 1.f / s;
+      // y / s as y times 1 / s in two terms (Brisebarre, Muller, Raina, "Accelerating correctly rounded
+      // floating-point division when the divisor is known in advance"): one term's product puts a
+      // value next to a tie on its other side, a division of each value takes a fifth more time
+      // (71680 x 1536 with a residual: 176 us against 147)
+      const float hi = 1.f / s, lo = s < INFINITY ? fmaf(-hi, s, 1.f) * hi : 0.f;
       if (in) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= inv;
+        for (int e = 0; e < 8; e += 2) {
+          float a, b;
+          fmul2(a, b, y[e], y[e + 1], lo, lo);
+          ffma2(y[e], y[e + 1], y[e], y[e + 1], hi, hi, a, b);
+        }
         store8_e4m3<kAligned>(static_cast<uint8_t*>(p.y) + row * p.C, c, p.C, y);
         if ((t & 15) == 0) p.scales[row * ((p.C + kGroup - 1) / kGroup) + c / kGroup] = s;
       }
