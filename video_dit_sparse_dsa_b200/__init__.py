@@ -629,6 +629,12 @@ def _ws(ws: Optional[torch.Tensor], n_bytes: int, on: _On, ref: torch.Tensor):
     return ws, ws.numel() * ws.element_size()
 
 
+def _fit(*sizes: int):
+    """Sizes that the C structures' 32 bits hold (ctypes would keep the low bits of larger ones)."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise DsaError(2, f"a size of {max(sizes)}")
+
+
 def _rows_view(t: torch.Tensor, name: str) -> View:
     """A [B, heads, rows, d] tensor as dsa_view_t."""
     s = t.stride()
@@ -642,6 +648,7 @@ def _cross(q, k, v, kv_len, scale) -> Cross:
         raise ValueError("q must be [B, heads, Lq, d], k and v [B, kv_heads, Lk, d]")
     B, heads, Lq, d = q.shape
     _, kv_heads, Lk, _ = k.shape
+    _fit(B, heads, kv_heads, Lq, Lk, d)
     _like(k, "k", q, (B, kv_heads, Lk, d), q.dtype)
     _like(v, "v", q, k.shape, q.dtype)
     if kv_len is not None:
@@ -721,6 +728,7 @@ def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0,
     axes = _axes(axes)
     if len(grid) != 3 or len(start) != 3 or len(step) != 3:
         raise ValueError("grid, start and step must have three entries")
+    _fit(*(int(g) for g in grid), *axes)
     n = sum(int(g) * (a // 2) for g, a in zip(grid, axes))
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
@@ -759,6 +767,7 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: 
         raise ValueError("q must be [B, heads, T, H, W, d]")
     axes = _axes(axes)
     B, heads, T, H, W, d = q.shape
+    _fit(*q.shape, *axes)
     p = Rope(B, heads, d, T, H, W, tuple(axes), 1 if interleaved else 0, 1 if inverse else 0, _dtype_of(q, "q"))
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
@@ -806,6 +815,7 @@ def _rows(t: torch.Tensor, name: str):
 
 def _norm(x: torch.Tensor, weight, eps: float):
     rows, C, ld = _rows(x, "x")
+    _fit(C)
     if weight is not None:
         _like(weight, "weight", x, (C,), x.dtype)
         if not weight.is_contiguous():
