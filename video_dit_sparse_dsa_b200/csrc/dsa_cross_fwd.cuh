@@ -262,10 +262,8 @@ struct Cursor {
 };
 
 // 2^x for a pair on the FMA pipe: as exp2_poly2, with a quartic for 2^f (minimax fit on
-// [-0.5, 0.5], relative error 2.6e-6), because the row sums also give the fp32 LSE, and a NaN
-// argument kept: the clamp keeps it, and 2^n comes in as a factor (added to the exponent field it
-// would make a number of it).  Times as with exp2_poly2's clamp and addition; a max over the scores
-// that keeps NaN took 1 to 2% more.
+// [-0.5, 0.5], relative error 2.6e-6), because the row sums also give the fp32 LSE.  (That it keeps
+// NaN costs nothing measurable; a max over the scores that keeps it took 1 to 2% more.)
 __device__ __forceinline__ void exp2_quartic2(float x0, float x1, float& y0, float& y1) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 0.9999992847442627f, c1 = 0.6931217908859253f, c2 = 0.240247443318367f,
@@ -281,7 +279,8 @@ __device__ __forceinline__ void exp2_quartic2(float x0, float x1, float& y0, flo
   ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
   ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
   constexpr int kOne = 0x3f800000;
-  fmul2(y0, y1, q0, q1, __int_as_float(kOne + (__float_as_int(t0) << 23)), __int_as_float(kOne + (__float_as_int(t1) << 23)));
+  fmul2_ftz(y0, y1, q0, q1, __int_as_float(kOne + (__float_as_int(t0) << 23)),
+            __int_as_float(kOne + (__float_as_int(t1) << 23)));
 }
 
 // An arrival on the MMA warp's barrier: this CTA's, or the even CTA's of the pair (whose address
@@ -345,13 +344,9 @@ __device__ __forceinline__ void exp_16(const uint32_t* s, float scale_log2, floa
 // A row's running softmax: the reference max, the row sum against it, and the factor that the old
 // O and l take where the reference moved in the last step.
 //
-// Scores that are not finite: NaN reaches l and O through its exponential; +inf becomes the
-// reference, and against it its own exponential is NaN; -inf has the weight 0 against the lowest
-// finite value, where the reference starts, so a row that ends there has no weight at all.
-constexpr float kLowest = -3.402823466e38f;
+// The reference starts at fwd::kLowest, for scores that are not finite.
 struct RowState {
-  static constexpr float kNan = __builtin_nanf("");
-  float m_used = kLowest, l = 0.f, alpha = 1.f;
+  float m_used = fwd::kLowest, l = 0.f, alpha = 1.f;
   // Agrees with the partner thread on the row max, mx being this thread's; true: it moved.
   __device__ __forceinline__ bool update(bool ok, float mx, float scale_log2, float* xbuf, int& xe, int i, int r, int bar_id) {
     mx = fmaxf(mx, fwd::pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
@@ -365,12 +360,6 @@ struct RowState {
     }
     l *= alpha;
     return need;
-  }
-  // 1 / l and LSE of the row, l being the sum of both threads'.
-  __device__ __forceinline__ float inverse(float l_all) const { return m_used == kLowest ? kNan : 1.f / l_all; }
-  __device__ __forceinline__ float lse(float l_all) const {
-    if (m_used == kLowest) return l_all == l_all ? -INFINITY : l_all;  // (every score NaN)
-    return m_used == INFINITY ? INFINITY : (m_used + __log2f(l_all)) * 0.69314718055994531f;
   }
 };
 
@@ -944,8 +933,8 @@ __global__ void __launch_bounds__(crossf::kThreads, 1)
       const float l_all = act ? st.l + fwd::pair_exchange(xbuf, xe, i, r, bar_id, st.l) : 1.f;
       px = c.x;
       px.row += 128 * rank;
-      p_inv = st.inverse(l_all);
-      p_lse = st.lse(l_all);
+      p_inv = fwd::row_inverse(st.m_used, l_all);
+      p_lse = fwd::row_lse(st.m_used, l_all);
       pending = true;
     }
     if (ok && pending) write_out();

@@ -285,6 +285,20 @@ __device__ __forceinline__ float pair_exchange(float* xbuf, int& xe, int i, int 
   return b[(i ^ 1) * 128 + r];
 }
 
+// A row's reference max starts at the lowest finite value, against which a score of -inf has the
+// weight 0 (against -inf it would be NaN).  A score of +inf becomes the reference for good; one of
+// NaN reaches l and O through its exponential or, where that is a polynomial, becomes the reference
+// (only those columns need a max that keeps NaN).  1 / l (NaN with such a reference, and of a row
+// without any weight) and the LSE, from the sum l of both threads of the row:
+constexpr float kLowest = -3.402823466e38f;
+__device__ __forceinline__ float row_inverse(float m_used, float l) {
+  return fabsf(m_used) < -kLowest ? 1.f / l : __int_as_float(0x7fc00000);
+}
+__device__ __forceinline__ float row_lse(float m_used, float l) {
+  if (m_used == kLowest) return l == l ? -INFINITY : l;  // (every score -inf; some NaN)
+  return m_used == INFINITY ? INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
+}
+
 // The softmax of one step for this thread's NC score columns at tS (NC = 128: a full step,
 // NC = 64: a half step): agrees on the row max with the partner thread, writes packed bf16
 // P (NC/2 columns) at tP, updates m_used and l, and returns whether the reference max
@@ -319,21 +333,26 @@ __device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, 
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(loaded) : "memory");
     }
   }
-  // row max: 8 independent chains over columns e, e + 8, ..., e + NC - 8
+  // row max: 8 independent chains over columns e, e + 8, ..., e + NC - 8, those of the polynomial
+  // last
+  static_assert((kPolyMask & 3u) == 0, "the chains start in the first two groups");
   float mxs[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    mxs[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[NC - 8 + e]));
+    mxs[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[8 + e]));
 #pragma unroll
-    for (int c = 8 + e; c < NC - 8; c += 16)
-      mxs[e] = max3f(mxs[e], __uint_as_float(s[c]), __uint_as_float(s[c + 8]));
+    for (int g = 1; g < NC / 16; ++g)
+      if (!((kPolyMask >> g) & 1u)) mxs[e] = max3f(mxs[e], __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + 8 + e]));
+#pragma unroll
+    for (int g = 1; g < NC / 16; ++g)
+      if ((kPolyMask >> g) & 1u) mxs[e] = max3_nan(mxs[e], __uint_as_float(s[16 * g + e]), __uint_as_float(s[16 * g + 8 + e]));
   }
-  float mx = max3f(max3f(mxs[0], mxs[1], mxs[2]), max3f(mxs[3], mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7]));
-  mx = fmaxf(mx, pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
+  float mx = max3_nan(max3_nan(mxs[0], mxs[1], mxs[2]), max3_nan(mxs[3], mxs[4], mxs[5]), max_nan(mxs[6], mxs[7]));
+  mx = max_nan(mx, pair_exchange(xbuf, xe, i, r, bar_id, ok ? mx : -INFINITY));
   alpha = 1.f;
   if (!ok) return false;
-  const float m_new = fmaxf(m_used, mx * scale_log2);
-  const bool need = m_new > m_used + kRescaleThreshold;
+  const float m_new = max_nan(m_used, mx * scale_log2);
+  const bool need = !(m_new <= m_used + kRescaleThreshold) && m_used == m_used;  // (to NaN once)
   if (need) {
     alpha = ex2_approx(m_used - m_new);
     m_used = m_new;
@@ -352,7 +371,7 @@ __device__ __forceinline__ bool softmax_step(bool ok, uint32_t tS, uint32_t tP, 
       ffma2(x0, x1, __uint_as_float(s[16 * g + 2 * e]), __uint_as_float(s[16 * g + 2 * e + 1]), scale_log2,
             scale_log2, neg_m, neg_m);
       if ((kPolyMask >> g) & 1u) {
-        exp2_poly2(x0, x1, p0, p1);
+        exp2_poly2<false>(x0, x1, p0, p1);
       } else {
         p0 = ex2_approx(x0);
         p1 = ex2_approx(x1);
@@ -706,7 +725,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
                     neg_lse);
               float p0, p1;
               if ((kPolyMaskMap >> ((c >> 1) & 7)) & 1u) {  // a share of 2^x on the FMA pipe
-                exp2_poly2(x0, x1, p0, p1);
+                exp2_poly2<true>(x0, x1, p0, p1);
               } else {
                 p0 = ex2_approx(x0);
                 p1 = ex2_approx(x1);
@@ -784,7 +803,7 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         }
         continue;
       }
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = kLowest, l = 0.f;
       for (int t = 0; t < n_steps; ++t) {
         const int e = (g + t) & 1;
         if (ok) ok = warp_wait(s_full + e, (e == 0 ? sc0++ : sc1++) & 1, abort, 40);
@@ -830,12 +849,12 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
         // (the TMEM loads of store_o are warp-collective: every lane takes part, and only
         // rows that exist are written)
         const bool row_ok = tok < rows;
-        store_o(tO, 2, 1.f / l_all,
+        store_o(tO, 2, row_inverse(m_used, l_all),
                 reinterpret_cast<uint4*>(p.out + po + (static_cast<int64_t>(x.bh) * rows + (row_ok ? tok : 0)) * 128) +
                     8 * i,
                 row_ok);
         if (i == 0 && row_ok)
-          p.lse[pl + static_cast<int64_t>(x.bh) * rows + tok] = (m_used + __log2f(l_all)) * 0.69314718055994531f;
+          p.lse[pl + static_cast<int64_t>(x.bh) * rows + tok] = row_lse(m_used, l_all);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
@@ -857,8 +876,8 @@ __global__ void __launch_bounds__(fwd::kThreads, 1)
 // Merge of n attentions of the same rows over disjoint key sets (parts j = 0..n-1 at
 // o + j * part_out, lse + j * part_lse):  L = ln sum_j e^lse_j,  O = sum_j e^(lse_j - L) O_j
 // (exact: the softmax over the union, written through the parts' own normalisations).  A
-// part with lse = -inf (no keys) has weight 0.  16 threads per 128-channel row, 8 channels
-// each; fp32 sums, bf16 result.
+// part with lse = -inf has weight 0 (its O is 0 without keys, NaN where every score is -inf).
+// 16 threads per 128-channel row, 8 channels each; fp32 sums, bf16 result.
 __global__ void __launch_bounds__(256) merge_parts_kernel(const __nv_bfloat16* o, const float* lse, int n_parts,
                                                           int64_t part_out, int64_t part_lse, int64_t rows,
                                                           __nv_bfloat16* out, float* lse_out) {
@@ -866,22 +885,23 @@ __global__ void __launch_bounds__(256) merge_parts_kernel(const __nv_bfloat16* o
   const int part = threadIdx.x % 16;
   if (row >= rows) return;
   float m = -INFINITY;
-  for (int j = 0; j < n_parts; ++j) m = fmaxf(m, lse[j * part_lse + row]);
+  for (int j = 0; j < n_parts; ++j) m = max_nan(m, lse[j * part_lse + row]);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float L = -INFINITY;
   if (m != -INFINITY) {
     float sum = 0.f;
     for (int j = 0; j < n_parts; ++j) sum += __expf(lse[j * part_lse + row] - m);
-    L = m + __logf(sum);
-    for (int j = 0; j < n_parts; ++j) {
-      const float w = __expf(lse[j * part_lse + row] - L);
-      const uint4 x = reinterpret_cast<const uint4*>(o + j * part_out + row * 128)[part];
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+    L = m == INFINITY ? m : m + __logf(sum);
+  }
+  for (int j = 0; j < n_parts; ++j) {
+    const float lj = lse[j * part_lse + row], w = lj == -INFINITY && L == L ? 0.f : __expf(lj - L);
+    const uint4 x = reinterpret_cast<const uint4*>(o + j * part_out + row * 128)[part];
+    if (w == 0.f && m != -INFINITY) continue;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] += w * __uint_as_float(xs[e] << 16);
-        acc[2 * e + 1] += w * __uint_as_float(xs[e] & 0xffff0000u);
-      }
+    for (int e = 0; e < 4; ++e) {
+      acc[2 * e] += w * __uint_as_float(xs[e] << 16);
+      acc[2 * e + 1] += w * __uint_as_float(xs[e] & 0xffff0000u);
     }
   }
   reinterpret_cast<uint4*>(out + row * 128)[part] =

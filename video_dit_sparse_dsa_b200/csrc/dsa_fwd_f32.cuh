@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(kF32Threads) fwd_f32_kernel(FwdF32Params p) {
     qv[c] = active ? p.q[base + qtok * D + part * 64 + c] : 0.f;
     acc[c] = 0.f;
   }
-  float m = -INFINITY, l = 0.f;
+  // from the lowest finite value, against which a score of -inf has the weight 0 (against -inf: NaN)
+  float m = -3.402823466e38f, l = 0.f;
 
   for (int wi = 0; wi < p.Wt; ++wi) {
     const int kt = p.kv_tiles[static_cast<int64_t>(tile) * p.Wt + wi];
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kF32Threads) fwd_f32_kernel(FwdF32Params p) {
   const float inv = 1.f / l;
 #pragma unroll
   for (int c = 0; c < 64; ++c) p.out[base + qtok * D + part * 64 + c] = acc[c] * inv;
-  if (part == 0) p.lse[bh * p.N + qtok] = m + logf(l);
+  if (part == 0) p.lse[bh * p.N + qtok] = m == INFINITY ? m : m + logf(l);
 }
 
 }  // namespace dsa

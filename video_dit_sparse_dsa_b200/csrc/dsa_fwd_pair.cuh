@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fwdp::kThreads, 1)
         if (i == 0) p.lse[static_cast<int64_t>(x.bh) * p.N + tok] = -INFINITY;
         continue;
       }
-      float m_used = -INFINITY, l = 0.f;
+      float m_used = fwd::kLowest, l = 0.f;
       for (int t = 0; t < n_steps; ++t) {
         const int e = (g + t) & 1;
         if (ok) ok = fwd::warp_wait(s_full + e, (e == 0 ? sc0++ : sc1++) & 1, abort, 72);
@@ -388,10 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fwdp::kThreads, 1)
       if (ok) {
         tc_fence_after();
         const int64_t tok = fwd::chunk_token(p, x.tile, x.sub, r);
-        fwd::store_o(tO, 2, 1.f / l_all,
+        fwd::store_o(tO, 2, fwd::row_inverse(m_used, l_all),
                      reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(x.bh) * p.N + tok) * 128) + 8 * i);
         if (i == 0)
-          p.lse[static_cast<int64_t>(x.bh) * p.N + tok] = (m_used + __log2f(l_all)) * 0.69314718055994531f;
+          p.lse[static_cast<int64_t>(x.bh) * p.N + tok] = fwd::row_lse(m_used, l_all);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(o_free), 0));

@@ -590,10 +590,16 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// max that keeps NaN
+// max that keeps NaN, of two and of three floats (one instruction on sm_100)
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -627,6 +633,17 @@ __device__ __forceinline__ void fadd2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// (a product below 2^-126 is 0)
+__device__ __forceinline__ void fmul2_ftz(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.ftz.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
   asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
       "mov.b64 ra, {%2, %3};\n\t"
@@ -643,12 +660,16 @@ __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, 
 // squares on Chebyshev nodes of [-0.5, 0.5], maximum relative error 7.6e-5, far below the
 // 2^-9 relative rounding of the bf16 probabilities it feeds); 2^n by adding n to the
 // exponent field.  Arguments below -126 are clamped there (2^-126 ~ 1e-38).
+// kNan: NaN stays NaN (in the clamp, and by 2^n as a factor: n added to the exponent of the
+// cubic's NaN would make a number of it), and arguments of -126 and below give 0 (the cubic is below
+// 1 there, and the product flushed).
+template <bool kNan>
 __device__ __forceinline__ void exp2_poly2(float x0, float x1, float& y0, float& y1) {
   constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 0.99992793798446655f, c1 = 0.69325828552246094f, c2 = 0.24261236190795898f,
                   c3 = 0.055186375975608826f;
-  x0 = fmaxf(x0, -126.f);
-  x1 = fmaxf(x1, -126.f);
+  x0 = kNan ? max_nan(x0, -126.f) : fmaxf(x0, -126.f);
+  x1 = kNan ? max_nan(x1, -126.f) : fmaxf(x1, -126.f);
   float t0, t1, n0, n1, f0, f1, q0, q1;
   fadd2(t0, t1, x0, x1, kRound, kRound);
   fadd2(n0, n1, t0, t1, -kRound, -kRound);
@@ -656,8 +677,14 @@ __device__ __forceinline__ void exp2_poly2(float x0, float x1, float& y0, float&
   ffma2(q0, q1, c3, c3, f0, f1, c2, c2);
   ffma2(q0, q1, q0, q1, f0, f1, c1, c1);
   ffma2(q0, q1, q0, q1, f0, f1, c0, c0);
-  y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+  if constexpr (kNan) {
+    constexpr int kOne = 0x3f800000;
+    fmul2_ftz(y0, y1, q0, q1, __int_as_float(kOne + (__float_as_int(t0) << 23)),
+              __int_as_float(kOne + (__float_as_int(t1) << 23)));
+  } else {
+    y0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+    y1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
