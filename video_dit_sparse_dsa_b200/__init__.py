@@ -221,339 +221,6 @@ def _need(t: torch.Tensor, name: str, like: torch.Tensor, dtype=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-def plan_shape(problem: Problem):
-    lib = load_library()
-    n, wt = ctypes.c_int32(), ctypes.c_int32()
-    _check(lib.dsa_plan_shape(ctypes.byref(problem), ctypes.byref(n), ctypes.byref(wt)), "dsa_plan_shape")
-    return n.value, wt.value
-
-
-def workspace_size(problem: Problem, backward: bool = False) -> int:
-    return int(load_library().dsa_workspace_size(ctypes.byref(problem), DSA_WS_BWD if backward else DSA_WS_FWD))
-
-
-def workspace(problem: Problem, device, backward: bool = False) -> torch.Tensor:
-    """A device workspace of the right size (torch's caching allocator returns 512-byte
-    aligned blocks)."""
-    return torch.empty(max(workspace_size(problem, backward), 256), dtype=torch.uint8, device=device)
-
-
-def plan(problem: Problem, offsets: torch.Tensor, inverse: bool = True, stream=None):
-    """Run the window planner.  Returns (starts, kv_tiles[, row_ptr, q_tiles]) on the device."""
-    lib = load_library()
-    n, wt = plan_shape(problem)
-    dev = offsets.device
-    if not offsets.is_cuda or offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.numel() != 3 * n:
-        raise ValueError("offsets must be a contiguous int32 CUDA tensor [nTiles, 3]")
-    starts = torch.empty((n, 3), dtype=torch.int32, device=dev)
-    kv = torch.empty((n, wt), dtype=torch.int32, device=dev)
-    row_ptr = torch.empty(n + 1, dtype=torch.int32, device=dev) if inverse else None
-    q_tiles = torch.empty(n * wt, dtype=torch.int32, device=dev) if inverse else None
-    _check(lib.dsa_plan(ctypes.byref(problem), _ptr(offsets), _ptr(starts), _ptr(kv), _ptr(row_ptr), _ptr(q_tiles),
-                        ctypes.c_void_p(_stream(stream))), "dsa_plan")
-    return (starts, kv, row_ptr, q_tiles) if inverse else (starts, kv)
-
-
-def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, tile: Sequence[int],
-            window: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-            lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
-    """3D-DSA forward.  Returns (out, lse)."""
-    lib = load_library()
-    p = _problem_of(q, tile, window, scale)
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    _need(offsets, "offsets", q, torch.int32)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(q.shape[:5], dtype=torch.float32, device=q.device)
-    _need(out, "out", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
-    if ws is None:
-        ws = workspace(p, q.device)
-    _check(lib.dsa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), _ptr(out), _ptr(lse), _ptr(ws),
-                       ws.numel(), ctypes.c_void_p(_stream(stream))), "dsa_fwd")
-    return out, lse
-
-
-def prefix_workspace_size(problem: Problem, L_text: int) -> int:
-    return int(load_library().dsa_prefix_workspace_size(ctypes.byref(problem), int(L_text)))
-
-
-def forward_prefix(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, q_text: torch.Tensor,
-                   k_text: torch.Tensor, v_text: torch.Tensor, tile: Sequence[int], window: Sequence[int],
-                   scale: Optional[float] = None, ws: Optional[torch.Tensor] = None, stream=None):
-    """3D-DSA with a text prefix: video queries over their windows and every text key, text
-    queries over every key.  q, k, v: [B, heads, T, H, W, 128]; q_text, k_text, v_text:
-    [B, heads, L_text, 128].  Returns (out, lse, out_text, lse_text)."""
-    lib = load_library()
-    p = _problem_of(q, tile, window, scale)
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    _need(offsets, "offsets", q, torch.int32)
-    if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
-        raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
-    for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q_text.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q_text shape {tuple(q_text.shape)}")
-    L_text = int(q_text.shape[2])
-    out = torch.empty_like(q)
-    lse = torch.empty(q.shape[:5], dtype=torch.float32, device=q.device)
-    out_text = torch.empty_like(q_text)
-    lse_text = torch.empty(q_text.shape[:3], dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.empty(max(prefix_workspace_size(p, L_text), 256), dtype=torch.uint8, device=q.device)
-    _check(lib.dsa_fwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), L_text, _ptr(q_text),
-                              _ptr(k_text), _ptr(v_text), _ptr(out), _ptr(lse), _ptr(out_text), _ptr(lse_text),
-                              _ptr(ws), ws.numel(), ctypes.c_void_p(_stream(stream))), "dsa_fwd_prefix")
-    return out, lse, out_text, lse_text
-
-
-def selftest_wait(stream=None):
-    """Enqueue the failure-path self-test (a bounded wait that runs out after 2 s and records
-    DSA_ERR_TIMEOUT at site 99); read the result with device_status()."""
-    _check(load_library().dsa_selftest_wait(ctypes.c_void_p(_stream(stream))), "dsa_selftest_wait")
-
-
-def prefix_bwd_workspace_size(problem: Problem, L_text: int) -> int:
-    return int(load_library().dsa_bwd_prefix_workspace_size(ctypes.byref(problem), int(L_text)))
-
-
-def backward_prefix(q, k, v, out, lse, dout, offsets, q_text, k_text, v_text, out_text, lse_text, dout_text,
-                    tile: Sequence[int], window: Sequence[int], scale: Optional[float] = None,
-                    ws: Optional[torch.Tensor] = None, stream=None):
-    """Backward of forward_prefix (gradients of sum(out * dout) + sum(out_text * dout_text)).
-    Returns (dq, dk, dv, dq_text, dk_text, dv_text)."""
-    lib = load_library()
-    p = _problem_of(q, tile, window, scale)
-    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
-    _need(offsets, "offsets", q, torch.int32)
-    if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
-        raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
-    for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text"), (out_text, "out_text"),
-                    (dout_text, "dout_text")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q_text.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q_text shape {tuple(q_text.shape)}")
-    _need(lse_text, "lse_text", q, torch.float32)
-    L_text = int(q_text.shape[2])
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
-    dqt, dkt, dvt = torch.empty_like(q_text), torch.empty_like(q_text), torch.empty_like(q_text)
-    if ws is None:
-        ws = torch.empty(max(prefix_bwd_workspace_size(p, L_text), 256), dtype=torch.uint8, device=q.device)
-    _check(lib.dsa_bwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                              _ptr(offsets), L_text, _ptr(q_text), _ptr(k_text), _ptr(v_text), _ptr(out_text),
-                              _ptr(lse_text), _ptr(dout_text), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dqt), _ptr(dkt),
-                              _ptr(dvt), _ptr(ws), ws.numel(), ctypes.c_void_p(_stream(stream))), "dsa_bwd_prefix")
-    return dq, dk, dv, dqt, dkt, dvt
-
-
-def forward_host_bytes(problem: Problem) -> int:
-    return int(load_library().dsa_fwd_host_bytes(ctypes.byref(problem)))
-
-
-def forward_host(problem: Problem, q_host: torch.Tensor, k_host: torch.Tensor, v_host: torch.Tensor,
-                 offsets_host: torch.Tensor, out_host: torch.Tensor, lse_host: torch.Tensor, dev: torch.Tensor,
-                 stream=None):
-    """3D-DSA forward from pinned host tensors through the caller's device buffer ``dev``
-    (uint8, at least forward_host_bytes(problem) bytes); asynchronous on ``stream``."""
-    lib = load_library()
-    for t in (q_host, k_host, v_host, offsets_host, out_host, lse_host):
-        if t.is_cuda or not t.is_contiguous():
-            raise ValueError("host tensors must be contiguous CPU tensors")
-    _check(lib.dsa_fwd_host(ctypes.byref(problem), _ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(offsets_host),
-                            _ptr(out_host), _ptr(lse_host), _ptr(dev), dev.numel(), ctypes.c_void_p(_stream(stream))),
-           "dsa_fwd_host")
-
-
-def backward(q, k, v, out, lse, dout, offsets, tile, window, scale=None, dq=None, dk=None, dv=None, ws=None,
-             stream=None):
-    """3D-DSA backward of sum(out * dout).  Returns (dq, dk, dv)."""
-    lib = load_library()
-    p = _problem_of(q, tile, window, scale)
-    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
-    _need(offsets, "offsets", q, torch.int32)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
-    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, name, q, q.dtype)
-    if ws is None:
-        ws = workspace(p, q.device, backward=True)
-    _check(lib.dsa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(offsets),
-                       _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), ctypes.c_void_p(_stream(stream))),
-           "dsa_bwd")
-    return dq, dk, dv
-
-
-def _list_args(q: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor, n_tiles: int):
-    """-> (list pointer, nnz, per_head): row_ptr [nTiles + 1] is one list for every head,
-    [B * heads, nTiles + 1] one list per (batch, head)."""
-    _need(row_ptr, "row_ptr", q, torch.int32)
-    BH = q.shape[0] * q.shape[1]
-    if row_ptr.numel() == n_tiles + 1 and row_ptr.dim() == 1:
-        per_head = 0
-    elif tuple(row_ptr.shape) == (BH, n_tiles + 1):
-        per_head = 1
-    else:
-        raise ValueError(f"row_ptr must be [nTiles + 1] or [B * heads, nTiles + 1], got {tuple(row_ptr.shape)}")
-    if kv_list is not None and kv_list.numel() > 0:
-        _need(kv_list, "kv_list", q, torch.int32)
-        return _ptr(kv_list), int(kv_list.numel()), per_head
-    return None, 0, per_head
-
-
-def forward_list(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor,
-                 tile: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                 lse: Optional[torch.Tensor] = None, stream=None):
-    """Block-sparse forward over key-tile lists: query tile i attends to the key tiles
-    kv_list[row_ptr[i]:row_ptr[i+1]] (int32 CUDA tensors; tiles in raster order of the tile
-    grid); row_ptr [nTiles + 1] is one list for every head, [B * heads, nTiles + 1] one per
-    (batch, head) with absolute positions in kv_list.  Returns (out, lse); an empty row
-    gives out = 0 and lse = -inf."""
-    lib = load_library()
-    p = _problem_of(q, tile, (1, 1, 1), scale)
-    for t, name in ((k, "k"), (v, "v")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    n_tiles, _ = plan_shape(p)
-    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty(q.shape[:5], dtype=torch.float32, device=q.device)
-    _need(out, "out", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
-    _check(lib.dsa_fwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), lst, nnz, per_head, _ptr(out),
-                            _ptr(lse), ctypes.c_void_p(_stream(stream))), "dsa_fwd_list")
-    return out, lse
-
-
-def backward_list(q, k, v, out, lse, dout, row_ptr, kv_list, tile, scale=None, dq=None, dk=None, dv=None, ws=None,
-                  stream=None):
-    """Backward of sum(out * dout) for forward_list.  Returns (dq, dk, dv)."""
-    lib = load_library()
-    p = _problem_of(q, tile, (1, 1, 1), scale)
-    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
-        _need(t, name, q, q.dtype)
-        if t.shape != q.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
-    _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
-    n_tiles, _ = plan_shape(p)
-    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
-    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, name, q, q.dtype)
-    if ws is None:
-        size = int(lib.dsa_list_workspace_size(ctypes.byref(p), nnz, per_head, DSA_WS_BWD))
-        ws = torch.empty(max(size, 256), dtype=torch.uint8, device=q.device)
-    _check(lib.dsa_bwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                            _ptr(row_ptr), lst, nnz, per_head, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-                            ctypes.c_void_p(_stream(stream))), "dsa_bwd_list")
-    return dq, dk, dv
-
-
-def block_map(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor,
-              tile: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None):
-    """Block attention mass [B * heads, nTiles, nTiles] (fp32): mean attention probability
-    of each query tile's tokens on each key tile, against the LSE forward_list wrote for
-    the same lists."""
-    lib = load_library()
-    p = _problem_of(q, tile, (1, 1, 1), scale)
-    _need(q, "q", q)
-    _need(k, "k", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
-    n_tiles, _ = plan_shape(p)
-    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
-    BH = q.shape[0] * q.shape[1]
-    if out is None:
-        out = torch.empty((BH, n_tiles, n_tiles), dtype=torch.float32, device=q.device)
-    _need(out, "out", q, torch.float32)
-    _check(lib.dsa_block_map(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_ptr), lst, nnz, per_head,
-                             _ptr(out), ctypes.c_void_p(_stream(stream))), "dsa_block_map")
-    return out
-
-
-def lstsq_factor(M: torch.Tensor, lam: float, stream=None) -> torch.Tensor:
-    """Cholesky factor (fp64 [p, p], lower) of M^T M + lam I for a design matrix M (fp32
-    CUDA [m, p], p <= 32), to be reused by lstsq_solve across heads and steps."""
-    lib = load_library()
-    if not M.is_cuda or M.dtype != torch.float32 or not M.is_contiguous() or M.dim() != 2:
-        raise ValueError("M must be a contiguous fp32 CUDA tensor [m, p]")
-    m, p = M.shape
-    L = torch.empty((p, p), dtype=torch.float64, device=M.device)
-    _check(lib.dsa_lstsq_factor(m, p, _ptr(M), float(lam), _ptr(L), ctypes.c_void_p(_stream(stream))),
-           "dsa_lstsq_factor")
-    return L
-
-
-def lstsq_solve(M: torch.Tensor, L: torch.Tensor, S: torch.Tensor, X: Optional[torch.Tensor] = None, ws=None,
-                stream=None) -> torch.Tensor:
-    """X [batch, p] (fp32) with (M^T M + lam I) x_b = M^T s_b for every row s_b of S
-    [batch, m] (fp32 CUDA), L from lstsq_factor."""
-    lib = load_library()
-    m, p = M.shape
-    if not S.is_cuda or S.dtype != torch.float32 or not S.is_contiguous() or S.dim() != 2 or S.shape[1] != m:
-        raise ValueError("S must be a contiguous fp32 CUDA tensor [batch, m]")
-    batch = S.shape[0]
-    if X is None:
-        X = torch.empty((batch, p), dtype=torch.float32, device=S.device)
-    n_ws = int(lib.dsa_lstsq_workspace_size(m, p, batch))
-    if ws is None and n_ws > 0:
-        ws = torch.empty(n_ws, dtype=torch.uint8, device=S.device)
-    _check(lib.dsa_lstsq_solve(m, p, batch, _ptr(M), _ptr(L), _ptr(S), _ptr(X), _ptr(ws),
-                               0 if ws is None else ws.numel(), ctypes.c_void_p(_stream(stream))), "dsa_lstsq_solve")
-    return X
-
-
-def plan_heads(problem: Problem, offsets: torch.Tensor, stream=None):
-    """Per-(batch, head) window offsets [B * heads, nTiles, 3] (int32 CUDA) as per-head
-    key-tile lists: returns (row_ptr [B * heads, nTiles + 1], kv_list) for forward_list /
-    backward_list."""
-    lib = load_library()
-    n, wt = plan_shape(problem)
-    BH = problem.B * problem.heads
-    if not offsets.is_cuda or offsets.dtype != torch.int32 or not offsets.is_contiguous() or \
-            offsets.numel() != BH * n * 3:
-        raise ValueError("offsets must be a contiguous int32 CUDA tensor [B * heads, nTiles, 3]")
-    row_ptr = torch.empty((BH, n + 1), dtype=torch.int32, device=offsets.device)
-    kv_list = torch.empty(BH * n * wt, dtype=torch.int32, device=offsets.device)
-    _check(lib.dsa_plan_heads(ctypes.byref(problem), _ptr(offsets), _ptr(row_ptr), _ptr(kv_list),
-                              ctypes.c_void_p(_stream(stream))), "dsa_plan_heads")
-    return row_ptr, kv_list
-
-
-# ---------------------------------------------------------------- around the sliding attention
-def _dtype_of(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
-        return DSA_BF16
-    if t.dtype == torch.float32:
-        return DSA_F32
-    raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-
-
 class _On:
     """Runs a call on a device and on ``stream`` (default: that device's current stream).  What the
     call allocates comes from that stream's memory: a block of another stream's (the current
@@ -606,6 +273,360 @@ class _On:
         if self.side is not None:
             t.record_stream(torch.cuda.current_stream(self.device))
         return t
+
+
+def plan_shape(problem: Problem):
+    lib = load_library()
+    n, wt = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib.dsa_plan_shape(ctypes.byref(problem), ctypes.byref(n), ctypes.byref(wt)), "dsa_plan_shape")
+    return n.value, wt.value
+
+
+def workspace_size(problem: Problem, backward: bool = False) -> int:
+    return int(load_library().dsa_workspace_size(ctypes.byref(problem), DSA_WS_BWD if backward else DSA_WS_FWD))
+
+
+def workspace(problem: Problem, device, backward: bool = False) -> torch.Tensor:
+    """A device workspace of the right size (torch's caching allocator returns 512-byte
+    aligned blocks)."""
+    return torch.empty(max(workspace_size(problem, backward), 256), dtype=torch.uint8, device=device)
+
+
+def plan(problem: Problem, offsets: torch.Tensor, inverse: bool = True, stream=None):
+    """Run the window planner.  Returns (starts, kv_tiles[, row_ptr, q_tiles]) on the device."""
+    lib = load_library()
+    n, wt = plan_shape(problem)
+    if not offsets.is_cuda or offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.numel() != 3 * n:
+        raise ValueError("offsets must be a contiguous int32 CUDA tensor [nTiles, 3]")
+    on = _On(offsets.device, stream)
+    starts = on.empty((n, 3), torch.int32)
+    kv = on.empty((n, wt), torch.int32)
+    row_ptr = on.empty((n + 1,), torch.int32) if inverse else None
+    q_tiles = on.empty((n * wt,), torch.int32) if inverse else None
+    with on:
+        _check(lib.dsa_plan(ctypes.byref(problem), _ptr(offsets), _ptr(starts), _ptr(kv), _ptr(row_ptr), _ptr(q_tiles),
+                            ctypes.c_void_p(on.ptr)), "dsa_plan")
+    return (starts, kv, row_ptr, q_tiles) if inverse else (starts, kv)
+
+
+def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, tile: Sequence[int],
+            window: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+            lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """3D-DSA forward.  Returns (out, lse)."""
+    lib = load_library()
+    p = _problem_of(q, tile, window, scale)
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    _need(offsets, "offsets", q, torch.int32)
+    on = _On(q.device, stream)
+    if out is None:
+        out = on.empty_like(q)
+    if lse is None:
+        lse = on.empty(q.shape[:5], torch.float32)
+    _need(out, "out", q, q.dtype)
+    _need(lse, "lse", q, torch.float32)
+    if ws is None:
+        ws = on.scratch(max(workspace_size(p), 256))
+    with on:
+        _check(lib.dsa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), _ptr(out), _ptr(lse), _ptr(ws),
+                           ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_fwd")
+    return out, lse
+
+
+def prefix_workspace_size(problem: Problem, L_text: int) -> int:
+    return int(load_library().dsa_prefix_workspace_size(ctypes.byref(problem), int(L_text)))
+
+
+def forward_prefix(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, q_text: torch.Tensor,
+                   k_text: torch.Tensor, v_text: torch.Tensor, tile: Sequence[int], window: Sequence[int],
+                   scale: Optional[float] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """3D-DSA with a text prefix: video queries over their windows and every text key, text
+    queries over every key.  q, k, v: [B, heads, T, H, W, 128]; q_text, k_text, v_text:
+    [B, heads, L_text, 128].  Returns (out, lse, out_text, lse_text)."""
+    lib = load_library()
+    p = _problem_of(q, tile, window, scale)
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    _need(offsets, "offsets", q, torch.int32)
+    if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
+        raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
+    for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q_text.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q_text shape {tuple(q_text.shape)}")
+    L_text = int(q_text.shape[2])
+    on = _On(q.device, stream)
+    out = on.empty_like(q)
+    lse = on.empty(q.shape[:5], torch.float32)
+    out_text = on.empty_like(q_text)
+    lse_text = on.empty(q_text.shape[:3], torch.float32)
+    if ws is None:
+        ws = on.scratch(max(prefix_workspace_size(p, L_text), 256))
+    with on:
+        _check(lib.dsa_fwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), L_text, _ptr(q_text),
+                                  _ptr(k_text), _ptr(v_text), _ptr(out), _ptr(lse), _ptr(out_text), _ptr(lse_text),
+                                  _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_fwd_prefix")
+    return out, lse, out_text, lse_text
+
+
+def selftest_wait(stream=None):
+    """Enqueue the failure-path self-test (a bounded wait that runs out after 2 s and records
+    DSA_ERR_TIMEOUT at site 99); read the result with device_status()."""
+    _check(load_library().dsa_selftest_wait(ctypes.c_void_p(_stream(stream))), "dsa_selftest_wait")
+
+
+def prefix_bwd_workspace_size(problem: Problem, L_text: int) -> int:
+    return int(load_library().dsa_bwd_prefix_workspace_size(ctypes.byref(problem), int(L_text)))
+
+
+def backward_prefix(q, k, v, out, lse, dout, offsets, q_text, k_text, v_text, out_text, lse_text, dout_text,
+                    tile: Sequence[int], window: Sequence[int], scale: Optional[float] = None,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """Backward of forward_prefix (gradients of sum(out * dout) + sum(out_text * dout_text)).
+    Returns (dq, dk, dv, dq_text, dk_text, dv_text)."""
+    lib = load_library()
+    p = _problem_of(q, tile, window, scale)
+    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    _need(lse, "lse", q, torch.float32)
+    _need(offsets, "offsets", q, torch.int32)
+    if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
+        raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
+    for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text"), (out_text, "out_text"),
+                    (dout_text, "dout_text")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q_text.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q_text shape {tuple(q_text.shape)}")
+    _need(lse_text, "lse_text", q, torch.float32)
+    L_text = int(q_text.shape[2])
+    on = _On(q.device, stream)
+    dq, dk, dv = on.empty_like(q), on.empty_like(q), on.empty_like(q)
+    dqt, dkt, dvt = on.empty_like(q_text), on.empty_like(q_text), on.empty_like(q_text)
+    if ws is None:
+        ws = on.scratch(max(prefix_bwd_workspace_size(p, L_text), 256))
+    with on:
+        _check(lib.dsa_bwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                  _ptr(offsets), L_text, _ptr(q_text), _ptr(k_text), _ptr(v_text), _ptr(out_text),
+                                  _ptr(lse_text), _ptr(dout_text), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dqt), _ptr(dkt),
+                                  _ptr(dvt), _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_bwd_prefix")
+    return dq, dk, dv, dqt, dkt, dvt
+
+
+def forward_host_bytes(problem: Problem) -> int:
+    return int(load_library().dsa_fwd_host_bytes(ctypes.byref(problem)))
+
+
+def forward_host(problem: Problem, q_host: torch.Tensor, k_host: torch.Tensor, v_host: torch.Tensor,
+                 offsets_host: torch.Tensor, out_host: torch.Tensor, lse_host: torch.Tensor, dev: torch.Tensor,
+                 stream=None):
+    """3D-DSA forward from pinned host tensors through the caller's device buffer ``dev``
+    (uint8, at least forward_host_bytes(problem) bytes); asynchronous on ``stream``."""
+    lib = load_library()
+    for t in (q_host, k_host, v_host, offsets_host, out_host, lse_host):
+        if t.is_cuda or not t.is_contiguous():
+            raise ValueError("host tensors must be contiguous CPU tensors")
+    _check(lib.dsa_fwd_host(ctypes.byref(problem), _ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(offsets_host),
+                            _ptr(out_host), _ptr(lse_host), _ptr(dev), dev.numel(), ctypes.c_void_p(_stream(stream))),
+           "dsa_fwd_host")
+
+
+def backward(q, k, v, out, lse, dout, offsets, tile, window, scale=None, dq=None, dk=None, dv=None, ws=None,
+             stream=None):
+    """3D-DSA backward of sum(out * dout).  Returns (dq, dk, dv)."""
+    lib = load_library()
+    p = _problem_of(q, tile, window, scale)
+    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    _need(lse, "lse", q, torch.float32)
+    _need(offsets, "offsets", q, torch.int32)
+    on = _On(q.device, stream)
+    dq = on.empty_like(q) if dq is None else dq
+    dk = on.empty_like(q) if dk is None else dk
+    dv = on.empty_like(q) if dv is None else dv
+    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        _need(t, name, q, q.dtype)
+    if ws is None:
+        ws = on.scratch(max(workspace_size(p, backward=True), 256))
+    with on:
+        _check(lib.dsa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(offsets),
+                           _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)),
+               "dsa_bwd")
+    return dq, dk, dv
+
+
+def _list_args(q: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor, n_tiles: int):
+    """-> (list pointer, nnz, per_head): row_ptr [nTiles + 1] is one list for every head,
+    [B * heads, nTiles + 1] one list per (batch, head)."""
+    _need(row_ptr, "row_ptr", q, torch.int32)
+    BH = q.shape[0] * q.shape[1]
+    if row_ptr.numel() == n_tiles + 1 and row_ptr.dim() == 1:
+        per_head = 0
+    elif tuple(row_ptr.shape) == (BH, n_tiles + 1):
+        per_head = 1
+    else:
+        raise ValueError(f"row_ptr must be [nTiles + 1] or [B * heads, nTiles + 1], got {tuple(row_ptr.shape)}")
+    if kv_list is not None and kv_list.numel() > 0:
+        _need(kv_list, "kv_list", q, torch.int32)
+        return _ptr(kv_list), int(kv_list.numel()), per_head
+    return None, 0, per_head
+
+
+def forward_list(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor,
+                 tile: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                 lse: Optional[torch.Tensor] = None, stream=None):
+    """Block-sparse forward over key-tile lists: query tile i attends to the key tiles
+    kv_list[row_ptr[i]:row_ptr[i+1]] (int32 CUDA tensors; tiles in raster order of the tile
+    grid); row_ptr [nTiles + 1] is one list for every head, [B * heads, nTiles + 1] one per
+    (batch, head) with absolute positions in kv_list.  Returns (out, lse); an empty row
+    gives out = 0 and lse = -inf."""
+    lib = load_library()
+    p = _problem_of(q, tile, (1, 1, 1), scale)
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    n_tiles, _ = plan_shape(p)
+    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
+    on = _On(q.device, stream)
+    if out is None:
+        out = on.empty_like(q)
+    if lse is None:
+        lse = on.empty(q.shape[:5], torch.float32)
+    _need(out, "out", q, q.dtype)
+    _need(lse, "lse", q, torch.float32)
+    with on:
+        _check(lib.dsa_fwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), lst, nnz, per_head, _ptr(out),
+                                _ptr(lse), ctypes.c_void_p(on.ptr)), "dsa_fwd_list")
+    return out, lse
+
+
+def backward_list(q, k, v, out, lse, dout, row_ptr, kv_list, tile, scale=None, dq=None, dk=None, dv=None, ws=None,
+                  stream=None):
+    """Backward of sum(out * dout) for forward_list.  Returns (dq, dk, dv)."""
+    lib = load_library()
+    p = _problem_of(q, tile, (1, 1, 1), scale)
+    for t, name in ((k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
+        _need(t, name, q, q.dtype)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
+    _need(q, "q", q)
+    _need(lse, "lse", q, torch.float32)
+    n_tiles, _ = plan_shape(p)
+    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
+    on = _On(q.device, stream)
+    dq = on.empty_like(q) if dq is None else dq
+    dk = on.empty_like(q) if dk is None else dk
+    dv = on.empty_like(q) if dv is None else dv
+    for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        _need(t, name, q, q.dtype)
+    if ws is None:
+        size = int(lib.dsa_list_workspace_size(ctypes.byref(p), nnz, per_head, DSA_WS_BWD))
+        ws = on.scratch(max(size, 256))
+    with on:
+        _check(lib.dsa_bwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                _ptr(row_ptr), lst, nnz, per_head, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+                                ctypes.c_void_p(on.ptr)), "dsa_bwd_list")
+    return dq, dk, dv
+
+
+def block_map(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, row_ptr: torch.Tensor, kv_list: torch.Tensor,
+              tile: Sequence[int], scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None):
+    """Block attention mass [B * heads, nTiles, nTiles] (fp32): mean attention probability
+    of each query tile's tokens on each key tile, against the LSE forward_list wrote for
+    the same lists."""
+    lib = load_library()
+    p = _problem_of(q, tile, (1, 1, 1), scale)
+    _need(q, "q", q)
+    _need(k, "k", q, q.dtype)
+    _need(lse, "lse", q, torch.float32)
+    n_tiles, _ = plan_shape(p)
+    lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
+    BH = q.shape[0] * q.shape[1]
+    on = _On(q.device, stream)
+    if out is None:
+        out = on.empty((BH, n_tiles, n_tiles), torch.float32)
+    _need(out, "out", q, torch.float32)
+    with on:
+        _check(lib.dsa_block_map(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_ptr), lst, nnz, per_head,
+                                 _ptr(out), ctypes.c_void_p(on.ptr)), "dsa_block_map")
+    return out
+
+
+def lstsq_factor(M: torch.Tensor, lam: float, stream=None) -> torch.Tensor:
+    """Cholesky factor (fp64 [p, p], lower) of M^T M + lam I for a design matrix M (fp32
+    CUDA [m, p], p <= 32), to be reused by lstsq_solve across heads and steps."""
+    lib = load_library()
+    if not M.is_cuda or M.dtype != torch.float32 or not M.is_contiguous() or M.dim() != 2:
+        raise ValueError("M must be a contiguous fp32 CUDA tensor [m, p]")
+    m, p = M.shape
+    on = _On(M.device, stream)
+    L = on.empty((p, p), torch.float64)
+    with on:
+        _check(lib.dsa_lstsq_factor(m, p, _ptr(M), float(lam), _ptr(L), ctypes.c_void_p(on.ptr)),
+               "dsa_lstsq_factor")
+    return L
+
+
+def lstsq_solve(M: torch.Tensor, L: torch.Tensor, S: torch.Tensor, X: Optional[torch.Tensor] = None, ws=None,
+                stream=None) -> torch.Tensor:
+    """X [batch, p] (fp32) with (M^T M + lam I) x_b = M^T s_b for every row s_b of S
+    [batch, m] (fp32 CUDA), L from lstsq_factor."""
+    lib = load_library()
+    m, p = M.shape
+    if not S.is_cuda or S.dtype != torch.float32 or not S.is_contiguous() or S.dim() != 2 or S.shape[1] != m:
+        raise ValueError("S must be a contiguous fp32 CUDA tensor [batch, m]")
+    batch = S.shape[0]
+    on = _On(S.device, stream)
+    if X is None:
+        X = on.empty((batch, p), torch.float32)
+    n_ws = int(lib.dsa_lstsq_workspace_size(m, p, batch))
+    if ws is None and n_ws > 0:
+        ws = on.scratch(n_ws)
+    with on:
+        _check(lib.dsa_lstsq_solve(m, p, batch, _ptr(M), _ptr(L), _ptr(S), _ptr(X), _ptr(ws),
+                                   0 if ws is None else ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_lstsq_solve")
+    return X
+
+
+def plan_heads(problem: Problem, offsets: torch.Tensor, stream=None):
+    """Per-(batch, head) window offsets [B * heads, nTiles, 3] (int32 CUDA) as per-head
+    key-tile lists: returns (row_ptr [B * heads, nTiles + 1], kv_list) for forward_list /
+    backward_list."""
+    lib = load_library()
+    n, wt = plan_shape(problem)
+    BH = problem.B * problem.heads
+    if not offsets.is_cuda or offsets.dtype != torch.int32 or not offsets.is_contiguous() or \
+            offsets.numel() != BH * n * 3:
+        raise ValueError("offsets must be a contiguous int32 CUDA tensor [B * heads, nTiles, 3]")
+    on = _On(offsets.device, stream)
+    row_ptr = on.empty((BH, n + 1), torch.int32)
+    kv_list = on.empty((BH * n * wt,), torch.int32)
+    with on:
+        _check(lib.dsa_plan_heads(ctypes.byref(problem), _ptr(offsets), _ptr(row_ptr), _ptr(kv_list),
+                                  ctypes.c_void_p(on.ptr)), "dsa_plan_heads")
+    return row_ptr, kv_list
+
+
+# ---------------------------------------------------------------- around the sliding attention
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return DSA_BF16
+    if t.dtype == torch.float32:
+        return DSA_F32
+    raise ValueError(f"{name}: unsupported dtype {t.dtype}")
 
 
 def _addr(t: Optional[torch.Tensor]):
