@@ -426,12 +426,14 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           uint32_t s[32];
-          tmem_ld32_wait(tmem + kColS + 64 * half + 32 * h + lane_off, s);
+          const bool any = 64 * half + 32 * h < nq;  // of the rows there are
+          if (any) tmem_ld32_wait(tmem + kColS + 64 * half + 32 * h + lane_off, s);
           if (half == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_read);
           }
+          if (!any) continue;
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             const float4 l4 = nl[16 * half + 8 * h + g];
@@ -454,34 +456,36 @@ __global__ void __launch_bounds__(crosskv::kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           const uint32_t tD = tmem + kColDP + 64 * half + 32 * h + lane_off;
           uint32_t d[32], pk[16], ds[16];
-          tmem_ld32_wait(tD, d);
+          const int left = nq - 64 * half - 32 * h;  // rows there are
+          if (left > 0) {
+            tmem_ld32_wait(tD, d);
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            const float4 d4 = nl[32 + 16 * half + 8 * h + g];
-            const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
+            for (int g = 0; g < 8; ++g) {
+              const float4 d4 = nl[32 + 16 * half + 8 * h + g];
+              const float dv[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const int i = 4 * g + e;
-              const float p0 = pf[32 * half + i], p1 = pf[32 * half + i + 1];
-              float a0, a1, d0, d1;
-              fadd2(a0, a1, __uint_as_float(d[i]), __uint_as_float(d[i + 1]), dv[e], dv[e + 1]);
-              ffma2(d0, d1, a0, a1, p0, p1, 0.f, 0.f);
-              pk[i / 2] = pack_bf16x2(p0, p1);
-              ds[i / 2] = pack_bf16x2(d0, d1);
+              for (int e = 0; e < 4; e += 2) {
+                const int i = 4 * g + e;
+                const float p0 = pf[32 * half + i], p1 = pf[32 * half + i + 1];
+                float a0, a1, d0, d1;
+                fadd2(a0, a1, __uint_as_float(d[i]), __uint_as_float(d[i + 1]), dv[e], dv[e + 1]);
+                ffma2(d0, d1, a0, a1, p0, p1, 0.f, 0.f);
+                pk[i / 2] = pack_bf16x2(p0, p1);
+                ds[i / 2] = pack_bf16x2(d0, d1);
+              }
+            }
+            if (left < 32) {  // a missing row's P and dP may be anything: both are zero
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t keep = 2 * e + 1 < left ? 0xffffffffu : 2 * e < left ? 0xffffu : 0u;
+                pk[e] &= keep;
+                ds[e] &= keep;
+              }
             }
           }
-          if (tail && !k_ok) {  // a padding key's P and dP may be anything: both are zero
+          if (left <= 0 || (tail && !k_ok)) {  // and a padding key's
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = ds[e] = 0u;
-          }
-          if (nq < 128) {  // and a missing row's
-            const int left = nq - 64 * half - 32 * h;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const uint32_t keep = 2 * e + 1 < left ? 0xffffffffu : 2 * e < left ? 0xffffu : 0u;
-              pk[e] &= keep;
-              ds[e] &= keep;
-            }
           }
           __syncwarp();
           tmem_st16(tD, pk);  // over this thread's own dP columns
