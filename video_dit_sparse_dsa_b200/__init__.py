@@ -256,10 +256,12 @@ class _On:
         return self._make(torch.empty, n_bytes, dtype=torch.uint8, device=self.device) if n_bytes else None
 
     def empty(self, shape, dtype: torch.dtype) -> torch.Tensor:
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
         return self._result(torch.empty, shape, dtype=dtype, device=self.device)
 
     def empty_like(self, t: torch.Tensor) -> torch.Tensor:
-        return self._result(torch.empty_like, t)
+        return torch.empty_like(t) if self.side is None else self._result(torch.empty_like, t)
 
     def _make(self, f, *args, **kw) -> torch.Tensor:
         if self.side is None:
@@ -268,10 +270,9 @@ class _On:
             return f(*args, **kw)
 
     def _result(self, f, *args, **kw) -> torch.Tensor:
-        """A tensor that the caller gets, and may use and drop on its own current stream."""
+        """On another stream: a tensor that the caller gets, and may use and drop on its current one."""
         t = self._make(f, *args, **kw)
-        if self.side is not None:
-            t.record_stream(torch.cuda.current_stream(self.device))
+        t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
 
@@ -650,10 +651,11 @@ def _ws(ws: Optional[torch.Tensor], n_bytes: int, on: _On, ref: torch.Tensor):
     return ws, ws.numel() * ws.element_size()
 
 
-def _fit(*sizes: int):
-    """Sizes that the C structures' 32 bits hold (ctypes would keep the low bits of larger ones)."""
-    if max(sizes) > 2 ** 31 - 1:
-        raise DsaError(2, f"a size of {max(sizes)}")
+def _fit(sizes: int):
+    """Sizes (their bits in one number, which costs a call least) that the C structures' 32 bits hold:
+    ctypes would keep the low bits of larger ones."""
+    if sizes > 2 ** 31 - 1:
+        raise DsaError(2, "a size of 2^31 or more")
 
 
 def _rows_view(t: torch.Tensor, name: str) -> View:
@@ -669,7 +671,7 @@ def _cross(q, k, v, kv_len, scale) -> Cross:
         raise ValueError("q must be [B, heads, Lq, d], k and v [B, kv_heads, Lk, d]")
     B, heads, Lq, d = q.shape
     _, kv_heads, Lk, _ = k.shape
-    _fit(B, heads, kv_heads, Lq, Lk, d)
+    _fit(B | heads | kv_heads | Lq | Lk | d)
     _like(k, "k", q, (B, kv_heads, Lk, d), q.dtype)
     _like(v, "v", q, k.shape, q.dtype)
     if kv_len is not None:
@@ -749,7 +751,7 @@ def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0,
     axes = _axes(axes)
     if len(grid) != 3 or len(start) != 3 or len(step) != 3:
         raise ValueError("grid, start and step must have three entries")
-    _fit(*(int(g) for g in grid), *axes)
+    _fit(max(*(int(g) for g in grid), *axes))
     n = sum(int(g) * (a // 2) for g, a in zip(grid, axes))
     device = torch.device(device)
     if device.type == "cuda" and device.index is None:
@@ -788,7 +790,7 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], table: torch.Tensor, axes: 
         raise ValueError("q must be [B, heads, T, H, W, d]")
     axes = _axes(axes)
     B, heads, T, H, W, d = q.shape
-    _fit(*q.shape, *axes)
+    _fit(B | heads | T | H | W | d)
     p = Rope(B, heads, d, T, H, W, tuple(axes), 1 if interleaved else 0, 1 if inverse else 0, _dtype_of(q, "q"))
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
