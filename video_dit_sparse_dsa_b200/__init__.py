@@ -212,13 +212,20 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _need(t: torch.Tensor, name: str, like: torch.Tensor, dtype=None):
+def _need(t: torch.Tensor, name: str, like: torch.Tensor, dtype=None, numel: Optional[int] = None):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, q on {like.device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+
+
+def _need_workspace(ws: torch.Tensor, like: torch.Tensor):
+    if not ws.is_contiguous() or ws.device != like.device or ws.element_size() != 1:
+        raise ValueError(f"workspace must be a contiguous tensor of bytes on {like.device}")
 
 
 class _On:
@@ -321,16 +328,17 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Te
         if t.shape != q.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
     _need(q, "q", q)
-    _need(offsets, "offsets", q, torch.int32)
+    _need(offsets, "offsets", q, torch.int32, 3 * plan_shape(p)[0])
     on = _On(q.device, stream)
     if out is None:
         out = on.empty_like(q)
     if lse is None:
         lse = on.empty(q.shape[:5], torch.float32)
-    _need(out, "out", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
+    _need(out, "out", q, q.dtype, q.numel())
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
     if ws is None:
         ws = on.scratch(max(workspace_size(p), 256))
+    _need_workspace(ws, q)
     with on:
         _check(lib.dsa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), _ptr(out), _ptr(lse), _ptr(ws),
                            ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_fwd")
@@ -354,7 +362,7 @@ def forward_prefix(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: t
         if t.shape != q.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
     _need(q, "q", q)
-    _need(offsets, "offsets", q, torch.int32)
+    _need(offsets, "offsets", q, torch.int32, 3 * plan_shape(p)[0])
     if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
         raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
     for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text")):
@@ -369,6 +377,7 @@ def forward_prefix(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: t
     lse_text = on.empty(q_text.shape[:3], torch.float32)
     if ws is None:
         ws = on.scratch(max(prefix_workspace_size(p, L_text), 256))
+    _need_workspace(ws, q)
     with on:
         _check(lib.dsa_fwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), L_text, _ptr(q_text),
                                   _ptr(k_text), _ptr(v_text), _ptr(out), _ptr(lse), _ptr(out_text), _ptr(lse_text),
@@ -398,8 +407,8 @@ def backward_prefix(q, k, v, out, lse, dout, offsets, q_text, k_text, v_text, ou
         if t.shape != q.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
     _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
-    _need(offsets, "offsets", q, torch.int32)
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
+    _need(offsets, "offsets", q, torch.int32, 3 * plan_shape(p)[0])
     if q_text.dim() != 4 or tuple(q_text.shape[:2]) != tuple(q.shape[:2]) or q_text.shape[3] != q.shape[5]:
         raise ValueError(f"q_text shape {tuple(q_text.shape)} does not match q {tuple(q.shape)}")
     for t, name in ((q_text, "q_text"), (k_text, "k_text"), (v_text, "v_text"), (out_text, "out_text"),
@@ -407,13 +416,14 @@ def backward_prefix(q, k, v, out, lse, dout, offsets, q_text, k_text, v_text, ou
         _need(t, name, q, q.dtype)
         if t.shape != q_text.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q_text shape {tuple(q_text.shape)}")
-    _need(lse_text, "lse_text", q, torch.float32)
+    _need(lse_text, "lse_text", q, torch.float32, q_text.shape[:3].numel())
     L_text = int(q_text.shape[2])
     on = _On(q.device, stream)
     dq, dk, dv = on.empty_like(q), on.empty_like(q), on.empty_like(q)
     dqt, dkt, dvt = on.empty_like(q_text), on.empty_like(q_text), on.empty_like(q_text)
     if ws is None:
         ws = on.scratch(max(prefix_bwd_workspace_size(p, L_text), 256))
+    _need_workspace(ws, q)
     with on:
         _check(lib.dsa_bwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                   _ptr(offsets), L_text, _ptr(q_text), _ptr(k_text), _ptr(v_text), _ptr(out_text),
@@ -435,6 +445,15 @@ def forward_host(problem: Problem, q_host: torch.Tensor, k_host: torch.Tensor, v
     for t in (q_host, k_host, v_host, offsets_host, out_host, lse_host):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError("host tensors must be contiguous CPU tensors")
+    rows = problem.B * problem.heads * problem.T * problem.H * problem.W
+    dtype = torch.bfloat16 if problem.dtype == DSA_BF16 else torch.float32
+    for t, name, n, dt in ((q_host, "q_host", rows * problem.d, dtype), (k_host, "k_host", rows * problem.d, dtype),
+                           (v_host, "v_host", rows * problem.d, dtype), (out_host, "out_host", rows * problem.d, dtype),
+                           (lse_host, "lse_host", rows, torch.float32),
+                           (offsets_host, "offsets_host", 3 * plan_shape(problem)[0], torch.int32)):
+        if t.numel() != n or t.dtype != dt:
+            raise ValueError(f"{name} must be {n} elements of {dt}")
+    _need_workspace(dev, dev)
     _check(lib.dsa_fwd_host(ctypes.byref(problem), _ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(offsets_host),
                             _ptr(out_host), _ptr(lse_host), _ptr(dev), dev.numel(), ctypes.c_void_p(_stream(stream))),
            "dsa_fwd_host")
@@ -450,16 +469,17 @@ def backward(q, k, v, out, lse, dout, offsets, tile, window, scale=None, dq=None
         if t.shape != q.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
     _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
-    _need(offsets, "offsets", q, torch.int32)
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
+    _need(offsets, "offsets", q, torch.int32, 3 * plan_shape(p)[0])
     on = _On(q.device, stream)
     dq = on.empty_like(q) if dq is None else dq
     dk = on.empty_like(q) if dk is None else dk
     dv = on.empty_like(q) if dv is None else dv
     for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, name, q, q.dtype)
+        _need(t, name, q, q.dtype, q.numel())
     if ws is None:
         ws = on.scratch(max(workspace_size(p, backward=True), 256))
+    _need_workspace(ws, q)
     with on:
         _check(lib.dsa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(offsets),
                            _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)),
@@ -506,8 +526,8 @@ def forward_list(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_ptr: tor
         out = on.empty_like(q)
     if lse is None:
         lse = on.empty(q.shape[:5], torch.float32)
-    _need(out, "out", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
+    _need(out, "out", q, q.dtype, q.numel())
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
     with on:
         _check(lib.dsa_fwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(row_ptr), lst, nnz, per_head, _ptr(out),
                                 _ptr(lse), ctypes.c_void_p(on.ptr)), "dsa_fwd_list")
@@ -524,7 +544,7 @@ def backward_list(q, k, v, out, lse, dout, row_ptr, kv_list, tile, scale=None, d
         if t.shape != q.shape:
             raise ValueError(f"{name} shape {tuple(t.shape)} != q shape {tuple(q.shape)}")
     _need(q, "q", q)
-    _need(lse, "lse", q, torch.float32)
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
     n_tiles, _ = plan_shape(p)
     lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
     on = _On(q.device, stream)
@@ -532,10 +552,11 @@ def backward_list(q, k, v, out, lse, dout, row_ptr, kv_list, tile, scale=None, d
     dk = on.empty_like(q) if dk is None else dk
     dv = on.empty_like(q) if dv is None else dv
     for t, name in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, name, q, q.dtype)
+        _need(t, name, q, q.dtype, q.numel())
     if ws is None:
         size = int(lib.dsa_list_workspace_size(ctypes.byref(p), nnz, per_head, DSA_WS_BWD))
         ws = on.scratch(max(size, 256))
+    _need_workspace(ws, q)
     with on:
         _check(lib.dsa_bwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                 _ptr(row_ptr), lst, nnz, per_head, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
@@ -551,15 +572,15 @@ def block_map(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, row_ptr: torc
     lib = load_library()
     p = _problem_of(q, tile, (1, 1, 1), scale)
     _need(q, "q", q)
-    _need(k, "k", q, q.dtype)
-    _need(lse, "lse", q, torch.float32)
+    _need(k, "k", q, q.dtype, q.numel())
+    _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
     n_tiles, _ = plan_shape(p)
     lst, nnz, per_head = _list_args(q, row_ptr, kv_list, n_tiles)
     BH = q.shape[0] * q.shape[1]
     on = _On(q.device, stream)
     if out is None:
         out = on.empty((BH, n_tiles, n_tiles), torch.float32)
-    _need(out, "out", q, torch.float32)
+    _need(out, "out", q, torch.float32, BH * n_tiles * n_tiles)
     with on:
         _check(lib.dsa_block_map(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(lse), _ptr(row_ptr), lst, nnz, per_head,
                                  _ptr(out), ctypes.c_void_p(on.ptr)), "dsa_block_map")
@@ -590,9 +611,12 @@ def lstsq_solve(M: torch.Tensor, L: torch.Tensor, S: torch.Tensor, X: Optional[t
     if not S.is_cuda or S.dtype != torch.float32 or not S.is_contiguous() or S.dim() != 2 or S.shape[1] != m:
         raise ValueError("S must be a contiguous fp32 CUDA tensor [batch, m]")
     batch = S.shape[0]
+    _need(M, "M", S, torch.float32)
+    _need(L, "L", S, torch.float64, p * p)
     on = _On(S.device, stream)
     if X is None:
         X = on.empty((batch, p), torch.float32)
+    _need(X, "X", S, torch.float32, batch * p)
     n_ws = int(lib.dsa_lstsq_workspace_size(m, p, batch))
     if ws is None and n_ws > 0:
         ws = on.scratch(n_ws)
