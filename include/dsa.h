@@ -15,6 +15,8 @@
  *     i.e. it is centred on i + o and then moved to lie fully inside the tile grid.
  *   - Every query token n of tile i attends to exactly the tokens K(i) of the tiles in that
  *     window:  O_n = sum_m softmax_m(scale * <q_n, k_m>) v_m,  LSE_n = ln sum_m exp(scale * <q_n, k_m>).
+ *     In the forward, scores that are not finite give what the formulas give: -inf the weight 0 (all
+ *     of a row: O = NaN, LSE = -inf), +inf O = NaN and LSE = +inf, NaN a row of NaN.
  *
  * Layouts (all contiguous, row-major):
  *   q, k, v, out, dout, dq, dk, dv : [B, heads, T, H, W, d]  (token n = (t*H + h)*W + w)

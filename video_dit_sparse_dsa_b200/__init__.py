@@ -18,11 +18,12 @@ tensors (bf16 with d = 128, or fp32 with d in {64, 128} for the forward); lse is
 Around it in a transformer block: ``forward_cross`` / ``backward_cross`` (cross attention to an
 encoder's states), ``rope_table`` / ``rope`` (rotary positions over the token grid) and
 ``rms_norm`` / ``rms_norm_fp8`` / ``rms_norm_backward`` (root-mean-square norm with the
-residual's addition).  These take strided tensors (views of a projection), run on the device
-of their first argument whichever device is current, and on ``stream`` (default: that device's
-current stream).  A call on another stream than the current one is ordered after what is on that
-stream, as its kernels would be: the caller orders it after the work that makes its inputs, and
-what reads its results after it.
+residual's addition).  These take strided tensors (views of a projection).
+
+Calls run on the device of their tensors, whichever device is current, and on ``stream`` (default:
+that device's current stream).  A call on another stream than the current one is ordered after
+what is on that stream, as its kernels would be, and allocates what it needs there: the caller
+orders it after the work that makes its inputs, and what reads its results after it.
 """
 from __future__ import annotations
 

@@ -454,8 +454,9 @@ dsa_status_t dsa_fwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     if (c.pair) {
       fp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
       fp.n_units = p->B * p->kv_heads * fp.tiles;
-      // measured on a 512 + 203-key pair: units of four and of two chunks take times of 9 : 5.7
-      // (with a cost of 4 the CTAs of the short entry ran 212 us, those of the long one 186)
+      // measured on a 512 + 203-key pair alone: units of four and of two chunks take times of 9 : 5.7
+      // (with a cost of 4 the CTAs of the short entry ran 212 us, those of the long one 186); a line
+      // through those two lengths, other pairs of lengths are not measured
       fp.unit_cost = 12;
       CUtensorMap to;
       int mo[3];
@@ -617,7 +618,9 @@ dsa_status_t dsa_bwd_cross(const dsa_cross_t* p, const dsa_view_t* q, const dsa_
     dp.tiles = static_cast<int>(c.group * ((static_cast<int64_t>(p->Lq) + 255) / 256));
     dp.n_units = p->B * p->kv_heads * dp.tiles;
     // measured on the same pair of lengths: units of four and of two chunks take times of 14.2 : 7.0
-    // (with a cost of 4 the CTAs of the long entry ran 510 thousand clocks, those of the short one 441)
+    // (with a cost of 4 the CTAs of the long entry ran 510 thousand clocks, those of the short one
+    // 441).  It is not a unit's own start and end alone, which take longer: the two chunks stay in
+    // the K and V rings from unit to unit, the four do not
     dp.unit_cost = 1;
     return launch_pairs<dsa::cross_dq_kernel<true>>(dsa::crossdq::kSmemBytes, dsa::crossdq::kThreads,
                                                     dsa::bdq::kRegsAtLaunch, dp.n_units, s, tq, tdo, tk64, tk, tv64, tdq, dp);

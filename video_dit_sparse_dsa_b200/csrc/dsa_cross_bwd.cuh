@@ -18,7 +18,7 @@ struct CrossPrepParams {
 };
 
 // D.  16 threads per row, 8 channels each, four rows a thread, all loads first (24 heads x
-// 35840 rows, 440 MB: 84 us, 5.2 TB/s; one row at a time took 96 us).
+// 35840 rows, 440 MB: 88 us with L2 flushed, 5.0 TB/s; one row at a time took 14% more).
 __global__ void __launch_bounds__(256) cross_preprocess(CrossPrepParams p) {
   constexpr int kRows = 4;
   const int part = threadIdx.x % 16;

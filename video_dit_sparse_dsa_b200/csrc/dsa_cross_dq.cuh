@@ -4,8 +4,8 @@
 //
 // Per 128 keys the tensor cores form S = Q K^T and dP = dO V^T again, the elementwise warps dS, and
 // dQ += dS K accumulates in TMEM: 1536 clocks of products, 1024 of exponentials (all on the MUFU
-// unit: with a quarter of them on the FMA pipe the whole backward took 722 in place of 714 us for the
-// 480p pair below, and a score of -inf got a small weight where 0 is meant).  A window holds
+// unit: with a quarter of them on the FMA pipe the whole backward took 656 in place of 650 us for the
+// pair of lengths below, and a score of -inf got a small weight where 0 is meant).  A window holds
 // thousands of keys, a prompt one to four steps' worth, so what counts here is that nothing drains
 // between units:
 //   * three regions of TMEM columns rotate: S of step G + 1 goes where dS of step G - 1 was, dP of
@@ -24,8 +24,8 @@
 // with a ring of its own and released by its own product.  (24 heads x 35840 rows over 512 and 203
 // keys, whole backward: 650 us, and 695 with this pass on single CTAs.)
 //
-// What bounds it: 302 us there, 3300 clocks per step.  Latency: the tensor pipe is active 41 to 52%
-// of the time, L2 at 14% of its rate; the MMA warp goes through seven waits of 200 clocks a step,
+// What bounds it: 289 us there, 3200 clocks per step.  Latency: the tensor pipe is active 40% of the
+// time, L2 at 18% of its rate; the MMA warp goes through seven waits of 200 clocks a step,
 // which follow one another, a unit's start and its dQ take 3000 to 3500 clocks of the elementwise
 // warps, and of the stalls of a warp a fifth are for instructions (long unrolled code, run once a
 // step).  Ring depth counts: two entries in place of three cost 40%.  Measured and not kept: rings of two entries with two Q tiles (430 us); one wait per step for all loads, behind

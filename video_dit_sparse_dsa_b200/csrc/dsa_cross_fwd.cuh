@@ -19,8 +19,8 @@
 // keys as N, half from each CTA's shared memory, and P V the 128 channels as N, half from each.
 // So a CTA holds half of K and V: up to 512 keys of both fit beside three Q tiles, and stay for
 // all consecutive units of their kv head, where a single CTA re-reads V for every unit and has no
-// room to load Q ahead (24 heads x 115200 rows over 512 keys: 694 us, and 953 as single CTAs).  Few rows over many keys (a
-// single token over every state) run on single CTAs, with up to 128 / Lq heads of a kv head packed
+// room to load Q ahead (24 heads x 115200 rows over 512 keys: 694 us when built, and 953 as single
+// CTAs).  Few rows over many keys (a single token over every state) run on single CTAs, with up to 128 / Lq heads of a kv head packed
 // into a unit, so that K and V are read once for them, and with the keys cut into parts, one unit
 // each, whose fp32 partial outputs cross_merge_kernel joins by their LSEs.
 //
@@ -44,11 +44,12 @@
 // Pair barriers: loads of K and Q count on the even CTA's barriers, products commit to both
 // CTAs', and the softmax warps and V hand-overs of both arrive on the even CTA's.
 //
-// Measured: 24 heads x 115200 rows over 512 keys 694 us alone (1.04 PFLOP/s, 63% of the tensor
-// peak; 812 us in a loop, at the power cap); 12 heads of 2 x 35840 rows over 512 and 203 keys 188 us
-// (0.84 PFLOP/s, 51%); 24 x 16384 rows over 77 keys 62 us (3.3 TB/s); one row of 24 heads, 6 of keys,
-// over 115201 and 70007 keys 112 us (5.1 TB/s).  With one or two steps per tile it is bound by the softmax of a step (2850 clocks per
-// 256 keys, 2048 of them products) and by the 1200 to 1500 that a unit's read-out adds.
+// Measured in a loop of calls (one call on a cool GPU with L2 flushed in brackets): 24 heads x 115200
+// rows over 512 keys 804 us, at the power cap, 901 TFLOP/s (686); 12 heads of 2 x 35840 rows over 512
+// and 203 keys 214 us, 735 TFLOP/s (188); 24 x 16384 rows over 77 keys 63 us, 3.3 TB/s (64); one row of
+// 24 heads, 6 of keys, over 115201 and 70007 keys 125 us, 4.5 TB/s (131).  With one or two steps per
+// tile it is bound by the softmax of a step (2850 clocks per 256 keys, 2048 of them products) and by
+// the 1200 to 1500 that a unit's read-out adds.
 //
 // TMEM (512 columns): as the window forward: regions R0 R1 R2 of 128 columns that scores and P
 // rotate through (even steps: S in R0 R1, P in R0; odd: S in R1 R2, P in R2), O in the fourth.

@@ -16,7 +16,7 @@
 // elementwise work is handed over in two halves of 64 queries:
 //   tensor pipe   dP(c)      S(c+1)       grads A(c)  grads B(c)   dP(c+1) ...
 //   elementwise   (exp of c) dS A, dS B(c)      exp of c+1 ...
-// 24 heads x 35840 rows over 512 and 203 keys: 267 us, 3700 clocks per chunk.  What bounds it is
+// 24 heads x 35840 rows over 512 and 203 keys: 257 us, 3600 clocks per chunk.  What bounds it is
 // that cycle: dP(c), dS (750 clocks), the four gradient products and dP(c + 1) follow one another,
 // with 1250 clocks of exponentials and some 200 per hand-over beside them; running a quarter or
 // three eighths of the exponentials on the FMA pipe changed nothing.  A second dP buffer would

@@ -15,9 +15,12 @@
 // vectors; vector i * tpr + t belongs to thread t of the row, so a warp's loads are contiguous and
 // a group of 128 channels is 16 consecutive lanes.  Rows whose address, length or stride is not a
 // multiple of 16 bytes go through the same kernel with element-wise loads (kAligned = false; about
-// a quarter of the rate, 1.6 TB/s).  71680 x 1536 bf16 with a residual: 134 us, a copy's rate (part of
-// it stays in L2 from call to call); backward, 35840 x 5120 with dh: 257 us, 5.7 TB/s (87%); 860160
-// x 128: 130 and 156 us.
+// a quarter of the rate: 40000 x 1537 bf16 with a residual 295 us, 1.7 TB/s, backward with dh 330).
+// Times of one call with L2 flushed, and the share of a copy's rate: bf16 with a residual, 71680 x
+// 1536: 133 us, 100%; to e4m3 150, 79%; 35840 x 5120 to e4m3: 244, 81%; 860160 x 128 without a
+// residual: 88, 77%; fp32 with a residual, 35840 x 1536: 135, 100%.  Backward, bf16 with dh, 35840 x
+// 5120: 256, 88%; 860160 x 128 without: 149, 68%; fp32 with dh, 35840 x 1536: 146, 92%; 17920 x 5120
+// (too wide for the ring, read twice): 235, 96%.
 #pragma once
 
 #include <cuda_bf16.h>
