@@ -1,5 +1,9 @@
 """The operators around the attention on another stream than the current one: what they allocate is
 never memory that work queued on the current stream still uses."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -8,7 +12,7 @@ import video_dit_sparse_dsa_b200 as dsa
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 BF = torch.bfloat16
-SLEEP = 100_000_000  # clocks, some 50 ms: the host queues everything else meanwhile
+SLEEP = 300_000_000  # clocks, some 150 ms: the host queues everything else meanwhile
 
 
 def rn(seed, *shape, dtype=BF):
@@ -139,3 +143,12 @@ def test_a_refused_stream_leaves_the_device():
     with pytest.raises((TypeError, ValueError)):
         dsa.rms_norm(x, stream="no stream")
     assert torch.cuda.current_device() == 0 and dsa.rms_norm(x)[0].shape == x.shape
+
+
+@pytest.mark.parametrize("device", ["cuda", "cuda:0"])
+def test_a_table_is_a_process_first_call(device):
+    code = ("import video_dit_sparse_dsa_b200 as dsa; "
+            f"t = dsa.rope_table((2, 3, 4), (4, 4, 4), device='{device}'); "
+            "assert t.shape == (18, 2) and float(t[0, 0]) == 1.0")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root, timeout=300)

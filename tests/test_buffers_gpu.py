@@ -37,7 +37,8 @@ def test_forward():
     refuses(f, out=SMALL())
     refuses(f, lse=LSE(1, 2, 4, 8, 8))
     refuses(f, ws=new(64, dtype=torch.uint8))
-    refuses(f, ws=new(1 << 16, dtype=torch.float32))
+    refuses(f, ws=new(16, dtype=torch.float32))
+    assert f(ws=new(1 << 16, dtype=torch.float32))[0].shape == q.shape
     refuses(f, ws=new(1 << 16, 2, dtype=torch.uint8)[:, 0])
     assert f()[0].shape == q.shape
 
@@ -93,3 +94,10 @@ def test_host(which):
     host += [new(dsa.forward_host_bytes(p), dtype=torch.uint8)]
     host[which] = host[which].flatten()[1:].clone() if which < 6 else host[which][:-256]
     refuses(dsa.forward_host, p, *host)
+
+
+def test_host_without_a_device_buffer():
+    p = dsa.make_problem(1, 2, 128, GRID, TILE, WINDOW)
+    x = new(1, 2, *GRID, 128, device="cpu")
+    refuses(dsa.forward_host, p, x, x, x, new(TILES, 3, dtype=torch.int32, device="cpu"), x.clone(),
+            new(1, 2, *GRID, dtype=torch.float32, device="cpu"), new(dsa.forward_host_bytes(p), dtype=torch.uint8, device="cpu"))

@@ -224,9 +224,11 @@ def _need(t: torch.Tensor, name: str, like: torch.Tensor, dtype=None, numel: Opt
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
 
 
-def _need_workspace(ws: torch.Tensor, like: torch.Tensor):
-    if not ws.is_contiguous() or ws.device != like.device or ws.element_size() != 1:
-        raise ValueError(f"workspace must be a contiguous tensor of bytes on {like.device}")
+def _need_workspace(ws: torch.Tensor, device: torch.device) -> int:
+    """The bytes of a workspace (whether they suffice, the library checks)."""
+    if not ws.is_contiguous() or ws.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return ws.numel() * ws.element_size()
 
 
 class _On:
@@ -339,10 +341,10 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Te
     _need(lse, "lse", q, torch.float32, q.shape[:5].numel())
     if ws is None:
         ws = on.scratch(max(workspace_size(p), 256))
-    _need_workspace(ws, q)
+    n_ws = _need_workspace(ws, q.device)
     with on:
         _check(lib.dsa_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), _ptr(out), _ptr(lse), _ptr(ws),
-                           ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_fwd")
+                           n_ws, ctypes.c_void_p(on.ptr)), "dsa_fwd")
     return out, lse
 
 
@@ -378,11 +380,11 @@ def forward_prefix(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: t
     lse_text = on.empty(q_text.shape[:3], torch.float32)
     if ws is None:
         ws = on.scratch(max(prefix_workspace_size(p, L_text), 256))
-    _need_workspace(ws, q)
+    n_ws = _need_workspace(ws, q.device)
     with on:
         _check(lib.dsa_fwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(offsets), L_text, _ptr(q_text),
                                   _ptr(k_text), _ptr(v_text), _ptr(out), _ptr(lse), _ptr(out_text), _ptr(lse_text),
-                                  _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_fwd_prefix")
+                                  _ptr(ws), n_ws, ctypes.c_void_p(on.ptr)), "dsa_fwd_prefix")
     return out, lse, out_text, lse_text
 
 
@@ -424,12 +426,12 @@ def backward_prefix(q, k, v, out, lse, dout, offsets, q_text, k_text, v_text, ou
     dqt, dkt, dvt = on.empty_like(q_text), on.empty_like(q_text), on.empty_like(q_text)
     if ws is None:
         ws = on.scratch(max(prefix_bwd_workspace_size(p, L_text), 256))
-    _need_workspace(ws, q)
+    n_ws = _need_workspace(ws, q.device)
     with on:
         _check(lib.dsa_bwd_prefix(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                   _ptr(offsets), L_text, _ptr(q_text), _ptr(k_text), _ptr(v_text), _ptr(out_text),
                                   _ptr(lse_text), _ptr(dout_text), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dqt), _ptr(dkt),
-                                  _ptr(dvt), _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)), "dsa_bwd_prefix")
+                                  _ptr(dvt), _ptr(ws), n_ws, ctypes.c_void_p(on.ptr)), "dsa_bwd_prefix")
     return dq, dk, dv, dqt, dkt, dvt
 
 
@@ -447,16 +449,17 @@ def forward_host(problem: Problem, q_host: torch.Tensor, k_host: torch.Tensor, v
         if t.is_cuda or not t.is_contiguous():
             raise ValueError("host tensors must be contiguous CPU tensors")
     rows = problem.B * problem.heads * problem.T * problem.H * problem.W
-    dtype = torch.bfloat16 if problem.dtype == DSA_BF16 else torch.float32
-    for t, name, n, dt in ((q_host, "q_host", rows * problem.d, dtype), (k_host, "k_host", rows * problem.d, dtype),
-                           (v_host, "v_host", rows * problem.d, dtype), (out_host, "out_host", rows * problem.d, dtype),
-                           (lse_host, "lse_host", rows, torch.float32),
-                           (offsets_host, "offsets_host", 3 * plan_shape(problem)[0], torch.int32)):
-        if t.numel() != n or t.dtype != dt:
-            raise ValueError(f"{name} must be {n} elements of {dt}")
-    _need_workspace(dev, dev)
+    row_bytes = problem.d * (2 if problem.dtype == DSA_BF16 else 4)
+    for t, name, n in ((q_host, "q_host", rows * row_bytes), (k_host, "k_host", rows * row_bytes),
+                       (v_host, "v_host", rows * row_bytes), (out_host, "out_host", rows * row_bytes),
+                       (lse_host, "lse_host", 4 * rows), (offsets_host, "offsets_host", 12 * plan_shape(problem)[0])):
+        if t.numel() * t.element_size() != n:
+            raise ValueError(f"{name} has {t.numel() * t.element_size()} bytes, expected {n}")
+    if not dev.is_cuda:
+        raise ValueError("dev must be a CUDA tensor")
+    n_dev = _need_workspace(dev, dev.device)
     _check(lib.dsa_fwd_host(ctypes.byref(problem), _ptr(q_host), _ptr(k_host), _ptr(v_host), _ptr(offsets_host),
-                            _ptr(out_host), _ptr(lse_host), _ptr(dev), dev.numel(), ctypes.c_void_p(_stream(stream))),
+                            _ptr(out_host), _ptr(lse_host), _ptr(dev), n_dev, ctypes.c_void_p(_stream(stream))),
            "dsa_fwd_host")
 
 
@@ -480,10 +483,10 @@ def backward(q, k, v, out, lse, dout, offsets, tile, window, scale=None, dq=None
         _need(t, name, q, q.dtype, q.numel())
     if ws is None:
         ws = on.scratch(max(workspace_size(p, backward=True), 256))
-    _need_workspace(ws, q)
+    n_ws = _need_workspace(ws, q.device)
     with on:
         _check(lib.dsa_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(offsets),
-                           _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(), ctypes.c_void_p(on.ptr)),
+                           _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n_ws, ctypes.c_void_p(on.ptr)),
                "dsa_bwd")
     return dq, dk, dv
 
@@ -557,10 +560,10 @@ def backward_list(q, k, v, out, lse, dout, row_ptr, kv_list, tile, scale=None, d
     if ws is None:
         size = int(lib.dsa_list_workspace_size(ctypes.byref(p), nnz, per_head, DSA_WS_BWD))
         ws = on.scratch(max(size, 256))
-    _need_workspace(ws, q)
+    n_ws = _need_workspace(ws, q.device)
     with on:
         _check(lib.dsa_bwd_list(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
-                                _ptr(row_ptr), lst, nnz, per_head, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+                                _ptr(row_ptr), lst, nnz, per_head, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), n_ws,
                                 ctypes.c_void_p(on.ptr)), "dsa_bwd_list")
     return dq, dk, dv
 
@@ -779,8 +782,9 @@ def rope_table(grid: Sequence[int], axes: Sequence[int], theta: float = 10000.0,
     _fit(max(*(int(g) for g in grid), *axes))
     n = sum(int(g) * (a // 2) for g, a in zip(grid, axes))
     device = torch.device(device)
-    if device.type == "cuda" and device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+    if device.type == "cuda":
+        current = torch.cuda.current_device()  # (this may be the process' first call to CUDA)
+        device = torch.device("cuda", current if device.index is None else device.index)
     with _On(device, stream) as on:
         table = on.empty((max(n, 0), 2), torch.float32)
         i3, d3 = ctypes.c_int32 * 3, ctypes.c_double * 3
